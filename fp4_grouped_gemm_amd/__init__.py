@@ -18,6 +18,8 @@ __all__ = [
     "quantize_blockwise", "moe_permute", "moe_permute_outputs", "moe_permute_workspace_bytes",
     "moe_permute_quantize_noalloc", "grouped_gemm_scaled", "grouped_gemm_silu_quantize", "pack_fp4_weights",
     "scaled_gemm", "moe_combine", "set_num_cus", "kernel_table", "kernel_compiled_lds",
+    "moe_route", "moe_route_backward", "moe_permute_rows", "moe_permute_rows_backward", "moe_unpermute_rows",
+    "moe_unpermute_rows_backward", "moe_gemv_fp4",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -26,6 +28,7 @@ _LIB_PATH = os.path.join(_HERE, "libfgg.so")
 FGG_F32, FGG_BF16, FGG_E4M3, FGG_E2M1X2, FGG_E8M0, FGG_E2M1X2_TILED = 0, 1, 2, 3, 4, 5
 FGG_ACT_NONE, FGG_ACT_SILU_MUL = 0, 1
 FGG_LAYOUT_CONTIGUOUS, FGG_LAYOUT_MASKED = 0, 1
+FGG_GATE_SOFTMAX, FGG_GATE_SIGMOID = 0, 1
 _STATUS = {0: "FGG_OK", 1: "FGG_ERR_INVALID_VALUE", 2: "FGG_ERR_UNSUPPORTED", 3: "FGG_ERR_HIP"}
 
 
@@ -75,7 +78,7 @@ def load_library():
     if not os.path.exists(_LIB_PATH):
         raise RuntimeError(f"{_LIB_PATH} is missing: build it with `python -m fp4_grouped_gemm_amd.build`")
     lib = ctypes.CDLL(_LIB_PATH)
-    P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    P, I32, I64, SZ, F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
     sig = {
         "fgg_status_string": ([I32], ctypes.c_char_p),
         "fgg_last_hip_error": ([], I32),
@@ -98,6 +101,14 @@ def load_library():
                                   P, I64, P], I32),
         "fgg_pack_fp4_weights_bytes": ([I32, I64, I64, ctypes.POINTER(SZ), ctypes.POINTER(SZ)], I32),
         "fgg_pack_fp4_weights": ([P, P, I32, I64, I64, P, P, P], I32),
+        "fgg_moe_route": ([P, I32, I64, I32, I64, I32, I32, P, I32, F32, P, P, P], I32),
+        "fgg_moe_route_backward": ([P, I32, I64, I32, I64, I32, I32, I32, F32, P, P, P, I64, P], I32),
+        "fgg_moe_permute_rows": ([P, I32, I64, I32, I64, I64, P, P, P, P, I32, I64, P, I64, P], I32),
+        "fgg_moe_permute_rows_backward": ([P, I32, I64, I64, P, I64, P, P, I64, I32, I64, P, I64, P, P], I32),
+        "fgg_moe_unpermute_rows": ([P, I32, I64, I64, P, P, I64, I32, I64, P, I64, P], I32),
+        "fgg_moe_unpermute_rows_backward": ([P, I32, I64, I32, I64, I64, P, I64, P, P, P, P, I32, I64, P, I64, P, P],
+                                            I32),
+        "fgg_moe_gemv_fp4": ([I32, I64, I32, I64, I64, P, I32, I64, I32, P, P, QDesc, P, P, I32, P, I32, I64, P], I32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -451,4 +462,218 @@ def moe_down_combine(a, a_scales, b, b_scales, offsets, counts, src_to_row, row_
         _ptr(offsets), _ptr(counts), _ptr(src_to_row), _ptr(row_to_src), _ptr(topk_w), T, k, _ptr(y), y.stride(0),
         _ptr(workspace), workspace.numel(), _ptr(out), out.stride(0), _stream(dev))
     _check("fgg_moe_down_combine", st)
+    return out
+
+
+# ---------------------------------------------- router, rows in bf16/fp32, few tokens
+
+_FLOAT = {torch.float32: FGG_F32, torch.bfloat16: FGG_BF16}
+_GATES = {"softmax": FGG_GATE_SOFTMAX, "sigmoid": FGG_GATE_SIGMOID}
+
+
+def _call(name, dev, *args):
+    """Call the entry point on dev's current stream, with dev as the current device."""
+    fn = getattr(_lib or load_library(), name)
+    if dev.index == torch.cuda.current_device():
+        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if status != 0:
+        _check(name, status)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _float_rows(t, name, dtype=None):
+    """A 2-D fp32/bf16 CUDA tensor with unit column stride and rows that do not overlap; returns its row stride."""
+    assert t.is_cuda and t.dim() == 2 and t.dtype in _FLOAT and (dtype is None or t.dtype == dtype), name
+    n = t.shape[1]
+    assert t.stride(1) == 1 or n <= 1, name
+    ld = t.stride(0)
+    if t.shape[0] <= 1 and ld < n:
+        ld = n
+    assert ld >= n, name
+    return ld
+
+
+def _dense(t, name, dev, dtype, shape=None, numel=None):
+    """A contiguous tensor of the given type and shape (or number of elements) on dev, or None."""
+    if t is None:
+        return
+    assert t.device == dev and t.dtype == dtype and t.is_contiguous(), name
+    assert (shape is None or tuple(t.shape) == shape) and (numel is None or t.numel() == numel), name
+
+
+def moe_route(logits, k, gate="softmax", bias=None, renormalize=False, scale=1.0, ids=None, weights=None):
+    """The router (fgg_moe_route): logits [T, E] (fp32 or bf16, rows may be strided) to
+    (topk_ids int32 [T, k], topk_w fp32 [T, k]) in decreasing order, ties to the lower
+    expert.  gate "softmax" or "sigmoid"; bias (fp32 [E]) enters the selection only;
+    renormalize divides the weights by their sum over the k; scale multiplies them.
+    Experts at -inf are never chosen; slots left over have id -1 and weight 0."""
+    ld = _float_rows(logits, "logits")
+    T, E = logits.shape
+    k, dev = int(k), logits.device
+    if ids is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    if weights is None:
+        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    _dense(bias, "bias", dev, torch.float32, (E,))
+    _dense(ids, "ids", dev, torch.int32, (T, k))
+    _dense(weights, "weights", dev, torch.float32, (T, k))
+    _call("fgg_moe_route", dev, logits.data_ptr(), _FLOAT[logits.dtype], T, E, ld, k, _GATES[gate], _addr(bias),
+          1 if renormalize else 0, float(scale), ids.data_ptr(), weights.data_ptr())
+    return ids, weights
+
+
+def moe_route_backward(logits, topk_ids, dtopk_w, gate="softmax", renormalize=False, scale=1.0, out=None):
+    """Gradient of moe_route's logits ([T, E], the logits' type) from that of its weights
+    (fp32 [T, k]) at the ids it chose (fgg_moe_route_backward)."""
+    ld = _float_rows(logits, "logits")
+    T, E = logits.shape
+    k, dev = topk_ids.shape[1], logits.device
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    ldo = _float_rows(out, "out", logits.dtype)
+    assert out.device == dev and out.shape == logits.shape, "out"
+    _dense(topk_ids, "topk_ids", dev, torch.int32, (T, k))
+    _dense(dtopk_w, "dtopk_w", dev, torch.float32, (T, k))
+    _call("fgg_moe_route_backward", dev, logits.data_ptr(), _FLOAT[logits.dtype], T, E, ld, k, _GATES[gate],
+          1 if renormalize else 0, float(scale), topk_ids.data_ptr(), dtopk_w.data_ptr(), out.data_ptr(), ldo)
+    return out
+
+
+def _slots(src_to_row, T, topk_w, dev):
+    """k, from the T * k entries of the map (of no token: from the weights, or 1)."""
+    _dense(src_to_row, "src_to_row", dev, torch.int32)
+    if T == 0:
+        return 1 if topk_w is None else topk_w.shape[1]
+    assert src_to_row.numel() % T == 0, "src_to_row holds T * k pairs"
+    return src_to_row.numel() // T
+
+
+def _rows_out(out, shape, like, name):
+    if out is None:
+        out = torch.empty(shape, dtype=like.dtype, device=like.device)
+    ld = _float_rows(out, name, like.dtype)
+    assert out.device == like.device and tuple(out.shape) == shape, name
+    return out, ld
+
+
+def moe_permute_rows(x, src_to_row, row_to_src, offsets, topk_w=None, out=None):
+    """Token rows (fp32 or bf16 [T, N]) in the order of moe_permute's maps, optionally scaled
+    by topk_w (fp32 [T, k]): out [M, N] with M = row_to_src's length (fgg_moe_permute_rows).
+    Padding rows are zeroed; rows past offsets[E] are left as they were."""
+    ldx = _float_rows(x, "x")
+    T, N = x.shape
+    dev, M = x.device, row_to_src.numel()
+    k = _slots(src_to_row, T, topk_w, dev)
+    out, ldr = _rows_out(out, (M, N), x, "out")
+    _dense(row_to_src, "row_to_src", dev, torch.int32)
+    _dense(offsets, "offsets", dev, torch.int32)
+    _dense(topk_w, "topk_w", dev, torch.float32, (T, k))
+    _call("fgg_moe_permute_rows", dev, x.data_ptr(), _FLOAT[x.dtype], T, k, N, ldx, _addr(topk_w),
+          src_to_row.data_ptr(), row_to_src.data_ptr(), offsets.data_ptr(), offsets.numel() - 1, M, out.data_ptr(),
+          ldr)
+    return out
+
+
+def moe_permute_rows_backward(drows, src_to_row, T, topk_w=None, x=None, out=None):
+    """Gradients of moe_permute_rows: (dx [T, N], dtopk_w fp32 [T, k] or None).  dtopk_w is
+    computed when the forward's input x is given (fgg_moe_permute_rows_backward)."""
+    lddr = _float_rows(drows, "drows")
+    M, N = drows.shape
+    dev = drows.device
+    k = _slots(src_to_row, T, topk_w, dev)
+    dx, lddx = _rows_out(out, (T, N), drows, "out")
+    _dense(topk_w, "topk_w", dev, torch.float32, (T, k))
+    dw, ldx = None, 0
+    if x is not None:
+        ldx = _float_rows(x, "x", drows.dtype)
+        assert x.device == dev and tuple(x.shape) == (T, N), "x"
+        dw = torch.empty((T, k), dtype=torch.float32, device=dev)
+    _call("fgg_moe_permute_rows_backward", dev, drows.data_ptr(), _FLOAT[drows.dtype], M, lddr, _addr(x), ldx,
+          _addr(topk_w), src_to_row.data_ptr(), T, k, N, dx.data_ptr(), lddx, _addr(dw))
+    return dx, dw
+
+
+def moe_unpermute_rows(rows, src_to_row, T, topk_w=None, out=None):
+    """out[t] = sum_j w[t, j] * rows[src_to_row[t k + j]] in the rows' type (fp32 or bf16,
+    [M, N] -> [T, N]; weights of 1 without topk_w) (fgg_moe_unpermute_rows)."""
+    ldr = _float_rows(rows, "rows")
+    M, N = rows.shape
+    dev = rows.device
+    k = _slots(src_to_row, T, topk_w, dev)
+    out, ldo = _rows_out(out, (T, N), rows, "out")
+    _dense(topk_w, "topk_w", dev, torch.float32, (T, k))
+    _call("fgg_moe_unpermute_rows", dev, rows.data_ptr(), _FLOAT[rows.dtype], M, ldr, _addr(topk_w),
+          src_to_row.data_ptr(), T, k, N, out.data_ptr(), ldo)
+    return out
+
+
+def moe_unpermute_rows_backward(dout, src_to_row, row_to_src, offsets, topk_w=None, rows=None, out=None):
+    """Gradients of moe_unpermute_rows: (drows [M, N], dtopk_w fp32 [T, k] or None).  dtopk_w
+    is computed when the forward's rows are given (fgg_moe_unpermute_rows_backward)."""
+    lddo = _float_rows(dout, "dout")
+    T, N = dout.shape
+    dev, M = dout.device, row_to_src.numel()
+    k = _slots(src_to_row, T, topk_w, dev)
+    drows, lddr = _rows_out(out, (M, N), dout, "out")
+    _dense(row_to_src, "row_to_src", dev, torch.int32)
+    _dense(offsets, "offsets", dev, torch.int32)
+    _dense(topk_w, "topk_w", dev, torch.float32, (T, k))
+    dw, ldr = None, 0
+    if rows is not None:
+        ldr = _float_rows(rows, "rows", dout.dtype)
+        assert rows.device == dev and tuple(rows.shape) == (M, N), "rows"
+        dw = torch.empty((T, k), dtype=torch.float32, device=dev)
+    _call("fgg_moe_unpermute_rows_backward", dev, dout.data_ptr(), _FLOAT[dout.dtype], T, k, N, lddo, _addr(rows), ldr,
+          _addr(topk_w), src_to_row.data_ptr(), row_to_src.data_ptr(), offsets.data_ptr(), offsets.numel() - 1, M,
+          drows.data_ptr(), lddr, _addr(dw))
+    return drows, dw
+
+
+def moe_gemv_fp4(x, b, b_scales, topk_ids=None, topk_w=None, b_qdesc=Q_E2M1_E8M0_1x32, n=None, silu_mul=False,
+                 out=None, out_dtype=torch.bfloat16):
+    """Few tokens times FP4 expert weights, activations unquantized (fgg_moe_gemv_fp4).
+
+    x: fp32/bf16 [T, K] (every slot of a token reads its row) or [T, k, K] (a row per slot).
+    b, b_scales: [G, N, K/2], [G, N, K/32] (with silu_mul 2N rows, [gate | up]), or their
+    tiled form (Q_E2M1_E8M0_1x32_TILED, from pack_fp4_weights; ``n`` gives N, the output columns).
+    topk_ids int32 [T, k]: the result is [T, k, N]; with topk_w (fp32 [T, k]) the
+    gate-weighted sum over the slots, [T, N].  Without topk_ids (G = 1): [T, N]."""
+    per_slot = x.dim() == 3
+    assert x.is_cuda and x.dim() in (2, 3) and x.dtype in _FLOAT and out_dtype in _FLOAT, "x"
+    T, K = x.shape[0], x.shape[-1]
+    dev, G = x.device, b.shape[0]
+    k = 1 if topk_ids is None else topk_ids.shape[1]
+    if per_slot:
+        assert x.shape[1] == k and x.is_contiguous(), "x"
+        ldx = K
+    else:
+        ldx = _float_rows(x, "x")
+    rows = 2 if silu_mul else 1
+    if b_qdesc == Q_E2M1_E8M0_1x32_TILED:
+        assert n is not None, "n"
+        N = int(n)
+        _dense(b, "b", dev, torch.uint8, numel=G * rows * N * K // 2)
+        _dense(b_scales, "b_scales", dev, torch.uint8, numel=G * (rows * N // 16) * ((K + 511) // 512) * 256)
+    else:
+        assert b.shape[1] % rows == 0 and (n is None or int(n) * rows == b.shape[1]), "n"
+        N = b.shape[1] // rows
+        _dense(b, "b", dev, torch.uint8, (G, rows * N, K // 2))
+        _dense(b_scales, "b_scales", dev, torch.uint8, (G, rows * N, K // 32))
+    _dense(topk_ids, "topk_ids", dev, torch.int32, (T, k))
+    _dense(topk_w, "topk_w", dev, torch.float32, (T, k))
+    shape = (T, N) if topk_ids is None or topk_w is not None else (T, k, N)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=dev)
+    assert out.device == dev and out.dtype in _FLOAT and tuple(out.shape) == shape, "out"
+    assert out.is_contiguous() or out.dim() == 2, "out"
+    ldo = N if out.dim() == 3 else _float_rows(out, "out")
+    _call("fgg_moe_gemv_fp4", dev, G, T, k, N, K, x.data_ptr(), _FLOAT[x.dtype], ldx, 1 if per_slot else 0,
+          b.data_ptr(), b_scales.data_ptr(), QDesc(*b_qdesc), _addr(topk_ids), _addr(topk_w),
+          FGG_ACT_SILU_MUL if silu_mul else FGG_ACT_NONE, out.data_ptr(), _FLOAT[out.dtype], ldo)
     return out

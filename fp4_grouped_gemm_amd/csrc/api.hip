@@ -58,6 +58,10 @@ bool same_q(const fgg_qdesc& q, fgg_dtype data, fgg_dtype scale, int br, int bk)
 
 fgg_status finish(hipError_t e) { return e == hipSuccess ? FGG_OK : hip_fail(e); }
 
+// The activations' own types: fp32 or bf16, and the alignment of one element.
+bool float_type(fgg_dtype t) { return t == FGG_F32 || t == FGG_BF16; }
+size_t float_size(fgg_dtype t) { return t == FGG_F32 ? 4 : 2; }
+
 }  // namespace
 
 namespace fgg {
@@ -91,6 +95,9 @@ int kernel_table(const KernelInfo* const** out) {
       &kInfoFp8Dense,        &kInfoMaskedFp4Tiled,    &kInfoMaskedFp4,
       &kInfoMaskedFp8,       &kInfoPackFp4,           &kInfoPackFp4Scales,  &kInfoW4a4Prep,
       &kInfoW4a4LowRank,     &kInfoW4a4Gemm,         &kInfoMxfp4Gemm,
+      &kInfoRoute,           &kInfoRouteBackward,     &kInfoRowsScatter,    &kInfoRowsCollect,
+      &kInfoRowsScatterDot,  &kInfoRowsCollectDot,    &kInfoGemvFp4,        &kInfoGemvFp4Silu,
+      &kInfoGemvFp4Sum,
   };
   *out = table;
   return (int)(sizeof table / sizeof table[0]);
@@ -443,6 +450,158 @@ fgg_status fgg_moe_down_combine(int32_t G, int64_t M, int64_t N, int64_t K, cons
   if (e == hipSuccess)
     e = fgg::launch_combine_rest((const uint16_t*)y, ldy, src_to_row, topk_w, T, k, N, (uint16_t*)out, ldo, hs);
   return finish(e);
+}
+
+static fgg_status route_check(fgg_dtype dtype, int64_t T, int32_t E, int64_t ld, int32_t k, fgg_gate gate, float scale) {
+  if (T < 0 || E < 1 || E > 1024 || k < 1 || k > 64 || k > E || ld < E) return FGG_ERR_INVALID_VALUE;
+  if (gate != FGG_GATE_SOFTMAX && gate != FGG_GATE_SIGMOID) return FGG_ERR_INVALID_VALUE;
+  if (!(scale - scale == 0.0f)) return FGG_ERR_INVALID_VALUE;   // finite
+  if (!float_type(dtype)) return FGG_ERR_UNSUPPORTED;
+  // (one group of lanes per token: 256-thread blocks of 4, 8 or 16 tokens, and int32 pairs)
+  if (T > (int64_t)fgg::kMaxRowBlocks * 4 || T * (int64_t)k > (int64_t)INT32_MAX) return FGG_ERR_UNSUPPORTED;
+  return FGG_OK;
+}
+
+fgg_status fgg_moe_route(const void* logits, fgg_dtype dtype, int64_t T, int32_t E, int64_t ld, int32_t k,
+                         fgg_gate gate, const float* bias, int32_t renormalize, float scale, int32_t* topk_ids,
+                         float* topk_w, void* stream) {
+  fgg_status st = route_check(dtype, T, E, ld, k, gate, scale);
+  if (st != FGG_OK) return st;
+  if (T == 0) return FGG_OK;
+  if (!logits || !topk_ids || !topk_w) return FGG_ERR_INVALID_VALUE;
+  if (!aligned(logits, float_size(dtype)) || !aligned(topk_ids, 4) || !aligned(topk_w, 4) || !aligned(bias, 4))
+    return FGG_ERR_INVALID_VALUE;
+  st = device_check(nullptr);
+  if (st != FGG_OK) return st;
+  return finish(fgg::launch_route(logits, dtype == FGG_BF16, T, E, ld, k, gate == FGG_GATE_SIGMOID, bias,
+                                  renormalize != 0, scale, topk_ids, topk_w, (hipStream_t)stream));
+}
+
+fgg_status fgg_moe_route_backward(const void* logits, fgg_dtype dtype, int64_t T, int32_t E, int64_t ld, int32_t k,
+                                  fgg_gate gate, int32_t renormalize, float scale, const int32_t* topk_ids,
+                                  const float* dtopk_w, void* dlogits, int64_t ldd, void* stream) {
+  fgg_status st = route_check(dtype, T, E, ld, k, gate, scale);
+  if (st != FGG_OK) return st;
+  if (ldd < E) return FGG_ERR_INVALID_VALUE;
+  if (T == 0) return FGG_OK;
+  if (!logits || !topk_ids || !dtopk_w || !dlogits) return FGG_ERR_INVALID_VALUE;
+  if (!aligned(logits, float_size(dtype)) || !aligned(dlogits, float_size(dtype)) || !aligned(topk_ids, 4) ||
+      !aligned(dtopk_w, 4))
+    return FGG_ERR_INVALID_VALUE;
+  st = device_check(nullptr);
+  if (st != FGG_OK) return st;
+  return finish(fgg::launch_route_backward(logits, dtype == FGG_BF16, T, E, ld, k, gate == FGG_GATE_SIGMOID,
+                                           renormalize != 0, scale, topk_ids, dtopk_w, dlogits, ldd,
+                                           (hipStream_t)stream));
+}
+
+// Arguments of the four row calls: tokens [T][ldt], rows [M][ldr], both of `dtype`.
+static fgg_status rows_check(fgg_dtype dtype, int64_t T, int32_t k, int64_t N, int64_t M, int64_t ldt, int64_t ldr) {
+  if (T < 0 || k < 1 || k > 64 || N < 1 || M < 0 || ldt < N || ldr < N) return FGG_ERR_INVALID_VALUE;
+  if (!float_type(dtype)) return FGG_ERR_UNSUPPORTED;
+  if (T * (int64_t)k > (int64_t)INT32_MAX || M > (int64_t)INT32_MAX || T > fgg::kMaxRowBlocks ||
+      T + M / 16 + 1 > fgg::kMaxRowBlocks || N > (int64_t(1) << 26))
+    return FGG_ERR_UNSUPPORTED;
+  return FGG_OK;
+}
+
+fgg_status fgg_moe_permute_rows(const void* x, fgg_dtype dtype, int64_t T, int32_t k, int64_t N, int64_t ldx,
+                                const float* topk_w, const int32_t* src_to_row, const int32_t* row_to_src,
+                                const int32_t* offsets, int32_t E, int64_t M, void* rows, int64_t ldr,
+                                void* stream) {
+  fgg_status st = rows_check(dtype, T, k, N, M, ldx, ldr);
+  if (st != FGG_OK) return st;
+  if (E < 1 || E > 1024) return FGG_ERR_INVALID_VALUE;
+  if (T == 0 || M == 0) return FGG_OK;
+  if (!x || !src_to_row || !row_to_src || !offsets || !rows) return FGG_ERR_INVALID_VALUE;
+  const size_t el = float_size(dtype);
+  if (!aligned(x, el) || !aligned(rows, el) || !aligned(topk_w, 4)) return FGG_ERR_INVALID_VALUE;
+  st = device_check(nullptr);
+  if (st != FGG_OK) return st;
+  return finish(fgg::launch_rows_scatter(x, dtype == FGG_BF16, ldx, nullptr, 0, topk_w, src_to_row, row_to_src,
+                                         offsets, E, T, k, N, M, rows, ldr, nullptr, (hipStream_t)stream));
+}
+
+fgg_status fgg_moe_permute_rows_backward(const void* drows, fgg_dtype dtype, int64_t M, int64_t lddr, const void* x,
+                                         int64_t ldx, const float* topk_w, const int32_t* src_to_row, int64_t T,
+                                         int32_t k, int64_t N, void* dx, int64_t lddx, float* dtopk_w, void* stream) {
+  fgg_status st = rows_check(dtype, T, k, N, M, lddx, lddr);
+  if (st != FGG_OK) return st;
+  if (dtopk_w && ldx < N) return FGG_ERR_INVALID_VALUE;
+  if (T == 0) return FGG_OK;
+  if ((M > 0 && !drows) || !src_to_row || !dx || (dtopk_w && !x)) return FGG_ERR_INVALID_VALUE;
+  const size_t el = float_size(dtype);
+  if (!aligned(drows, el) || !aligned(dx, el) || !aligned(topk_w, 4) || !aligned(dtopk_w, 4) ||
+      (dtopk_w && !aligned(x, el)))
+    return FGG_ERR_INVALID_VALUE;
+  st = device_check(nullptr);
+  if (st != FGG_OK) return st;
+  return finish(fgg::launch_rows_collect(drows, dtype == FGG_BF16, lddr, x, ldx, topk_w, src_to_row, T, k, N, M, dx,
+                                         lddx, dtopk_w, (hipStream_t)stream));
+}
+
+fgg_status fgg_moe_unpermute_rows(const void* rows, fgg_dtype dtype, int64_t M, int64_t ldr, const float* topk_w,
+                                  const int32_t* src_to_row, int64_t T, int32_t k, int64_t N, void* out, int64_t ldo,
+                                  void* stream) {
+  fgg_status st = rows_check(dtype, T, k, N, M, ldo, ldr);
+  if (st != FGG_OK) return st;
+  if (T == 0) return FGG_OK;
+  if ((M > 0 && !rows) || !src_to_row || !out) return FGG_ERR_INVALID_VALUE;
+  const size_t el = float_size(dtype);
+  if (!aligned(rows, el) || !aligned(out, el) || !aligned(topk_w, 4)) return FGG_ERR_INVALID_VALUE;
+  st = device_check(nullptr);
+  if (st != FGG_OK) return st;
+  return finish(fgg::launch_rows_collect(rows, dtype == FGG_BF16, ldr, nullptr, 0, topk_w, src_to_row, T, k, N, M, out,
+                                         ldo, nullptr, (hipStream_t)stream));
+}
+
+fgg_status fgg_moe_unpermute_rows_backward(const void* dout, fgg_dtype dtype, int64_t T, int32_t k, int64_t N,
+                                           int64_t lddo, const void* rows, int64_t ldr, const float* topk_w,
+                                           const int32_t* src_to_row, const int32_t* row_to_src,
+                                           const int32_t* offsets, int32_t E, int64_t M, void* drows, int64_t lddr,
+                                           float* dtopk_w, void* stream) {
+  fgg_status st = rows_check(dtype, T, k, N, M, lddo, lddr);
+  if (st != FGG_OK) return st;
+  if (E < 1 || E > 1024 || (dtopk_w && ldr < N)) return FGG_ERR_INVALID_VALUE;
+  if (T == 0 || (M == 0 && !dtopk_w)) return FGG_OK;
+  if (!dout || !src_to_row || !offsets || (M > 0 && (!row_to_src || !drows || (dtopk_w && !rows))))
+    return FGG_ERR_INVALID_VALUE;
+  const size_t el = float_size(dtype);
+  if (!aligned(dout, el) || !aligned(drows, el) || !aligned(topk_w, 4) || !aligned(dtopk_w, 4) ||
+      (dtopk_w && !aligned(rows, el)))
+    return FGG_ERR_INVALID_VALUE;
+  st = device_check(nullptr);
+  if (st != FGG_OK) return st;
+  return finish(fgg::launch_rows_scatter(dout, dtype == FGG_BF16, lddo, rows, ldr, topk_w, src_to_row, row_to_src,
+                                         offsets, E, T, k, N, M, drows, lddr, dtopk_w, (hipStream_t)stream));
+}
+
+fgg_status fgg_moe_gemv_fp4(int32_t G, int64_t T, int32_t k, int64_t N, int64_t K, const void* x, fgg_dtype x_dtype,
+                            int64_t ldx, int32_t x_per_slot, const void* b, const void* b_scales, fgg_qdesc bq,
+                            const int32_t* topk_ids, const float* topk_w, fgg_act act, void* out,
+                            fgg_dtype out_dtype, int64_t ldo, void* stream) {
+  if (G < 1 || G > 1024 || T < 0 || k < 1 || k > 64 || N < 0 || K < 0 || ldx < K || ldo < N)
+    return FGG_ERR_INVALID_VALUE;
+  if (act != FGG_ACT_NONE && act != FGG_ACT_SILU_MUL) return FGG_ERR_INVALID_VALUE;
+  // one set of weights has one slot per token; a weighted sum needs slots
+  if (!topk_ids && T > 0 && (G != 1 || k != 1 || topk_w)) return FGG_ERR_INVALID_VALUE;
+  if (!float_type(x_dtype) || !float_type(out_dtype)) return FGG_ERR_UNSUPPORTED;
+  if (topk_w && act != FGG_ACT_NONE) return FGG_ERR_UNSUPPORTED;
+  const bool tiled = same_q(bq, FGG_E2M1X2_TILED, FGG_E8M0, 1, 32);
+  if (!tiled && !same_q(bq, FGG_E2M1X2, FGG_E8M0, 1, 32)) return FGG_ERR_UNSUPPORTED;
+  if (K == 0 || K % (tiled ? 128 : 32) != 0 || (tiled && N % 16 != 0)) return FGG_ERR_UNSUPPORTED;
+  // (grid limits: 16 rows and 16 tokens per workgroup)
+  if (N > (int64_t(1) << 26) || K > (int64_t(1) << 26) || T > 16 * (int64_t)65535) return FGG_ERR_UNSUPPORTED;
+  if (T == 0 || N == 0) return FGG_OK;
+  if (!x || !b || !b_scales || !out) return FGG_ERR_INVALID_VALUE;
+  if (!aligned(x, float_size(x_dtype)) || !aligned(out, float_size(out_dtype)) || !aligned(b, 16) ||
+      (tiled && !aligned(b_scales, 16)) || !aligned(topk_ids, 4) || !aligned(topk_w, 4))
+    return FGG_ERR_INVALID_VALUE;
+  fgg_status st = device_check(nullptr);
+  if (st != FGG_OK) return st;
+  return finish(fgg::launch_gemv_fp4(tiled, G, T, k, N, K, x, x_dtype == FGG_BF16, ldx, x_per_slot != 0,
+                                     (const uint8_t*)b, (const uint8_t*)b_scales, topk_ids, topk_w,
+                                     act == FGG_ACT_SILU_MUL, out, out_dtype == FGG_BF16, ldo, (hipStream_t)stream));
 }
 
 int32_t fgg_kernel_count(void) {

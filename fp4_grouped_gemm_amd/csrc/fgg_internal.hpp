@@ -38,7 +38,8 @@ extern const KernelInfo kInfoQuantE4m3_1x128, kInfoQuantE4m3_128x128, kInfoQuant
     kInfoPermuteQuantize, kInfoFill, kInfoCombine, kInfoCombineRows, kInfoCombineRest, kInfoFp8Contig,
     kInfoFp8ContigSilu, kInfoFp8ContigCombine, kInfoFp8Dense,
     kInfoMaskedFp4Tiled, kInfoMaskedFp4, kInfoMaskedFp8, kInfoPackFp4, kInfoPackFp4Scales, kInfoW4a4Prep, kInfoW4a4LowRank,
-    kInfoW4a4Gemm, kInfoMxfp4Gemm;
+    kInfoW4a4Gemm, kInfoMxfp4Gemm, kInfoRoute, kInfoRouteBackward, kInfoRowsScatter, kInfoRowsCollect,
+    kInfoRowsScatterDot, kInfoRowsCollectDot, kInfoGemvFp4, kInfoGemvFp4Silu, kInfoGemvFp4Sum;
 
 enum class QuantKind { E4M3_1x128, E4M3_128x128, E2M1_1x16, E2M1_E8M0_1x32 };
 
@@ -121,5 +122,30 @@ size_t mxfp4_workspace_bytes(int64_t M, int32_t rank);
 hipError_t launch_mxfp4(int64_t M, int64_t N, int64_t K, const uint8_t* a, const uint8_t* sa, const uint8_t* b,
                         const uint8_t* sb, const uint16_t* x_bf16, const uint16_t* l_down, const uint16_t* l_up,
                         int32_t rank, const uint16_t* bias, uint16_t* d, int64_t ldd, void* ws, hipStream_t st);
+
+// The router: logits [T][E] to the k largest experts' ids and gate weights, and the logits' gradient.
+hipError_t launch_route(const void* logits, bool bf16, int64_t T, int32_t E, int64_t ld, int32_t k, bool sigmoid,
+                        const float* bias, bool renorm, float scale, int32_t* ids, float* w, hipStream_t st);
+hipError_t launch_route_backward(const void* logits, bool bf16, int64_t T, int32_t E, int64_t ld, int32_t k,
+                                 bool sigmoid, bool renorm, float scale, const int32_t* ids, const float* dw,
+                                 void* dlogits, int64_t ldd, hipStream_t st);
+
+// Token rows to permuted rows (padding rows zeroed), and permuted rows summed per token; w (nullable)
+// weights each pair.  dw (nullable): also <tok, rows> per pair, against fwd_rows / fwd_tok.
+hipError_t launch_rows_scatter(const void* tok, bool bf16, int64_t ldt, const void* fwd_rows, int64_t ldf,
+                               const float* w, const int32_t* src_to_row, const int32_t* row_to_src,
+                               const int32_t* offsets, int32_t E, int64_t T, int32_t k, int64_t N, int64_t M,
+                               void* rows, int64_t ldr, float* dw, hipStream_t st);
+hipError_t launch_rows_collect(const void* rows, bool bf16, int64_t ldr, const void* fwd_tok, int64_t ldf,
+                               const float* w, const int32_t* src_to_row, int64_t T, int32_t k, int64_t N, int64_t M,
+                               void* tok, int64_t ldt, float* dw, hipStream_t st);
+// Tokens (and padding blocks) that one row launch holds: its grid has that many 256-thread blocks.
+constexpr int64_t kMaxRowBlocks = 0xFFFFFF;
+
+// Few tokens times FP4 expert weights: plain or SiLU(gate)*up per slot, or (w given) summed per token.
+hipError_t launch_gemv_fp4(bool tiled, int32_t G, int64_t T, int32_t k, int64_t N, int64_t K, const void* x,
+                           bool x_bf16, int64_t ldx, bool per_slot, const uint8_t* b, const uint8_t* s,
+                           const int32_t* ids, const float* w, bool silu, void* out, bool out_bf16, int64_t ldo,
+                           hipStream_t st);
 
 }  // namespace fgg

@@ -1,0 +1,327 @@
+// The router of a mixture-of-experts layer: from each token's logits over the experts
+// to its k expert ids and gate weights, and the gradient of the logits.
+//
+//   s_e   = softmax(l)_e  or  sigmoid(l_e)
+//   key_e = l_e without a selection bias (both gates grow with l), s_e + b_e with one
+//   ids   = the k largest keys in decreasing order, ties to the lower expert
+//   w_j   = scale * s_{ids j}          or, renormalized,   scale * s_{ids j} / sum_m s_{ids m}
+//
+// One group of lanes (16, 32 or 64, the smallest that has a lane for every expert up to
+// 64) owns a token and holds its logits in registers, expert i * GW + lane in register i;
+// a wave takes 64 / GW tokens.  Selection: k rounds of a group-wide maximum over 32-bit
+// keys in integer order.  What depends on every expert (the softmax's normalizer) is
+// computed only when it is asked for: the renormalized softmax is the softmax of the k
+// chosen logits.
+//
+// With a bias the keys are sums of rounded scores, and two experts whose keys differ by
+// less than the rounding of 32 bits would be ordered by it: keys are formed in 64 bits
+// (the sigmoid or exponential of every logit in double), and ranked as 64-bit integers.
+#include "fgg_device.hpp"
+#include "fgg_internal.hpp"
+#include "fgg_wave.hpp"
+
+namespace fgg {
+
+namespace {
+
+constexpr float kInf = __builtin_inff();
+
+template <class T>
+__device__ inline float load_one(const T* p);
+template <>
+__device__ inline float load_one<float>(const float* p) { return *p; }
+template <>
+__device__ inline float load_one<uint16_t>(const uint16_t* p) { return bf16_to_f32(*p); }
+
+__device__ inline void store_one(float* p, float v) { *p = v; }
+__device__ inline void store_one(uint16_t* p, float v) { *p = bf16_bits_rne(v); }
+
+// Floating order as unsigned order; 0 is below every number's key (the key of -inf is
+// 0x007FFFFF) and stands for "cannot be chosen".  Signed zeros are made equal first.
+__device__ inline uint32_t order_key(float x) {
+  const uint32_t u = __float_as_uint(x + 0.0f);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ inline float order_value(uint32_t k) {
+  return __uint_as_float(k ^ ((uint32_t)((int32_t)~k >> 31) | 0x80000000u));
+}
+__device__ inline uint64_t order_key(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x + 0.0);
+  return u ^ ((uint64_t)((int64_t)u >> 63) | 0x8000000000000000ull);
+}
+
+// sigma(v) * e^-m for m <= 0 and v <= max(m, 0): the scale e^-m keeps the sum of the
+// chosen scores away from zero when every chosen logit is far below zero.
+__device__ inline float sigmoid_scaled(float v, float m) {
+  if (v >= 0.0f) return 1.0f / (1.0f + expf(-v));
+  return expf(v - m) / (1.0f + expf(v));
+}
+
+// The group's lane `src` (0 <= src < GW) of v.
+template <int GW>
+__device__ inline int group_lane(int v, int src) {
+  return __shfl(v, src, GW);
+}
+
+// Gate weights of the chosen experts: lane j of a group holds slot j's logit v (on:
+// the slot holds an expert).  m_all, sum_all: the softmax's maximum and normalizer over
+// all experts (read only for the softmax without renormalization).
+template <int GW>
+__device__ inline float gate_weight(float v, bool on, bool sigmoid, bool renorm, float m_all, float sum_all) {
+  float num;
+  if (sigmoid) {
+    const float top = renorm ? group_reduce<GW>(on ? v : -kInf, OpFMax()) : 0.0f;
+    num = on ? sigmoid_scaled(v, fminf(top, 0.0f)) : 0.0f;
+    if (!renorm) return num;
+  } else if (renorm) {
+    const float top = group_reduce<GW>(on ? v : -kInf, OpFMax());
+    num = on ? expf(v - top) : 0.0f;
+  } else {
+    return on ? expf(v - m_all) / sum_all : 0.0f;
+  }
+  const float sum = group_reduce<GW>(num, OpAdd());
+  return on ? num / sum : 0.0f;
+}
+
+}  // namespace
+
+template <class TI, int GW, int EPL, bool BIAS>
+__global__ void __launch_bounds__(256) route_kernel(const TI* __restrict__ logits, int64_t T, int E, int64_t ld, int k,
+                                                    bool sigmoid, const float* __restrict__ bias, bool renorm,
+                                                    float scale, int32_t* __restrict__ ids, float* __restrict__ w) {
+  const int lane = threadIdx.x & 63, gl = lane & (GW - 1);
+  const int64_t t = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * (64 / GW) + lane / GW;
+  const bool live = t < T;
+  const TI* row = logits + (live ? t : 0) * ld;
+  float x[EPL];
+  int bad = 0;                                        // a NaN in the row
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = i * GW + gl;
+    x[i] = (live && e < E) ? load_one(row + e) : -kInf;
+    bad |= x[i] != x[i];
+  }
+  bad = group_reduce<GW>(bad, OpMax());
+
+  // the softmax's maximum and normalizer, where something depends on every expert
+  float m_all = -kInf, sum_all = 0.0f;
+  if (!sigmoid && (BIAS || !renorm)) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) m_all = fmaxf(m_all, x[i]);
+    m_all = group_reduce<GW>(m_all, OpFMax());
+    if (!renorm) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) sum_all += x[i] == -kInf ? 0.0f : expf(x[i] - m_all);
+      sum_all = group_reduce<GW>(sum_all, OpAdd());
+    }
+  }
+
+  using Key = typename std::conditional<BIAS, uint64_t, uint32_t>::type;
+  Key key[EPL];
+  if constexpr (BIAS) {
+    double s[EPL];
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const bool shut = !(x[i] > -kInf);
+      if (sigmoid) {
+        s[i] = 1.0 / (1.0 + exp(-(double)x[i]));
+      } else {
+        s[i] = shut ? 0.0 : exp((double)x[i] - (double)m_all);
+        sum += s[i];
+      }
+    }
+    if (!sigmoid) sum = group_reduce<GW>(sum, OpAdd());
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = i * GW + gl;
+      double c = sigmoid ? s[i] : s[i] / sum;
+      if (!(c == c)) c = 0.0;                         // a row with NaN or +inf: by the bias alone
+      c += e < E ? (double)bias[e] : 0.0;
+      key[i] = (x[i] > -kInf && c > -(double)kInf) ? order_key(c) : 0;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = x[i] > -kInf ? order_key(x[i]) : 0;
+  }
+
+  int my_id = -1;
+  float my_v = 0.0f;
+  for (int j = 0; j < k; ++j) {
+    Key best = 0;
+    int bi = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (key[i] > best) best = key[i], bi = i;
+    const Key top = group_reduce<GW>(best, OpMax());
+    // the lowest expert among those with the largest key
+    const int e = group_reduce<GW>(best == top ? bi * GW + gl : 0x7FFFFFFF, OpMin());
+    const bool found = top != 0;
+    float v;
+    if constexpr (BIAS) {
+      float mine = x[0];
+#pragma unroll
+      for (int i = 1; i < EPL; ++i) mine = i == e / GW ? x[i] : mine;
+      v = __int_as_float(group_lane<GW>(__float_as_int(mine), e & (GW - 1)));
+    } else {
+      v = order_value(top);
+    }
+    if (gl == j && found) my_id = e, my_v = v;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (i * GW + gl == e) key[i] = 0;
+  }
+  const bool on = my_id >= 0;
+  float g = gate_weight<GW>(my_v, on, sigmoid, renorm, m_all, sum_all) * scale;
+  if (bad) g = __builtin_nanf("");
+  if (live && gl < k) {
+    ids[t * k + gl] = my_id;
+    w[t * k + gl] = on ? g : 0.0f;
+  }
+}
+
+// Gradient of the logits from the gradient of the gate weights.  With u_j = scale * dw_j:
+//   softmax:               dl_e = s_e (sum_{j: id_j = e} u_j - sum_j u_j s_{id_j})
+//   softmax, renormalized: dl_e = sum_{j: id_j = e} p_j (u_j - sum_m u_m p_m),  p = softmax of the chosen logits
+//   sigmoid:               dl_e = sum_{j: id_j = e} u_j s_j (1 - s_j)
+//   sigmoid, renormalized: dl_e = sum_{j: id_j = e} p_j (1 - s_j)(u_j - sum_m u_m p_m),  p_j = s_j / sum_m s_m
+// Only the first reads every logit; the others read the chosen ones and write the row.
+template <class TI, int GW, int EPL>
+__global__ void __launch_bounds__(256) route_backward_kernel(const TI* __restrict__ logits, int64_t T, int E,
+                                                             int64_t ld, int k, bool sigmoid, bool renorm, float scale,
+                                                             const int32_t* __restrict__ ids,
+                                                             const float* __restrict__ dw, TI* __restrict__ dlogits,
+                                                             int64_t ldd) {
+  const int lane = threadIdx.x & 63, gl = lane & (GW - 1);
+  const int64_t t = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * (64 / GW) + lane / GW;
+  const bool live = t < T;
+  const TI* row = logits + (live ? t : 0) * ld;
+  int id = -1;
+  float u = 0.0f, v = -kInf;
+  if (live && gl < k) {
+    id = ids[t * k + gl];
+    if (id < 0 || id >= E) {
+      id = -1;
+    } else {
+      u = scale * dw[t * k + gl];
+      v = load_one(row + id);
+    }
+  }
+  const bool on = id >= 0;
+  float out[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) out[i] = 0.0f;
+  float d, dot = 0.0f, m = -kInf, sum = 0.0f;
+  const bool whole = !sigmoid && !renorm;
+  float x[EPL];
+  if (whole) {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = i * GW + gl;
+      x[i] = (live && e < E) ? load_one(row + e) : -kInf;
+      m = fmaxf(m, x[i]);
+      bad |= x[i] != x[i];
+    }
+    m = group_reduce<GW>(m, OpFMax());
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      x[i] = x[i] == -kInf ? 0.0f : expf(x[i] - m);   // 0 for closed experts, also in a row of them
+      sum += x[i];
+    }
+    if (bad) sum = __builtin_nanf("");
+    sum = group_reduce<GW>(sum, OpAdd());
+    const float inv_ok = sum > 0.0f || sum != sum ? sum : 1.0f;   // a row without any expert: all zero
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) x[i] = x[i] / inv_ok;
+    const float s = on && v > -kInf ? expf(v - m) / inv_ok : (on && v != v ? v : 0.0f);
+    dot = group_reduce<GW>(on ? u * s : 0.0f, OpAdd());
+    d = u;
+  } else {
+    float p = gate_weight<GW>(v, on && v != -kInf, sigmoid, renorm, 0.0f, 1.0f);
+    if (renorm) {
+      const float mean = group_reduce<GW>(on ? u * p : 0.0f, OpAdd());
+      d = p * (u - mean);
+    } else {
+      d = u * p;
+    }
+    if (sigmoid && on) d *= v >= 0.0f ? expf(-v) / (1.0f + expf(-v)) : 1.0f / (1.0f + expf(v));   // 1 - sigma(v)
+  }
+  for (int j = 0; j < k; ++j) {
+    const int ej = group_lane<GW>(id, j);
+    const float dj = __int_as_float(group_lane<GW>(__float_as_int(d), j));
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (i * GW + gl == ej) out[i] += dj;
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = i * GW + gl;
+    if (live && e < E) store_one(dlogits + t * ldd + e, whole ? x[i] * (out[i] - dot) : out[i]);
+  }
+}
+
+const KernelInfo kInfoRoute = {"route_kernel", "fgg_moe_route", 0, 0, 0, 256, 0, 0, 0, 0,
+                               (const void*)route_kernel<float, 64, 4, false>};
+const KernelInfo kInfoRouteBackward = {"route_backward_kernel", "fgg_moe_route_backward", 0, 0, 0, 256, 0, 0, 0, 0,
+                                       (const void*)route_backward_kernel<float, 64, 4>};
+
+// Calls f(group width, experts per lane) as compile-time constants: the smallest that hold E.
+template <class F>
+static void with_shape(int E, F f) {
+  using std::integral_constant;
+  if (E <= 16) f(integral_constant<int, 16>(), integral_constant<int, 1>());
+  else if (E <= 32) f(integral_constant<int, 32>(), integral_constant<int, 1>());
+  else if (E <= 64) f(integral_constant<int, 64>(), integral_constant<int, 1>());
+  else if (E <= 128) f(integral_constant<int, 64>(), integral_constant<int, 2>());
+  else if (E <= 256) f(integral_constant<int, 64>(), integral_constant<int, 4>());
+  else if (E <= 512) f(integral_constant<int, 64>(), integral_constant<int, 8>());
+  else f(integral_constant<int, 64>(), integral_constant<int, 16>());
+}
+
+static int64_t route_blocks(int64_t T, int E) {
+  const int per_block = 4 * (E <= 16 ? 4 : E <= 32 ? 2 : 1);
+  return (T + per_block - 1) / per_block;
+}
+
+hipError_t launch_route(const void* logits, bool bf16, int64_t T, int32_t E, int64_t ld, int32_t k, bool sigmoid,
+                        const float* bias, bool renorm, float scale, int32_t* ids, float* w, hipStream_t st) {
+  const dim3 grid((unsigned)route_blocks(T, E));
+  trace_launch(kInfoRoute, grid, "T=%lld E=%d k=%d %s %s%s%s", (long long)T, (int)E, (int)k, bf16 ? "bf16" : "fp32",
+               sigmoid ? "sigmoid" : "softmax", bias ? " bias" : "", renorm ? " renorm" : "");
+  with_shape(E, [&](auto gw, auto epl) {
+    constexpr int GW = decltype(gw)::value, EPL = decltype(epl)::value;
+    auto go = [&](auto* in) {
+      using TI = std::remove_cv_t<std::remove_pointer_t<decltype(in)>>;
+      if (bias)
+        hipLaunchKernelGGL((route_kernel<TI, GW, EPL, true>), grid, dim3(256), 0, st, in, T, (int)E, ld, (int)k,
+                           sigmoid, bias, renorm, scale, ids, w);
+      else
+        hipLaunchKernelGGL((route_kernel<TI, GW, EPL, false>), grid, dim3(256), 0, st, in, T, (int)E, ld, (int)k,
+                           sigmoid, bias, renorm, scale, ids, w);
+    };
+    if (bf16) go((const uint16_t*)logits);
+    else go((const float*)logits);
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_route_backward(const void* logits, bool bf16, int64_t T, int32_t E, int64_t ld, int32_t k,
+                                 bool sigmoid, bool renorm, float scale, const int32_t* ids, const float* dw,
+                                 void* dlogits, int64_t ldd, hipStream_t st) {
+  const dim3 grid((unsigned)route_blocks(T, E));
+  trace_launch(kInfoRouteBackward, grid, "T=%lld E=%d k=%d %s %s%s", (long long)T, (int)E, (int)k,
+               bf16 ? "bf16" : "fp32", sigmoid ? "sigmoid" : "softmax", renorm ? " renorm" : "");
+  with_shape(E, [&](auto gw, auto epl) {
+    constexpr int GW = decltype(gw)::value, EPL = decltype(epl)::value;
+    if (bf16)
+      hipLaunchKernelGGL((route_backward_kernel<uint16_t, GW, EPL>), grid, dim3(256), 0, st, (const uint16_t*)logits,
+                         T, (int)E, ld, (int)k, sigmoid, renorm, scale, ids, dw, (uint16_t*)dlogits, ldd);
+    else
+      hipLaunchKernelGGL((route_backward_kernel<float, GW, EPL>), grid, dim3(256), 0, st, (const float*)logits, T,
+                         (int)E, ld, (int)k, sigmoid, renorm, scale, ids, dw, (float*)dlogits, ldd);
+  });
+  return hipGetLastError();
+}
+
+}  // namespace fgg

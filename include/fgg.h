@@ -70,6 +70,7 @@ typedef struct {
 
 typedef enum { FGG_ACT_NONE = 0, FGG_ACT_SILU_MUL = 1 } fgg_act;
 typedef enum { FGG_LAYOUT_CONTIGUOUS = 0, FGG_LAYOUT_MASKED = 1 } fgg_layout;
+typedef enum { FGG_GATE_SOFTMAX = 0, FGG_GATE_SIGMOID = 1 } fgg_gate;
 
 /* W4A4 epilogue ([W4A4] §1: Y = (Q(X)·Q(W)ᵀ) ⊙ scale + L(X) + b).  All fields may be NULL/0. */
 typedef struct {
@@ -428,6 +429,108 @@ fgg_status fgg_moe_down_combine(int32_t G, int64_t M, int64_t N, int64_t K, cons
                                 const float* topk_w, int64_t T, int32_t k, void* y, int64_t ldy,
                                 void* workspace, size_t ws_bytes, void* out, int64_t ldo,
                                 void* stream);
+
+/*
+ * fgg_moe_route — the router: from each token's logits over the experts to the ids and
+ * gate weights that fgg_moe_permute, fgg_moe_combine and fgg_moe_gemv_fp4 take.
+ *   s[t][e]     = softmax(logits[t])[e]  or  1 / (1 + e^-logits[t][e])
+ *   key[t][e]   = logits[t][e] when bias is NULL (both gates grow with the logit),
+ *                 s[t][e] + bias[e] otherwise (formed in 64 bits)
+ *   topk_ids[t] = the experts of the k largest keys, in decreasing order, ties to the
+ *                 lower expert
+ *   topk_w[t][j] = scale * s[t][id_j], or with renormalize != 0
+ *                 scale * s[t][id_j] / sum_m s[t][id_m]
+ * The bias (e.g. of a load-balancing scheme) selects only; it never enters the weights.
+ * Experts that are closed to a token have logit -inf (or bias -inf): such an expert, and
+ * one whose logit or bias is NaN, is never selected.  A token with fewer than k experts
+ * left gets id -1 and weight 0 in its last slots (ids the permute drops); a row of -inf
+ * gets k of them.  A row with a NaN logit has NaN weights in every slot that holds an
+ * expert; a +inf logit makes a softmax's weights NaN, as the formula does.  (With a bias,
+ * the experts of a softmax row with NaN or +inf are ranked by the bias alone.)
+ * logits: [T][ld] fp32 or bf16, ld >= E, any alignment of the element.  bias: [E] fp32 or
+ * NULL.  topk_ids [T][k] int32, topk_w [T][k] fp32.  1 <= E <= 1024, 1 <= k <= min(E, 64),
+ * scale finite.  T == 0 is a no-op.
+ *
+ * fgg_moe_route_backward — the gradient of the logits from that of the gate weights, at
+ * the ids the forward chose (the choice itself is constant, and the bias has none):
+ *   dlogits[t][e] = sum_j dtopk_w[t][j] * d topk_w[t][j] / d logits[t][e]
+ * Every element of the [T][E] gradient is written (in the logits' type, row stride
+ * ldd >= E; it must not overlap the inputs).  Ids outside [0, E) contribute nothing; an
+ * id that stands twice in a row contributes twice.  Closed experts (-inf) get 0.  Rounded
+ * once from fp32.
+ */
+fgg_status fgg_moe_route(const void* logits, fgg_dtype dtype, int64_t T, int32_t E, int64_t ld, int32_t k,
+                         fgg_gate gate, const float* bias, int32_t renormalize, float scale, int32_t* topk_ids,
+                         float* topk_w, void* stream);
+fgg_status fgg_moe_route_backward(const void* logits, fgg_dtype dtype, int64_t T, int32_t E, int64_t ld, int32_t k,
+                                  fgg_gate gate, int32_t renormalize, float scale, const int32_t* topk_ids,
+                                  const float* dtopk_w, void* dlogits, int64_t ldd, void* stream);
+
+/*
+ * fgg_moe_permute_rows — the token activations themselves (fp32 or bf16) in the permuted
+ * order, optionally scaled by their gate weights; fgg_moe_unpermute_rows — permuted rows
+ * back in token order as a weighted sum; and the gradients of both.  The maps are those of
+ * fgg_moe_permute (its index-only form suffices); p = t·k + j, r = src_to_row[p].
+ *   permute_rows:   rows[r][n] = w[p] * x[t][n];  padding rows of [0, min(offsets[E], M)) are zeroed,
+ *                   rows from there on are left as they were
+ *     backward:     dx[t][n] = sum_j w[p] * drows[r][n];   dtopk_w[p] = sum_n drows[r][n] * x[t][n]
+ *   unpermute_rows: out[t][n] = sum_j w[p] * rows[r][n]    (+0 for a token with no row)
+ *     backward:     drows[r][n] = w[p] * dout[t][n] (padding rows as above);
+ *                   dtopk_w[p] = sum_n dout[t][n] * rows[r][n]
+ * topk_w [T][k] fp32 may be NULL: every weight is 1 (a row is then the token's bits).  dtopk_w
+ * may be NULL; when given, the forward's input (x, or rows) is read and dtopk_w [T][k] fp32 is
+ * written whole, 0 for a pair without a row.  A pair whose r is outside [0, M) has no row.
+ * Sums over slots run in increasing j in fp32 (with bf16 rows, the result of
+ * fgg_moe_combine bit for bit) and are rounded once; dot products are fp32 sums in a fixed
+ * order.  All results are the same from run to run.
+ * Any N >= 1, row strides >= N and element-aligned pointers; each output must not overlap
+ * an input.  row_to_src [M], offsets [E + 1], 1 <= k <= 64, 1 <= E <= 1024.  T == 0 is a
+ * no-op (nothing is written).  T + M/16 must stay below 2^24 - 1, N at most 2^26
+ * (FGG_ERR_UNSUPPORTED beyond).
+ */
+fgg_status fgg_moe_permute_rows(const void* x, fgg_dtype dtype, int64_t T, int32_t k, int64_t N, int64_t ldx,
+                                const float* topk_w, const int32_t* src_to_row, const int32_t* row_to_src,
+                                const int32_t* offsets, int32_t E, int64_t M, void* rows, int64_t ldr, void* stream);
+fgg_status fgg_moe_permute_rows_backward(const void* drows, fgg_dtype dtype, int64_t M, int64_t lddr, const void* x,
+                                         int64_t ldx, const float* topk_w, const int32_t* src_to_row, int64_t T,
+                                         int32_t k, int64_t N, void* dx, int64_t lddx, float* dtopk_w, void* stream);
+fgg_status fgg_moe_unpermute_rows(const void* rows, fgg_dtype dtype, int64_t M, int64_t ldr, const float* topk_w,
+                                  const int32_t* src_to_row, int64_t T, int32_t k, int64_t N, void* out, int64_t ldo,
+                                  void* stream);
+fgg_status fgg_moe_unpermute_rows_backward(const void* dout, fgg_dtype dtype, int64_t T, int32_t k, int64_t N,
+                                           int64_t lddo, const void* rows, int64_t ldr, const float* topk_w,
+                                           const int32_t* src_to_row, const int32_t* row_to_src,
+                                           const int32_t* offsets, int32_t E, int64_t M, void* drows, int64_t lddr,
+                                           float* dtopk_w, void* stream);
+
+/*
+ * fgg_moe_gemv_fp4 — few tokens times 4-bit weights with group scales, the activations
+ * unquantized: the form of the experts' products for single tokens (no permute, no
+ * workspace, one launch).
+ *   y[t][j][n] = sum_K x[t(, j)][K] * code(b[e][n][K]) * 2^(b_scales[e][n][K/32] - 127),  e = topk_ids[t][j]
+ * accumulated in fp32 (the products are exact), then, per output form:
+ *   topk_w NULL, FGG_ACT_NONE:     out[t·k + j][n] = y[t][j][n]
+ *   topk_w NULL, FGG_ACT_SILU_MUL: b holds [gate | up] rows (2N of them):
+ *                                  out[t·k + j][n] = g / (1 + e^-g) * u,  g = y[t][j][n], u = y[t][j][N + n]
+ *   topk_w given (FGG_ACT_NONE):   out[t][n] = sum_j topk_w[t][j] * y[t][j][n]
+ * and rounded once to out_dtype (FGG_BF16 or FGG_F32; row stride ldo >= N).  A slot whose id is
+ * outside [0, G) has no expert: its output row is 0, and the sum skips it (its weight and x are
+ * not read).  An id may stand twice in a token.  topk_ids NULL: one set of weights for every
+ * token (G = 1, k = 1, topk_w NULL).
+ * x: fp32 or bf16, [T][ldx], or with x_per_slot != 0 [T·k][ldx] (row t·k + j for slot j);
+ * ldx >= K, any alignment of the element.  bq: {E2M1X2,E8M0,1,32} (b [G][N][K/2], b_scales
+ * [G][N][K/32], any N, K % 32 == 0) or {E2M1X2_TILED,E8M0,1,32} (from fgg_pack_fp4_weights:
+ * N % 16 == 0, K % 128 == 0), b 16-byte aligned.  Scale bytes up to 252 are exact (6 times a
+ * larger power of two is beyond the bf16 and fp32 range).
+ * Each expert that tokens 16i .. 16i + 15 name is read once for the 16 of them, so the call
+ * is meant for up to 16 tokens; more are taken 16 by 16.  No result depends on an order of
+ * arrival: the same call gives the same bits.  1 <= G <= 1024, 1 <= k <= 64, K >= 32;
+ * N, K <= 2^26, T <= 1048560.  T == 0 or N == 0 is a no-op.
+ */
+fgg_status fgg_moe_gemv_fp4(int32_t G, int64_t T, int32_t k, int64_t N, int64_t K, const void* x, fgg_dtype x_dtype,
+                            int64_t ldx, int32_t x_per_slot, const void* b, const void* b_scales, fgg_qdesc bq,
+                            const int32_t* topk_ids, const float* topk_w, fgg_act act, void* out,
+                            fgg_dtype out_dtype, int64_t ldo, void* stream);
 
 #ifdef __cplusplus
 }

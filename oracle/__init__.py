@@ -78,3 +78,13 @@ from .gemm import (  # noqa: F401
     w4a4_lowrank_gemm,
     mxfp4_lowrank_gemm,
 )
+from .routing import (  # noqa: F401
+    fp4_weights,
+    gate_weights,
+    moe_gemv_fp4,
+    moe_route,
+    moe_route_backward,
+    pair_dots,
+    rows_from_tokens,
+    tokens_from_rows,
+)

@@ -1,0 +1,187 @@
+"""GPU parity of the router and its gradient against the float64 oracle.
+
+Tolerances (fp32, u = 2^-24): a score is one exponential of a difference (the
+difference's rounding is worth |x - max| u relative, the exponential 2u), a sum
+of at most 16 + 6 roundings, a division and the scale: (64 + R) u with R the
+spread of the logits (at most 104, below which an fp32 exponential is 0).  The
+gradient multiplies two such scores and subtracts: twice that, relative to the
+sum of the magnitudes of its terms.  A bf16 result adds half a step, 2^-8."""
+
+import numpy as np
+import pytest
+import torch
+
+import fp4_grouped_gemm_amd as fgg
+import oracle
+import synth
+from _util import cuda, to_np
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+TINY = 2.0 ** -120
+
+
+def _logits(seed, T, E, dtype, shut=0.05, spread=2.0):
+    g = synth.rng(seed)
+    x = (g.standard_normal((T, E)) * spread).astype(np.float32)
+    if shut:
+        x[g.random((T, E)) < shut] = -np.inf
+        x[T // 2] = -np.inf                                # a token without any expert
+    if dtype == torch.bfloat16:
+        f = np.isfinite(x)
+        x[f] = synth.to_bf16_values(x)[f]
+    return x
+
+
+def _spread(x):
+    f = x[np.isfinite(x)]
+    return min(104.0, float(f.max() - f.min())) if f.size else 0.0
+
+
+def _check_weights(w, ref, x, what=""):
+    tol = (64 + _spread(x)) * U
+    assert np.all(np.abs(w - ref) <= tol * np.abs(ref) + TINY), (what, np.abs(w - ref).max())
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 256, 8), (3, 16, 16), (65, 17, 3), (9, 64, 64), (130, 33, 5),
+                                   (31, 160, 6), (7, 256, 1), (515, 256, 8), (5, 1000, 64), (2, 1024, 10)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("gate", ["softmax", "sigmoid"])
+def test_route(T, E, k, dtype, gate):
+    x = _logits(T + E, T, E, dtype)
+    bias = (synth.rng(E).standard_normal(E) * 0.1).astype(np.float32)
+    d = cuda(x, dtype)
+    for b in (None, bias):
+        for renorm, scale in ((False, 1.0), (True, 2.5)):
+            ids, w = fgg.moe_route(d, k, gate, bias=None if b is None else cuda(b), renormalize=renorm, scale=scale)
+            ref_ids, ref_w = oracle.moe_route(x, k, gate, b, renorm, scale)
+            assert np.array_equal(to_np(ids), ref_ids), (b is not None, renorm)
+            _check_weights(to_np(w), ref_w, x, (b is not None, renorm))
+
+
+def test_ties_go_to_the_lower_expert():
+    x = np.zeros((6, 200), np.float32)
+    x[1, ::2] = -0.0
+    x[2, 150:] = 1.0
+    x[3, [7, 71, 135, 199]] = 3.0                           # the same lane of four registers
+    x[4, [64, 1]] = 2.0
+    x[5] = -np.inf
+    x[5, [190, 5]] = -np.inf
+    for b in (None, np.zeros(200, np.float32)):
+        ids, _ = fgg.moe_route(cuda(x), 5, bias=None if b is None else cuda(b))
+        got = to_np(ids)
+        assert got[0].tolist() == got[1].tolist() == [0, 1, 2, 3, 4]
+        assert got[2].tolist() == [150, 151, 152, 153, 154]
+        assert got[3].tolist() == [7, 71, 135, 199, 0]
+        assert got[4].tolist() == [1, 64, 0, 2, 3]
+        assert got[5].tolist() == [-1] * 5
+
+
+def test_extreme_logits():
+    low, top = np.float32(-3e38), np.float32(3e38)
+    x = np.array([[low, low, 0, 0], [top, low, 0, 0], [-200, -201, -300, -250], [low, -np.inf, -np.inf, -np.inf],
+                  [90, 88, -90, 0]], np.float32)
+    for gate in ("softmax", "sigmoid"):
+        for renorm in (False, True):
+            ids, w = fgg.moe_route(cuda(x), 3, gate, renormalize=renorm)
+            ref_ids, ref_w = oracle.moe_route(x, 3, gate, None, renorm)
+            assert np.array_equal(to_np(ids), ref_ids)
+            _check_weights(to_np(w), ref_w, np.array([0.0, 104.0]), (gate, renorm))
+
+
+def test_nan_and_inf_logits():
+    x = np.array([[1, np.nan, 2, 0], [np.inf, 1, 2, 0], [np.nan] * 4, [1, 2, 3, 4]], np.float32)
+    for gate in ("softmax", "sigmoid"):
+        for bias in (None, cuda(np.array([0, 0, 0, 0.5], np.float32))):
+            ids, w = fgg.moe_route(cuda(x), 2, gate, bias=bias, renormalize=True)
+            ids, w = to_np(ids), to_np(w)
+            assert 1 not in ids[0] and (ids[0] >= 0).all() and np.isnan(w[0]).all()
+            assert ids[2].tolist() == [-1, -1] and (w[2] == 0).all()
+            assert ids[3].tolist() == [3, 2] and np.isfinite(w[3]).all()
+            assert ids[1, 0] == 0 or (gate == "softmax" and bias is not None)
+    # a closed or NaN bias closes the expert
+    b = np.array([0, -np.inf, np.nan, 0], np.float32)
+    ids, _ = fgg.moe_route(cuda(x[3:]), 4, "sigmoid", bias=cuda(b))
+    assert to_np(ids)[0].tolist() == [3, 0, -1, -1]
+
+
+def test_strided_logits_and_outputs_in_place():
+    x = _logits(3, 40, 60, torch.float32, shut=0)
+    big = torch.full((40, 77), float("nan"), device="cuda")
+    big[:, 5:65] = cuda(x)
+    ids = torch.full((40, 4), 99, dtype=torch.int32, device="cuda")
+    w = torch.full((40, 4), 99.0, device="cuda")
+    fgg.moe_route(big[:, 5:65], 4, ids=ids, weights=w)
+    ref_ids, ref_w = oracle.moe_route(x, 4)
+    assert np.array_equal(to_np(ids), ref_ids)
+    _check_weights(to_np(w), ref_w, x)
+    out = torch.full((40, 80), 7.0, device="cuda")
+    dw = torch.randn(40, 4, device="cuda")
+    fgg.moe_route_backward(big[:, 5:65], ids, dw, out=out[:, 3:63])
+    assert torch.equal(out[:, 3:63], fgg.moe_route_backward(cuda(x), ids, dw))
+    assert (out[:, :3] == 7).all() and (out[:, 63:] == 7).all()
+
+
+def _gradient_scale(x, ids, dw, gate, renorm, scale):
+    """Sum of the magnitudes of the gradient's terms."""
+    s = oracle.gate_weights(x, np.tile(np.arange(x.shape[1]), (x.shape[0], 1)), gate, False)
+    w = oracle.gate_weights(x, ids, gate, renorm)
+    u = np.abs(scale * dw) * (ids >= 0)
+    mean = (u * w).sum(1, keepdims=True)
+    out = np.zeros(x.shape)
+    for t in range(x.shape[0]):
+        for j, e in enumerate(ids[t]):
+            if e >= 0:
+                out[t, e] += (w[t, j] if renorm else s[t, e]) * (u[t, j] + (mean[t, 0] if renorm else 0))
+    return out + (s * mean if gate == "softmax" and not renorm else 0)
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 256, 8), (65, 17, 3), (9, 64, 64), (31, 160, 6), (70, 30, 4),
+                                   (257, 256, 8), (5, 1000, 64)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("gate", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_backward(T, E, k, dtype, gate, renorm):
+    x = _logits(T + 2 * E, T, E, dtype)
+    ids, _ = oracle.moe_route(x, k, gate)
+    if T > 3 and k > 1:
+        ids[0, 1] = ids[0, 0]                               # a repeated id
+        ids[1, 0] = E + 5                                   # and ids that are no expert's
+        ids[2, :] = -1
+    dw = synth.rng(T).standard_normal((T, k)).astype(np.float32)
+    got = to_np(fgg.moe_route_backward(cuda(x, dtype), cuda(ids), cuda(dw), gate, renorm, 1.5))
+    ids = np.where(ids >= E, -1, ids)
+    ref = oracle.moe_route_backward(x, ids, dw, gate, renorm, 1.5)
+    tol = 2 * (64 + _spread(x)) * U * _gradient_scale(x, ids, dw, gate, renorm, 1.5) + TINY
+    if dtype == torch.bfloat16:
+        tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref)
+    assert np.all(np.abs(got - ref) <= tol), (np.abs(got - ref) / tol).max()
+    assert np.all(got[np.isneginf(x)] == 0)
+
+
+def test_route_in_a_graph_and_on_another_stream():
+    x = cuda(_logits(9, 300, 128, torch.float32))
+    bias = torch.randn(128, device="cuda") * 0.1
+    want = fgg.moe_route(x, 6, "sigmoid", bias=bias, renormalize=True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = fgg.moe_route(x, 6, "sigmoid", bias=bias, renormalize=True)
+        grad = fgg.moe_route_backward(x, got[0], got[1], "sigmoid", True)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    held = x.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ids, w = fgg.moe_route(held, 6, "sigmoid", bias=bias, renormalize=True)
+        d = fgg.moe_route_backward(held, ids, w, "sigmoid", True)
+    for seed in range(3):
+        held.copy_(cuda(_logits(20 + seed, 300, 128, torch.float32)) if seed else x)
+        graph.replay()
+        torch.cuda.synchronize()
+        a, b = fgg.moe_route(held, 6, "sigmoid", bias=bias, renormalize=True)
+        assert torch.equal(a, ids) and torch.equal(b, w)
+        assert torch.equal(d, fgg.moe_route_backward(held, a, b, "sigmoid", True))
+        if seed == 0:
+            assert torch.equal(d, grad)
