@@ -23,6 +23,7 @@
 // occurrences; a token that names one expert twice has its second slot visited on its own.
 #include "fgg_device.hpp"
 #include "fgg_internal.hpp"
+#include "fgg_wave.hpp"
 
 namespace fgg {
 
@@ -65,26 +66,33 @@ __device__ inline bf16x8 dequant8(uint32_t codes, float scale) {
   return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// The 32 activations of a lane's K chunk: four operands of eight bf16 (per part).
-template <class TX>
+// Activations of one K block for up to NC tokens (4, 8 or 16).  The matrix instruction has 16
+// columns and a K block takes four of them (operand d: elements 8d .. 8d + 7 of each lane's 32).
+// With few tokens the columns hold several operands at once: column NC * i + t holds token t's
+// operand s * F + i of register set s (F = 16 / NC operands per set), so a K block takes NC / 4
+// 16-byte loads per lane instead of four.  Instruction d multiplies set d / F into accumulator
+// d % F, of which only columns NC * (d % F) + t mean anything: those are picked at the end.
+template <class TX, int NC>
 struct Frag;
-template <>
-struct Frag<uint16_t> {
-  u32x4 v[4];
+template <int NC>
+struct Frag<uint16_t, NC> {
+  static constexpr int F = 16 / NC;
+  u32x4 v[NC / 4];
   __device__ void load(const uint16_t* p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const u32x4_a2*>(p + 8 * i);
+    for (int s = 0; s < NC / 4; ++s) v[s] = *reinterpret_cast<const u32x4_a2*>(p + 8 * F * s);
   }
   __device__ void clear() {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = u32x4{0, 0, 0, 0};
+    for (int s = 0; s < NC / 4; ++s) v[s] = u32x4{0, 0, 0, 0};
   }
-  __device__ v4f mul(int i, bf16x8 a, v4f acc) const {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, v[i]), acc, 0, 0, 0);
+  __device__ void mul(int d, bf16x8 a, v4f (&acc)[F]) const {
+    acc[d % F] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, v[d / F]), acc[d % F], 0, 0, 0);
   }
 };
 template <>
-struct Frag<float> {
+struct Frag<float, 16> {
+  static constexpr int F = 1;
   u32x4 v[8];
   __device__ void load(const float* p) {
 #pragma unroll
@@ -95,7 +103,7 @@ struct Frag<float> {
     for (int i = 0; i < 8; ++i) v[i] = u32x4{0, 0, 0, 0};
   }
   // x = hi + mid + lo: the top 16 bits, then the top 16 bits of each exact remainder
-  __device__ v4f mul(int i, bf16x8 a, v4f acc) const {
+  __device__ void mul(int i, bf16x8 a, v4f (&acc)[1]) const {
     u32x4 part[3];
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
@@ -116,8 +124,7 @@ struct Frag<float> {
     }
 #pragma unroll
     for (int q = 2; q >= 0; --q)
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, part[q]), acc, 0, 0, 0);
-    return acc;
+      acc[0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, part[q]), acc[0], 0, 0, 0);
   }
 };
 
@@ -131,7 +138,33 @@ struct Items {
   uint16_t item[kMaxPairs];  // the pairs that stand for one visit each, in increasing order
   uint8_t again[kMaxPairs];  // the pair's expert is named by an earlier slot of its token
   int count[2 * kWaves];
+  uint16_t column[kWaves][16];   // each wave's visit: token + 16 * slot of each column in use
 };
+
+// The list of at most 64 pairs, by each wave on its own: lane p holds pair p and looks at the
+// pairs before it one by one.  Every wave writes the same values to LDS and reads only what it
+// wrote itself, so there is no barrier.
+__device__ inline int list_few_items(Items& L, const int32_t* ids, int64_t t0, int P, int k, int G) {
+  const int p = threadIdx.x & 63, t = p / k;
+  int e = p < P ? ids[t0 * k + p] : -1;
+  if (e < 0 || e >= G) e = -1;
+  int again = 0, covered = 0;
+  for (int q = 0; q + 1 < P; ++q) {
+    const int eq = __builtin_amdgcn_readlane(e, q), aq = __builtin_amdgcn_readlane(again, q);
+    if (p > q && e == eq) {
+      if (t == q / k) again = 1;
+      else if (!aq) covered = 1;
+    }
+  }
+  const bool lead = e >= 0 && (again || !covered);
+  const uint64_t m = __ballot(lead);
+  if (p < P) {
+    L.ids[p] = e;
+    L.again[p] = (uint8_t)again;
+    if (lead) L.item[__popcll(m & ((1ull << p) - 1))] = (uint16_t)p;
+  }
+  return __popcll(m);
+}
 
 // Builds the list for tokens [t0, t0 + Tn); returns the number of visits.  All threads call it.
 __device__ inline int list_items(Items& L, const int32_t* ids, int64_t t0, int Tn, int k, int G) {
@@ -183,90 +216,160 @@ __device__ inline int slot_of(const Items& L, int p0, int t, int Tn, int k) {
   return -1;
 }
 
-// One wave's share: K blocks [kb0, kb1) of NT row tiles of one expert, added to acc.
-// xrow: the lane's token row (null: no token in this column).
-template <class TX, bool TILED, int NT, int U>
-__device__ inline void gemv_run(const uint8_t* const (&wp)[NT], const uint8_t* const (&sp)[NT], const TX* xrow,
-                                int64_t K, int kb0, int kb1, v4f (&acc)[NT]) {
-  const int lane = threadIdx.x & 63, c = lane >> 4;
-  for (int kb = kb0; kb < kb1; kb += U) {
-    u32x4 q[U][NT];
-    uint32_t e[U][NT];
-    Frag<TX> f[U];
+// The weights of NT row tiles of one expert: wave-uniform pointers to each tile's first K block,
+// and this lane's offsets (row lane % 16, piece lane / 16) in a block of codes and of scales.
+template <int NT>
+struct Tiles {
+  const uint8_t* codes[NT];
+  const uint8_t* scales[NT];
+  uint32_t code_lane[NT], scale_lane[NT];
+};
+
+// n <= U K blocks from kb on of NT row tiles of one expert, added to acc: every load is issued
+// before the first is used, and none is conditional (a load under a branch is waited for at
+// the branch's end; past n the last block is read again).  LAST: the block that K ends in,
+// whose lanes past the end read the block's first piece and multiply it by zeros.
+template <class TX, bool TILED, int NT, int NC, int U, bool LAST>
+__device__ inline void gemv_step(const Tiles<NT>& w, const TX* xrow, int64_t K, int kb, int n,
+                                 v4f (&acc)[NT][Frag<TX, NC>::F]) {
+  const int c = (threadIdx.x & 63) >> 4;
+  const bool in = !LAST || (int64_t)kb * 128 + 32 * c < K;
+  const int back = in ? 0 : c;                       // pieces back to the block's first one
+  u32x4 q[U][NT];
+  uint32_t e[U][NT];
+  Frag<TX, NC> f[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool in = kb + u < kb1 && (int64_t)(kb + u) * 128 + 32 * c < K;
+  for (int u = 0; u < U; ++u) {
+    const int b = kb + (u < n ? u : n - 1);
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        q[u][i] = u32x4{0, 0, 0, 0};
-        e[u][i] = 127;
-        if (in) {
-          if constexpr (TILED) {
-            q[u][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wp[i] + (int64_t)(kb + u) * 1024));
-            e[u][i] = sp[i][(int64_t)((kb + u) >> 2) * 256 + 4 * ((kb + u) & 3)];
-          } else {
-            q[u][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wp[i] + (int64_t)(kb + u) * 64));
-            e[u][i] = sp[i][(int64_t)(kb + u) * 4];
-          }
-        }
-      }
-      if (in && xrow) f[u].load(xrow + (int64_t)(kb + u) * 128);
-      else f[u].clear();
+    for (int i = 0; i < NT; ++i) {
+      // (a block's codes and scales: uniform pointer + 32-bit lane offset)
+      const uint8_t* wb = w.codes[i] + (int64_t)b * (TILED ? 1024 : 64);
+      const uint8_t* sb = w.scales[i] + (TILED ? (int64_t)(b >> 2) * 256 + 4 * (b & 3) : (int64_t)b * 4);
+      q[u][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wb + (w.code_lane[TILED ? 0 : i] - 16u * back)));
+      e[u][i] = sb[w.scale_lane[TILED ? 0 : i] - (uint32_t)back];
     }
+    f[u].load(xrow + (int64_t)b * 128 - 32 * back);
+    if (LAST && !in) f[u].clear();
+  }
+  __builtin_amdgcn_sched_barrier(0);                 // keep the loads together, ahead of their uses
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+  for (int u = 0; u < U; ++u) {
+    if (u >= n) break;
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const float scale = __uint_as_float(e[u][i] << 23);
+    for (int i = 0; i < NT; ++i) {
+      const float scale = __uint_as_float(e[u][i] << 23);
 #pragma unroll
-        for (int d = 0; d < 4; ++d) acc[i] = f[u].mul(d, dequant8(q[u][i][d], scale), acc[i]);
-      }
+      for (int d = 0; d < 4; ++d) f[u].mul(d, dequant8(q[u][i][d], scale), acc[i]);
+    }
+  }
+}
+
+// One wave's share: K blocks [kb0, kb1); the sums of column t (t < NC) in the lanes of column t.
+// xrow: the lane's activations at operand col / NC (in a column without a token any: a column's
+// sums depend on its own activations only).
+template <class TX, bool TILED, int NT, int NC>
+__device__ inline void gemv_run(const Tiles<NT>& w, const TX* xrow, int64_t K, int kb0, int kb1, v4f (&sum)[NT]) {
+  constexpr int F = Frag<TX, NC>::F;
+  // blocks in flight: as many as about 64 registers of operands hold
+  constexpr int U = sizeof(TX) == 4 ? 2 : NC == 16 ? 2 : NT == 1 && NC == 4 ? 8 : 4;
+  v4f acc[NT][F];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int f = 0; f < F; ++f) acc[i][f] = v4f{0, 0, 0, 0};
+  const int whole = (int64_t)kb1 * 128 <= K ? kb1 : kb1 - 1;
+  int kb = kb0;
+  for (; kb + U <= whole; kb += U) gemv_step<TX, TILED, NT, NC, U, false>(w, xrow, K, kb, U, acc);
+  const int left = whole - kb;
+  if (U > 2 && left > U / 2) gemv_step<TX, TILED, NT, NC, U, false>(w, xrow, K, kb, left, acc);
+  else if (left > 0) gemv_step<TX, TILED, NT, NC, (U + 1) / 2, false>(w, xrow, K, kb, left, acc);
+  if (!TILED && whole < kb1) gemv_step<TX, TILED, NT, NC, 1, true>(w, xrow, K, whole, 1, acc);
+  // column NC * f + t of accumulator f: pick, then add the F columns of each token
+  const int mine = (threadIdx.x & 15) / NC;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    v4f v = acc[i][0];
+#pragma unroll
+    for (int f = 1; f < F; ++f)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = mine == f ? acc[i][f][r] : v[r];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if constexpr (F >= 2) v[r] += dpp_move<0x128>(v[r]);   // 8 columns round
+      if constexpr (F >= 4) v[r] += dpp_move<0x124>(v[r]);   // 4 columns round
+    }
+    sum[i] = v;
   }
 }
 
 }  // namespace
 
 template <int MODE, bool TILED, class TX, class TO, int RT>
-__global__ void __launch_bounds__(64 * kWaves) gemv_fp4_kernel(GemvArgs a) {
+__global__ void __launch_bounds__(64 * kWaves, 4) gemv_fp4_kernel(GemvArgs a) {
   constexpr int NT = MODE == kSilu ? 2 * RT : RT;    // row tiles: RT of gate, then RT of up
-  constexpr int U = sizeof(TX) == 2 ? 4 : 2;
   __shared__ Items L;
   __shared__ float part[kWaves][NT][16][16];         // [wave][tile][token][row]
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, c = lane >> 4;
   const int64_t n0 = (int64_t)blockIdx.x * 16 * RT;
   const int64_t t0 = (int64_t)blockIdx.z * 16;
   const int Tn = a.T - t0 < 16 ? (int)(a.T - t0) : 16;
-  const int64_t width = MODE == kSilu ? 2 * a.N : a.N, nkb = (a.K + 127) / 128;
+  const int64_t width = MODE == kSilu ? 2 * a.N : a.N;
+  const int nkb = (int)((a.K + 127) / 128);
   const TX* x = (const TX*)a.x;
   TO* out = (TO*)a.out;
 
-  const int items = a.ids ? list_items(L, a.ids, t0, Tn, a.k, a.G) : 1;
+  const int items = !a.ids              ? 1
+                    : Tn * a.k <= 64 ? list_few_items(L, a.ids, t0, Tn * a.k, a.k, a.G)
+                                     : list_items(L, a.ids, t0, Tn, a.k, a.G);
 
-  // weight and scale pointers of this lane in row tile i of expert e
-  const uint8_t* wp[NT];
-  const uint8_t* sp[NT];
-  auto at_expert = [&](int e) {
+  // The tokens of visit p0, one a column: returns their number, and in L.column[wave] which.
+  auto columns = [&](int p0) -> int {
+    if (!a.ids) {
+      if (lane < 16) L.column[wave][lane] = (uint16_t)(lane < Tn ? lane : 0);
+      return Tn;
+    }
+    const int j = slot_of(L, p0, col, Tn, a.k);
+    const uint32_t m = (uint32_t)__ballot(lane < 16 && j >= 0);
+    if (lane < 16 && j >= 0) L.column[wave][__popc(m & ((1u << lane) - 1))] = (uint16_t)(lane + 16 * j);
+    return __popc(m);
+  };
+  // K blocks [kb0, kb1) of expert e for the nc tokens of L.column[wave], into sum (column t: the t-th)
+  auto visit = [&](int e, int nc, int kb0, int kb1, v4f (&sum)[NT]) {
+    Tiles<NT> w;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const int64_t r0 = n0 + 16 * (i % RT);
+      const int64_t up = i >= RT ? a.N : 0, r0 = n0 + 16 * (i % RT);
       if constexpr (TILED) {
-        const int64_t last = a.N / 16 - 1;
-        int64_t nb = r0 / 16 < last ? r0 / 16 : last;
-        if (i >= RT) nb += a.N / 16;
-        wp[i] = a.b + ((int64_t)e * (width / 16) + nb) * (a.K / 128) * 1024 + 16 * lane;
-        sp[i] = a.s + ((int64_t)e * (width / 16) + nb) * ((a.K + 511) / 512) * 256 + 16 * col + c;
+        const int64_t last = a.N / 16 - 1, nb = (r0 / 16 < last ? r0 / 16 : last) + up / 16;
+        w.codes[i] = uniform_ptr(a.b + ((int64_t)e * (width / 16) + nb) * (a.K / 128) * 1024);
+        w.scales[i] = uniform_ptr(a.s + ((int64_t)e * (width / 16) + nb) * ((a.K + 511) / 512) * 256);
+        w.code_lane[i] = 16 * lane;
+        w.scale_lane[i] = 16 * col + c;
       } else {
-        int64_t n = r0 + col < a.N ? r0 + col : a.N - 1;   // rows past the end: any row, not stored
-        if (i >= RT) n += a.N;
-        wp[i] = a.b + ((int64_t)e * width + n) * (a.K / 2) + 16 * c;
-        sp[i] = a.s + ((int64_t)e * width + n) * (a.K / 32) + c;
+        const int64_t last = a.N - 1, base = r0 < last ? r0 : last;
+        const uint32_t row = (uint32_t)(r0 + col < last ? r0 + col - base : last - base);   // past the end: not stored
+        w.codes[i] = uniform_ptr(a.b + ((int64_t)e * width + up + base) * (a.K / 2));
+        w.scales[i] = uniform_ptr(a.s + ((int64_t)e * width + up + base) * (a.K / 32));
+        w.code_lane[i] = row * (uint32_t)(a.K / 2) + 16 * c;
+        w.scale_lane[i] = row * (uint32_t)(a.K / 32) + c;
       }
     }
-  };
-  auto row_of = [&](int j) -> const TX* {
-    if (j < 0) return nullptr;
-    return x + (a.per_slot ? (t0 + col) * a.k + j : t0 + col) * a.ldx + 32 * c;
+    auto go = [&](auto n) {
+      constexpr int NC = decltype(n)::value;
+      const int t = col % NC;
+      const int tj = L.column[wave][t < nc ? t : 0];
+      const int64_t row = a.per_slot ? (t0 + (tj & 15)) * a.k + (tj >> 4) : t0 + (tj & 15);
+      gemv_run<TX, TILED, NT, NC>(w, x + row * a.ldx + 32 * c + 8 * (col / NC), a.K, kb0, kb1, sum);
+    };
+    if constexpr (sizeof(TX) == 4) {
+      go(std::integral_constant<int, 16>());
+    } else {
+      if (nc <= 4) go(std::integral_constant<int, 4>());
+      else if (nc <= 8) go(std::integral_constant<int, 8>());
+      else go(std::integral_constant<int, 16>());
+    }
   };
   // the sum over the waves of one value, in wave order
   auto joined = [&](int i, int t, int r) {
@@ -275,38 +378,34 @@ __global__ void __launch_bounds__(64 * kWaves) gemv_fp4_kernel(GemvArgs a) {
     for (int q = 1; q < kWaves; ++q) v += part[q][i][t][r];
     return v;
   };
-  auto publish = [&](const v4f (&acc)[NT]) {
-#pragma unroll
-    for (int i = 0; i < NT; ++i) *reinterpret_cast<v4f*>(&part[wave][i][col][4 * c]) = acc[i];
-  };
 
   if constexpr (MODE == kSum) {
-    // the waves split the K blocks of all visits, expert by expert
+    // the waves split the K blocks of all visits, expert by expert, and keep their own sums in LDS
+#pragma unroll
+    for (int i = 0; i < NT; ++i) *reinterpret_cast<v4f*>(&part[wave][i][col][4 * c]) = v4f{0, 0, 0, 0};
     const int64_t units = (int64_t)items * nkb;
     int64_t at = units * wave / kWaves;
     const int64_t end = units * (wave + 1) / kWaves;
-    v4f total[NT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) total[i] = v4f{0, 0, 0, 0};
     while (at < end) {
-      const int it = (int)(at / nkb), kb0 = (int)(at - it * nkb);
-      const int kb1 = (int)(end - it * nkb < nkb ? end - it * nkb : nkb);
-      const int p0 = L.item[it], j = slot_of(L, p0, col, Tn, a.k);
-      v4f acc[NT];
+      const int it = (int)(at / nkb), kb0 = (int)(at - (int64_t)it * nkb);
+      const int kb1 = (int)(end - (int64_t)it * nkb < nkb ? end - (int64_t)it * nkb : nkb);
+      const int p0 = __builtin_amdgcn_readfirstlane(L.item[it]), nc = columns(p0);
+      v4f sum[NT];
+      visit(__builtin_amdgcn_readfirstlane(L.ids[p0]), nc, kb0, kb1, sum);
+      if (col < nc) {
+        const int tj = L.column[wave][col], t = tj & 15;
+        const float g = a.w[(t0 + t) * a.k + (tj >> 4)];
 #pragma unroll
-      for (int i = 0; i < NT; ++i) acc[i] = v4f{0, 0, 0, 0};
-      at_expert(L.ids[p0]);
-      gemv_run<TX, TILED, NT, U>(wp, sp, row_of(j), a.K, kb0, kb1, acc);
-      if (j >= 0) {
-        const float g = a.w[(t0 + col) * a.k + j];
+        for (int i = 0; i < NT; ++i) {
+          v4f* p = reinterpret_cast<v4f*>(&part[wave][i][t][4 * c]);
+          v4f v = *p;
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) total[i][r] = fmaf(g, acc[i][r], total[i][r]);
+          for (int r = 0; r < 4; ++r) v[r] = fmaf(g, sum[i][r], v[r]);
+          *p = v;
+        }
       }
       at += kb1 - kb0;
     }
-    publish(total);
     __syncthreads();
     for (int i = tid; i < RT * 256; i += 64 * kWaves) {
       const int t = (i >> 4) & 15, r = i & 15;
@@ -314,30 +413,22 @@ __global__ void __launch_bounds__(64 * kWaves) gemv_fp4_kernel(GemvArgs a) {
       if (t < Tn && n < a.N) put(out + (t0 + t) * a.ldo + n, joined(i >> 8, t, r));
     }
   } else {
-    const int kb0 = (int)(nkb * wave / kWaves), kb1 = (int)(nkb * (wave + 1) / kWaves);
+    const int kb0 = (int)((int64_t)nkb * wave / kWaves), kb1 = (int)((int64_t)nkb * (wave + 1) / kWaves);
     for (int it = blockIdx.y; it < items; it += gridDim.y) {
-      int j, p0 = 0;
-      if (a.ids) {
-        p0 = L.item[it];
-        j = slot_of(L, p0, col, Tn, a.k);
-      } else {
-        j = col < Tn ? 0 : -1;
-      }
-      v4f acc[NT];
+      const int p0 = a.ids ? __builtin_amdgcn_readfirstlane(L.item[it]) : 0, nc = columns(p0);
+      v4f sum[NT];
+      visit(a.ids ? __builtin_amdgcn_readfirstlane(L.ids[p0]) : 0, nc, kb0, kb1, sum);
 #pragma unroll
-      for (int i = 0; i < NT; ++i) acc[i] = v4f{0, 0, 0, 0};
-      at_expert(a.ids ? L.ids[p0] : 0);
-      gemv_run<TX, TILED, NT, U>(wp, sp, row_of(j), a.K, kb0, kb1, acc);
-      publish(acc);
+      for (int i = 0; i < NT; ++i) *reinterpret_cast<v4f*>(&part[wave][i][col][4 * c]) = sum[i];
       __syncthreads();
       for (int i = tid; i < RT * 256; i += 64 * kWaves) {
         const int t = (i >> 4) & 15, r = i & 15;
         const int64_t n = n0 + 16 * (i >> 8) + r;
-        const int jt = a.ids ? slot_of(L, p0, t, Tn, a.k) : (t < Tn ? 0 : -1);
-        if (jt < 0 || n >= a.N) continue;
+        if (t >= nc || n >= a.N) continue;
         float v = joined(i >> 8, t, r);
         if constexpr (MODE == kSilu) v = v / (1.0f + expf(-v)) * joined(RT + (i >> 8), t, r);
-        put(out + ((t0 + t) * a.k + jt) * a.ldo + n, v);
+        const int tj = L.column[wave][t];
+        put(out + ((t0 + (tj & 15)) * a.k + (tj >> 4)) * a.ldo + n, v);
       }
       __syncthreads();
     }
