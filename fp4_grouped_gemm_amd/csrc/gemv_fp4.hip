@@ -30,12 +30,13 @@ namespace fgg {
 namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_a1 __attribute__((aligned(1)));
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kWaves = 8;
+constexpr int kMaxWaves = 8;
 constexpr int kMaxPairs = 1024;    // 16 tokens x 64 slots
 constexpr int kMaxGroups = 1024;
 
@@ -54,6 +55,7 @@ struct GemvArgs {
   const int32_t* ids;    // null: one set of weights, every token
   const float* w;
   void* out;
+  int out_bf16;
   int64_t ldo;
 };
 
@@ -128,8 +130,10 @@ struct Frag<float, 16> {
   }
 };
 
-__device__ inline void put(uint16_t* p, float v) { *p = bf16_bits_rne(v); }
-__device__ inline void put(float* p, float v) { *p = v; }
+__device__ inline void put(void* out, bool bf16, int64_t i, float v) {
+  if (bf16) ((uint16_t*)out)[i] = bf16_bits_rne(v);
+  else ((float*)out)[i] = v;
+}
 
 // Which experts a workgroup visits for its tokens.
 struct Items {
@@ -137,8 +141,8 @@ struct Items {
   int first[kMaxGroups];     // lowest pair that names the expert (as a first occurrence in its token)
   uint16_t item[kMaxPairs];  // the pairs that stand for one visit each, in increasing order
   uint8_t again[kMaxPairs];  // the pair's expert is named by an earlier slot of its token
-  int count[2 * kWaves];
-  uint16_t column[kWaves][16];   // each wave's visit: token + 16 * slot of each column in use
+  int count[kMaxWaves];
+  uint16_t column[kMaxWaves][16];   // each wave's visit: token + 16 * slot of each column in use
 };
 
 // The list of at most 64 pairs, by each wave on its own: lane p holds pair p and looks at the
@@ -168,14 +172,14 @@ __device__ inline int list_few_items(Items& L, const int32_t* ids, int64_t t0, i
 
 // Builds the list for tokens [t0, t0 + Tn); returns the number of visits.  All threads call it.
 __device__ inline int list_items(Items& L, const int32_t* ids, int64_t t0, int Tn, int k, int G) {
-  const int tid = threadIdx.x, P = Tn * k;
-  for (int i = tid; i < G; i += 64 * kWaves) L.first[i] = 0x7FFFFFFF;
-  for (int p = tid; p < P; p += 64 * kWaves) {
+  const int tid = threadIdx.x, P = Tn * k, threads = blockDim.x;
+  for (int i = tid; i < G; i += threads) L.first[i] = 0x7FFFFFFF;
+  for (int p = tid; p < P; p += threads) {
     const int e = ids[t0 * k + p];
     L.ids[p] = (e >= 0 && e < G) ? e : -1;
   }
   __syncthreads();
-  for (int p = tid; p < P; p += 64 * kWaves) {
+  for (int p = tid; p < P; p += threads) {
     const int e = L.ids[p];
     bool again = false;
     for (int q = p / k * k; q < p; ++q) again |= L.ids[q] == e;
@@ -183,27 +187,22 @@ __device__ inline int list_items(Items& L, const int32_t* ids, int64_t t0, int T
     if (e >= 0 && !again) atomicMin(&L.first[e], p);
   }
   __syncthreads();
-  bool lead[2];
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const int p = c * 64 * kWaves + tid;
-    const int e = p < P ? L.ids[p] : -1;
-    lead[c] = e >= 0 && (L.again[p] || L.first[e] == p);
-    const uint64_t m = __ballot(lead[c]);
-    if ((tid & 63) == 0) L.count[c * kWaves + (tid >> 6)] = __popcll(m);
-  }
-  __syncthreads();
   int total = 0;
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const uint64_t m = __ballot(lead[c]);
-    int before = 0;
-    for (int i = 0; i < c * kWaves + (tid >> 6); ++i) before += L.count[i];
-    if (lead[c]) L.item[before + __popcll(m & ((1ull << (tid & 63)) - 1))] = (uint16_t)(c * 64 * kWaves + tid);
+  for (int p0 = 0; p0 < P; p0 += threads) {
+    const int p = p0 + tid, e = p < P ? L.ids[p] : -1;
+    const bool lead = e >= 0 && (L.again[p] || L.first[e] == p);
+    const uint64_t m = __ballot(lead);
+    if ((tid & 63) == 0) L.count[tid >> 6] = __popcll(m);
+    __syncthreads();
+    int before = total;
+    for (int i = 0; i < threads >> 6; ++i) {
+      if (i < tid >> 6) before += L.count[i];
+      total += L.count[i];
+    }
+    if (lead) L.item[before + __popcll(m & ((1ull << (tid & 63)) - 1))] = (uint16_t)p;
+    __syncthreads();
   }
-  for (int i = 0; i < 2 * kWaves; ++i) total += L.count[i];
-  __syncthreads();
-  return total;
+  return __builtin_amdgcn_readfirstlane(total);
 }
 
 // The slot of token `t` (of the workgroup's) that visit `p0` serves, -1: none.
@@ -227,16 +226,17 @@ struct Tiles {
 
 // n <= U K blocks from kb on of NT row tiles of one expert, added to acc: every load is issued
 // before the first is used, and none is conditional (a load under a branch is waited for at
-// the branch's end; past n the last block is read again).  LAST: the block that K ends in,
-// whose lanes past the end read the block's first piece and multiply it by zeros.
-template <class TX, bool TILED, int NT, int NC, int U, bool LAST>
+// the branch's end; past n the last block is read again).  WIDE (kb a multiple of 4): a row's 16
+// scale bytes of four blocks in one load; a byte per block otherwise.  LAST: the block that K ends
+// in, whose lanes past the end read the block's first piece and multiply it by zeros.
+template <class TX, bool TILED, int NT, int NC, int U, bool WIDE, bool LAST>
 __device__ inline void gemv_step(const Tiles<NT>& w, const TX* xrow, int64_t K, int kb, int n,
                                  v4f (&acc)[NT][Frag<TX, NC>::F]) {
   const int c = (threadIdx.x & 63) >> 4;
   const bool in = !LAST || (int64_t)kb * 128 + 32 * c < K;
   const int back = in ? 0 : c;                       // pieces back to the block's first one
-  u32x4 q[U][NT];
-  uint32_t e[U][NT];
+  u32x4 q[U][NT], wide[WIDE ? U / 4 : 1][NT];
+  uint32_t e[WIDE ? 1 : U][NT];
   Frag<TX, NC> f[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -245,9 +245,14 @@ __device__ inline void gemv_step(const Tiles<NT>& w, const TX* xrow, int64_t K, 
     for (int i = 0; i < NT; ++i) {
       // (a block's codes and scales: uniform pointer + 32-bit lane offset)
       const uint8_t* wb = w.codes[i] + (int64_t)b * (TILED ? 1024 : 64);
-      const uint8_t* sb = w.scales[i] + (TILED ? (int64_t)(b >> 2) * 256 + 4 * (b & 3) : (int64_t)b * 4);
       q[u][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wb + (w.code_lane[TILED ? 0 : i] - 16u * back)));
-      e[u][i] = sb[w.scale_lane[TILED ? 0 : i] - (uint32_t)back];
+      if constexpr (!WIDE) {
+        const uint8_t* sb = w.scales[i] + (TILED ? (int64_t)(b >> 2) * 256 + 4 * (b & 3) : (int64_t)b * 4);
+        e[u][i] = sb[w.scale_lane[TILED ? 0 : i] + (uint32_t)(c - back)];
+      } else if (u % 4 == 0) {
+        const uint8_t* sb = w.scales[i] + (int64_t)(b >> 2) * (TILED ? 256 : 16);
+        wide[u / 4][i] = *reinterpret_cast<const u32x4_a1*>(sb + w.scale_lane[TILED ? 0 : i]);
+      }
     }
     f[u].load(xrow + (int64_t)b * 128 - 32 * back);
     if (LAST && !in) f[u].clear();
@@ -258,21 +263,23 @@ __device__ inline void gemv_step(const Tiles<NT>& w, const TX* xrow, int64_t K, 
     if (u >= n) break;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const float scale = __uint_as_float(e[u][i] << 23);
+      const uint32_t byte = WIDE ? (wide[WIDE ? u / 4 : 0][i][u % 4] >> (8 * c)) & 0xFFu : e[WIDE ? 0 : u][i];
+      const float scale = __uint_as_float(byte << 23);
 #pragma unroll
       for (int d = 0; d < 4; ++d) f[u].mul(d, dequant8(q[u][i][d], scale), acc[i]);
     }
+    __builtin_amdgcn_sched_barrier(0);               // and the converted codes of one block at a time
   }
 }
 
-// One wave's share: K blocks [kb0, kb1); the sums of column t (t < NC) in the lanes of column t.
-// xrow: the lane's activations at operand col / NC (in a column without a token any: a column's
-// sums depend on its own activations only).
+// One wave's share: K blocks [kb0, kb1), kb0 a multiple of 4; the sums of column t (t < NC) in the
+// lanes of column t.  xrow: the lane's activations at operand col / NC (in a column without a token
+// any: a column's sums depend on its own activations only).
 template <class TX, bool TILED, int NT, int NC>
 __device__ inline void gemv_run(const Tiles<NT>& w, const TX* xrow, int64_t K, int kb0, int kb1, v4f (&sum)[NT]) {
   constexpr int F = Frag<TX, NC>::F;
-  // blocks in flight: as many as about 64 registers of operands hold
-  constexpr int U = sizeof(TX) == 4 ? 2 : NC == 16 ? 2 : NT == 1 && NC == 4 ? 8 : 4;
+  // blocks in flight: as many as about 70 registers of operands hold
+  constexpr int U = sizeof(TX) == 4 ? (NT == 1 ? 2 : 1) : NT == 1 ? (NC == 4 ? 8 : 4) : NC == 16 ? 2 : 4;
   v4f acc[NT][F];
 #pragma unroll
   for (int i = 0; i < NT; ++i)
@@ -280,11 +287,18 @@ __device__ inline void gemv_run(const Tiles<NT>& w, const TX* xrow, int64_t K, i
     for (int f = 0; f < F; ++f) acc[i][f] = v4f{0, 0, 0, 0};
   const int whole = (int64_t)kb1 * 128 <= K ? kb1 : kb1 - 1;
   int kb = kb0;
-  for (; kb + U <= whole; kb += U) gemv_step<TX, TILED, NT, NC, U, false>(w, xrow, K, kb, U, acc);
-  const int left = whole - kb;
-  if (U > 2 && left > U / 2) gemv_step<TX, TILED, NT, NC, U, false>(w, xrow, K, kb, left, acc);
-  else if (left > 0) gemv_step<TX, TILED, NT, NC, (U + 1) / 2, false>(w, xrow, K, kb, left, acc);
-  if (!TILED && whole < kb1) gemv_step<TX, TILED, NT, NC, 1, true>(w, xrow, K, whole, 1, acc);
+  if constexpr (U >= 4) {
+    for (; kb + U <= whole; kb += U) gemv_step<TX, TILED, NT, NC, U, true, false>(w, xrow, K, kb, U, acc);
+    if constexpr (U == 8) {
+      if (kb + 4 <= whole) gemv_step<TX, TILED, NT, NC, 4, true, false>(w, xrow, K, kb, 4, acc), kb += 4;
+    }
+    // one to three blocks of a span of four (a plain row has no bytes behind it, a tiled one is padded)
+    if (kb < whole) gemv_step<TX, TILED, NT, NC, 4, TILED, false>(w, xrow, K, kb, whole - kb, acc);
+  } else {
+    for (; kb + U <= whole; kb += U) gemv_step<TX, TILED, NT, NC, U, false, false>(w, xrow, K, kb, U, acc);
+    if (U == 2 && kb < whole) gemv_step<TX, TILED, NT, NC, 1, false, false>(w, xrow, K, kb, 1, acc);
+  }
+  if (!TILED && whole < kb1) gemv_step<TX, TILED, NT, NC, 1, false, true>(w, xrow, K, whole, 1, acc);
   // column NC * f + t of accumulator f: pick, then add the F columns of each token
   const int mine = (threadIdx.x & 15) / NC;
 #pragma unroll
@@ -305,20 +319,21 @@ __device__ inline void gemv_run(const Tiles<NT>& w, const TX* xrow, int64_t K, i
 
 }  // namespace
 
-template <int MODE, bool TILED, class TX, class TO, int RT>
-__global__ void __launch_bounds__(64 * kWaves, 4) gemv_fp4_kernel(GemvArgs a) {
-  constexpr int NT = MODE == kSilu ? 2 * RT : RT;    // row tiles: RT of gate, then RT of up
+template <int MODE, bool TILED, class TX, int NCMAX>
+__global__ void __launch_bounds__(64 * kMaxWaves, 4) gemv_fp4_kernel(GemvArgs a) {
+  constexpr int NT = MODE == kSilu ? 2 : 1;          // row tiles: one, or gate and up
   __shared__ Items L;
-  __shared__ float part[kWaves][NT][16][16];         // [wave][tile][token][row]
+  __shared__ float part[kMaxWaves][NT][16][16];      // [wave][tile][token][row]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, c = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * 16 * RT;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
   const int64_t t0 = (int64_t)blockIdx.z * 16;
   const int Tn = a.T - t0 < 16 ? (int)(a.T - t0) : 16;
   const int64_t width = MODE == kSilu ? 2 * a.N : a.N;
-  const int nkb = (int)((a.K + 127) / 128);
+  // the waves share the K blocks in spans of four
+  const int nkb = (int)((a.K + 127) / 128), spans = (nkb + 3) / 4, waves = blockDim.x >> 6;
   const TX* x = (const TX*)a.x;
-  TO* out = (TO*)a.out;
+  const bool obf = a.out_bf16;
 
   const int items = !a.ids              ? 1
                     : Tn * a.k <= 64 ? list_few_items(L, a.ids, t0, Tn * a.k, a.k, a.G)
@@ -340,20 +355,20 @@ __global__ void __launch_bounds__(64 * kWaves, 4) gemv_fp4_kernel(GemvArgs a) {
     Tiles<NT> w;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const int64_t up = i >= RT ? a.N : 0, r0 = n0 + 16 * (i % RT);
+      const int64_t up = i ? a.N : 0;
       if constexpr (TILED) {
-        const int64_t last = a.N / 16 - 1, nb = (r0 / 16 < last ? r0 / 16 : last) + up / 16;
+        const int64_t last = a.N / 16 - 1, nb = (n0 / 16 < last ? n0 / 16 : last) + up / 16;
         w.codes[i] = uniform_ptr(a.b + ((int64_t)e * (width / 16) + nb) * (a.K / 128) * 1024);
         w.scales[i] = uniform_ptr(a.s + ((int64_t)e * (width / 16) + nb) * ((a.K + 511) / 512) * 256);
         w.code_lane[i] = 16 * lane;
-        w.scale_lane[i] = 16 * col + c;
+        w.scale_lane[i] = 16 * col;
       } else {
-        const int64_t last = a.N - 1, base = r0 < last ? r0 : last;
-        const uint32_t row = (uint32_t)(r0 + col < last ? r0 + col - base : last - base);   // past the end: not stored
+        const int64_t last = a.N - 1, base = n0 < last ? n0 : last;
+        const uint32_t row = (uint32_t)(n0 + col < last ? n0 + col - base : last - base);   // past the end: not stored
         w.codes[i] = uniform_ptr(a.b + ((int64_t)e * width + up + base) * (a.K / 2));
         w.scales[i] = uniform_ptr(a.s + ((int64_t)e * width + up + base) * (a.K / 32));
         w.code_lane[i] = row * (uint32_t)(a.K / 2) + 16 * c;
-        w.scale_lane[i] = row * (uint32_t)(a.K / 32) + c;
+        w.scale_lane[i] = row * (uint32_t)(a.K / 32);
       }
     }
     auto go = [&](auto n) {
@@ -366,7 +381,7 @@ __global__ void __launch_bounds__(64 * kWaves, 4) gemv_fp4_kernel(GemvArgs a) {
     if constexpr (sizeof(TX) == 4) {
       go(std::integral_constant<int, 16>());
     } else {
-      if (nc <= 4) go(std::integral_constant<int, 4>());
+      if (NCMAX == 4 || nc <= 4) go(std::integral_constant<int, 4>());
       else if (nc <= 8) go(std::integral_constant<int, 8>());
       else go(std::integral_constant<int, 16>());
     }
@@ -374,8 +389,7 @@ __global__ void __launch_bounds__(64 * kWaves, 4) gemv_fp4_kernel(GemvArgs a) {
   // the sum over the waves of one value, in wave order
   auto joined = [&](int i, int t, int r) {
     float v = part[0][i][t][r];
-#pragma unroll
-    for (int q = 1; q < kWaves; ++q) v += part[q][i][t][r];
+    for (int q = 1; q < waves; ++q) v += part[q][i][t][r];
     return v;
   };
 
@@ -383,18 +397,18 @@ __global__ void __launch_bounds__(64 * kWaves, 4) gemv_fp4_kernel(GemvArgs a) {
     // the waves split the K blocks of all visits, expert by expert, and keep their own sums in LDS
 #pragma unroll
     for (int i = 0; i < NT; ++i) *reinterpret_cast<v4f*>(&part[wave][i][col][4 * c]) = v4f{0, 0, 0, 0};
-    const int64_t units = (int64_t)items * nkb;
-    int64_t at = units * wave / kWaves;
-    const int64_t end = units * (wave + 1) / kWaves;
+    const int64_t units = (int64_t)items * spans;
+    int64_t at = units * wave / waves;
+    const int64_t end = units * (wave + 1) / waves;
     while (at < end) {
-      const int it = (int)(at / nkb), kb0 = (int)(at - (int64_t)it * nkb);
-      const int kb1 = (int)(end - (int64_t)it * nkb < nkb ? end - (int64_t)it * nkb : nkb);
+      const int it = (int)(at / spans), s0 = (int)(at - (int64_t)it * spans);
+      const int s1 = (int)(end - (int64_t)it * spans < spans ? end - (int64_t)it * spans : spans);
       const int p0 = __builtin_amdgcn_readfirstlane(L.item[it]), nc = columns(p0);
+      const int tj = L.column[wave][col < nc ? col : 0], t = tj & 15;
+      const float g = a.w[(t0 + t) * a.k + (tj >> 4)];
       v4f sum[NT];
-      visit(__builtin_amdgcn_readfirstlane(L.ids[p0]), nc, kb0, kb1, sum);
+      visit(__builtin_amdgcn_readfirstlane(L.ids[p0]), nc, 4 * s0, 4 * s1 < nkb ? 4 * s1 : nkb, sum);
       if (col < nc) {
-        const int tj = L.column[wave][col], t = tj & 15;
-        const float g = a.w[(t0 + t) * a.k + (tj >> 4)];
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
           v4f* p = reinterpret_cast<v4f*>(&part[wave][i][t][4 * c]);
@@ -404,16 +418,16 @@ __global__ void __launch_bounds__(64 * kWaves, 4) gemv_fp4_kernel(GemvArgs a) {
           *p = v;
         }
       }
-      at += kb1 - kb0;
+      at += s1 - s0;
     }
     __syncthreads();
-    for (int i = tid; i < RT * 256; i += 64 * kWaves) {
-      const int t = (i >> 4) & 15, r = i & 15;
-      const int64_t n = n0 + 16 * (i >> 8) + r;
-      if (t < Tn && n < a.N) put(out + (t0 + t) * a.ldo + n, joined(i >> 8, t, r));
+    for (int i = tid; i < 256; i += blockDim.x) {
+      const int t = i >> 4, r = i & 15;
+      if (t < Tn && n0 + r < a.N) put(a.out, obf, (t0 + t) * a.ldo + n0 + r, joined(0, t, r));
     }
   } else {
-    const int kb0 = (int)((int64_t)nkb * wave / kWaves), kb1 = (int)((int64_t)nkb * (wave + 1) / kWaves);
+    const int kb0 = 4 * (int)((int64_t)spans * wave / waves), end = 4 * (int)((int64_t)spans * (wave + 1) / waves);
+    const int kb1 = end < nkb ? end : nkb;
     for (int it = blockIdx.y; it < items; it += gridDim.y) {
       const int p0 = a.ids ? __builtin_amdgcn_readfirstlane(L.item[it]) : 0, nc = columns(p0);
       v4f sum[NT];
@@ -421,64 +435,61 @@ __global__ void __launch_bounds__(64 * kWaves, 4) gemv_fp4_kernel(GemvArgs a) {
 #pragma unroll
       for (int i = 0; i < NT; ++i) *reinterpret_cast<v4f*>(&part[wave][i][col][4 * c]) = sum[i];
       __syncthreads();
-      for (int i = tid; i < RT * 256; i += 64 * kWaves) {
-        const int t = (i >> 4) & 15, r = i & 15;
-        const int64_t n = n0 + 16 * (i >> 8) + r;
-        if (t >= nc || n >= a.N) continue;
-        float v = joined(i >> 8, t, r);
-        if constexpr (MODE == kSilu) v = v / (1.0f + expf(-v)) * joined(RT + (i >> 8), t, r);
+      for (int i = tid; i < 256; i += blockDim.x) {
+        const int t = i >> 4, r = i & 15;
+        if (t >= nc || n0 + r >= a.N) continue;
+        float v = joined(0, t, r);
+        if constexpr (MODE == kSilu) v = v / (1.0f + expf(-v)) * joined(1, t, r);
         const int tj = L.column[wave][t];
-        put(out + ((t0 + (tj & 15)) * a.k + (tj >> 4)) * a.ldo + n, v);
+        put(a.out, obf, ((t0 + (tj & 15)) * a.k + (tj >> 4)) * a.ldo + n0 + r, v);
       }
       __syncthreads();
     }
     if (a.ids && blockIdx.y == 0) {                  // slots without an expert
-      for (int p = tid >> 4; p < Tn * a.k; p += 4 * kWaves) {
+      for (int p = tid >> 4; p < Tn * a.k; p += blockDim.x >> 4) {
         if (L.ids[p] >= 0) continue;
-        for (int r = tid & 15; r < 16 * RT; r += 16)
-          if (n0 + r < a.N) put(out + (t0 * a.k + p) * a.ldo + n0 + r, 0.0f);
+        const int r = tid & 15;
+        if (n0 + r < a.N) put(a.out, obf, (t0 * a.k + p) * a.ldo + n0 + r, 0.0f);
       }
     }
   }
 }
 
-static constexpr int gemv_lds(int nt) { return (int)sizeof(Items) + kWaves * nt * 1024; }
-const KernelInfo kInfoGemvFp4 = {"gemv_fp4_kernel", "fgg_moe_gemv_fp4", 16, 16, 128, 64 * kWaves, 0, 0, gemv_lds(1),
-                                 gemv_lds(1), (const void*)gemv_fp4_kernel<kPlain, true, uint16_t, uint16_t, 1>};
-const KernelInfo kInfoGemvFp4Silu = {"gemv_fp4_kernel<silu>", "fgg_moe_gemv_fp4", 16, 16, 128, 64 * kWaves, 0, 0,
+static constexpr int gemv_lds(int nt) { return (int)sizeof(Items) + kMaxWaves * nt * 1024; }
+const KernelInfo kInfoGemvFp4 = {"gemv_fp4_kernel", "fgg_moe_gemv_fp4", 16, 16, 128, 64 * kMaxWaves, 0, 0, gemv_lds(1),
+                                 gemv_lds(1), (const void*)gemv_fp4_kernel<kPlain, true, uint16_t, 16>};
+const KernelInfo kInfoGemvFp4Silu = {"gemv_fp4_kernel<silu>", "fgg_moe_gemv_fp4", 16, 16, 128, 64 * kMaxWaves, 0, 0,
                                      gemv_lds(2), gemv_lds(2),
-                                     (const void*)gemv_fp4_kernel<kSilu, true, uint16_t, uint16_t, 1>};
-const KernelInfo kInfoGemvFp4Sum = {"gemv_fp4_kernel<sum>", "fgg_moe_gemv_fp4", 16, 16, 128, 64 * kWaves, 0, 0,
-                                    gemv_lds(1), gemv_lds(1),
-                                    (const void*)gemv_fp4_kernel<kSum, true, uint16_t, uint16_t, 1>};
+                                     (const void*)gemv_fp4_kernel<kSilu, true, uint16_t, 16>};
+const KernelInfo kInfoGemvFp4Sum = {"gemv_fp4_kernel<sum>", "fgg_moe_gemv_fp4", 16, 16, 128, 64 * kMaxWaves, 0, 0,
+                                    gemv_lds(1), gemv_lds(1), (const void*)gemv_fp4_kernel<kSum, true, uint16_t, 16>};
 
 hipError_t launch_gemv_fp4(bool tiled, int32_t G, int64_t T, int32_t k, int64_t N, int64_t K, const void* x,
                            bool x_bf16, int64_t ldx, bool per_slot, const uint8_t* b, const uint8_t* s,
                            const int32_t* ids, const float* w, bool silu, void* out, bool out_bf16, int64_t ldo,
                            hipStream_t st) {
-  const GemvArgs a = {G, T, k, N, K, x, ldx, per_slot, b, s, ids, w, out, ldo};
+  const GemvArgs a = {G, T, k, N, K, x, ldx, per_slot, b, s, ids, w, out, out_bf16, ldo};
   const int64_t pairs = (T < 16 ? T : 16) * k;
   const unsigned visits = ids && !w ? (unsigned)(pairs < G ? pairs : G) : 1;
+  const int waves = !w && K <= 2048 ? 4 : kMaxWaves;   // a span of 512 K for each
   const dim3 grid((unsigned)((N + 15) / 16), visits, (unsigned)((T + 15) / 16));
   const KernelInfo& info = w ? kInfoGemvFp4Sum : silu ? kInfoGemvFp4Silu : kInfoGemvFp4;
   trace_launch(info, grid, "G=%d T=%lld k=%d N=%lld K=%lld %s %s->%s", (int)G, (long long)T, (int)k, (long long)N,
                (long long)K, tiled ? "tiled" : "rows", x_bf16 ? "bf16" : "fp32", out_bf16 ? "bf16" : "fp32");
-  auto go = [&](auto mode, auto til, auto tx, auto to) {
-    using TX = decltype(tx);
-    using TO = decltype(to);
-    hipLaunchKernelGGL((gemv_fp4_kernel<decltype(mode)::value, decltype(til)::value, TX, TO, 1>), grid,
-                       dim3(64 * kWaves), 0, st, a);
+  auto go = [&](auto mode, auto til, auto tx, auto nc) {
+    hipLaunchKernelGGL((gemv_fp4_kernel<decltype(mode)::value, decltype(til)::value, decltype(tx), decltype(nc)::value>),
+                       grid, dim3(64 * waves), 0, st, a);
   };
-  auto with_types = [&](auto mode, auto til) {
-    if (x_bf16 && out_bf16) go(mode, til, uint16_t(), uint16_t());
-    else if (x_bf16) go(mode, til, uint16_t(), float());
-    else if (out_bf16) go(mode, til, float(), uint16_t());
-    else go(mode, til, float(), float());
+  using std::integral_constant;
+  auto with_type = [&](auto mode, auto til) {
+    if (!x_bf16) go(mode, til, float(), integral_constant<int, 16>());
+    else if (T <= 4) go(mode, til, uint16_t(), integral_constant<int, 4>());
+    else go(mode, til, uint16_t(), integral_constant<int, 16>());
   };
   auto with_mode = [&](auto til) {
-    if (w) with_types(std::integral_constant<int, kSum>(), til);
-    else if (silu) with_types(std::integral_constant<int, kSilu>(), til);
-    else with_types(std::integral_constant<int, kPlain>(), til);
+    if (w) with_type(integral_constant<int, kSum>(), til);
+    else if (silu) with_type(integral_constant<int, kSilu>(), til);
+    else with_type(integral_constant<int, kPlain>(), til);
   };
   if (tiled) with_mode(std::true_type());
   else with_mode(std::false_type());
