@@ -597,11 +597,13 @@ fgg_status fgg_moe_gemv_fp4(int32_t G, int64_t T, int32_t k, int64_t N, int64_t 
   if (!aligned(x, float_size(x_dtype)) || !aligned(out, float_size(out_dtype)) || !aligned(b, 16) ||
       (tiled && !aligned(b_scales, 16)) || !aligned(topk_ids, 4) || !aligned(topk_w, 4))
     return FGG_ERR_INVALID_VALUE;
-  fgg_status st = device_check(nullptr);
+  int num_cus = 0;
+  fgg_status st = device_check(&num_cus);
   if (st != FGG_OK) return st;
   return finish(fgg::launch_gemv_fp4(tiled, G, T, k, N, K, x, x_dtype == FGG_BF16, ldx, x_per_slot != 0,
                                      (const uint8_t*)b, (const uint8_t*)b_scales, topk_ids, topk_w,
-                                     act == FGG_ACT_SILU_MUL, out, out_dtype == FGG_BF16, ldo, (hipStream_t)stream));
+                                     act == FGG_ACT_SILU_MUL, out, out_dtype == FGG_BF16, ldo, num_cus,
+                                     (hipStream_t)stream));
 }
 
 int32_t fgg_kernel_count(void) {

@@ -146,6 +146,6 @@ constexpr int64_t kMaxRowBlocks = 0xFFFFFF;
 hipError_t launch_gemv_fp4(bool tiled, int32_t G, int64_t T, int32_t k, int64_t N, int64_t K, const void* x,
                            bool x_bf16, int64_t ldx, bool per_slot, const uint8_t* b, const uint8_t* s,
                            const int32_t* ids, const float* w, bool silu, void* out, bool out_bf16, int64_t ldo,
-                           hipStream_t st);
+                           int num_cus, hipStream_t st);
 
 }  // namespace fgg

@@ -217,11 +217,13 @@ __device__ inline int slot_of(const Items& L, int p0, int t, int Tn, int k) {
 
 // The weights of NT row tiles of one expert: wave-uniform pointers to each tile's first K block,
 // and this lane's offsets (row lane % 16, piece lane / 16) in a block of codes and of scales.
+// (code_high, scale_high: from the lane's row to the one eight below, for the paired form.)
 template <int NT>
 struct Tiles {
   const uint8_t* codes[NT];
   const uint8_t* scales[NT];
   uint32_t code_lane[NT], scale_lane[NT];
+  uint32_t code_high[NT], scale_high[NT];
 };
 
 // n <= U K blocks from kb on of NT row tiles of one expert, added to acc: every load is issued
@@ -317,16 +319,144 @@ __device__ inline void gemv_run(const Tiles<NT>& w, const TX* xrow, int64_t K, i
   }
 }
 
+// The untiled layout, bf16 activations.  A tile's row is K / 2 bytes from the next, and a K block of
+// it only half a cache line; a request for half a line occupies the vector cache like a whole
+// one.  So a load takes eight rows x two K blocks: in the lanes of rows 0-7 the first block of
+// the lane's row, in those of rows 8-15 the second block of row - 8, and a second load the same of
+// rows 8-15.  The matrix instruction is given activations of both blocks at once, in different
+// columns (col = t + NC * (h + 2 * i): token t, block h, operand i); of its results only rows
+// 0-7 x the columns h = 0 and rows 8-15 x the columns h = 1 mean anything, and their sum is
+// the eight rows' products.  More than eight tokens take two sets of columns (TG = 2).
+//
+// n <= U pairs of K blocks from pair p on.  WIDE (p even, U even): sixteen scale bytes per row and two pairs
+// in one load.  LAST: the pair that K ends in; pieces past the end read the pair's first piece, and
+// their activations are zeros.
+template <int NT, int NC, int TG, int U, bool WIDE, bool LAST>
+__device__ inline void rows_step(const Tiles<NT>& w, const uint16_t* const (&xrow)[TG], int64_t K, int p, int n,
+                                 v4f (&acc)[NT][2][TG][8 / NC]) {
+  constexpr int F = 8 / NC;                          // operands per register set
+  const int lane = threadIdx.x & 63, c = lane >> 4, second = (lane >> 3) & 1;
+  // this lane's piece of the pair in the codes, and in the activations
+  const bool in = !LAST || (int64_t)p * 256 + 128 * second + 32 * c < K;
+  const uint32_t back = in ? 0 : 4 * second + c;
+  const int xh = (lane & 15) / NC % 2;
+  const bool xin = !LAST || (int64_t)p * 256 + 128 * xh + 32 * c < K;
+  const int xback = xin ? 0 : 128 * xh + 32 * c;
+  u32x4 q[U][NT][2], wide[WIDE ? U / 2 : 1][NT][2], x[U][TG][4 / F];
+  uint32_t e[WIDE ? 1 : U][NT][2];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int b = p + (u < n ? u : n - 1);
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const uint32_t cl = w.code_lane[i] + (z ? w.code_high[i] : 0), sl = w.scale_lane[i] + (z ? w.scale_high[i] : 0);
+        q[u][i][z] = __builtin_nontemporal_load(
+            reinterpret_cast<const u32x4*>(w.codes[i] + (int64_t)b * 128 + (cl - 16u * back)));
+        if constexpr (!WIDE) e[u][i][z] = (w.scales[i] + (int64_t)b * 8)[sl + (4u * second + c - back)];
+        else if (u % 2 == 0)
+          wide[u / 2][i][z] = *reinterpret_cast<const u32x4_a1*>(w.scales[i] + (int64_t)(b >> 1) * 16 + sl);
+      }
+#pragma unroll
+    for (int g = 0; g < TG; ++g)
+#pragma unroll
+      for (int s = 0; s < 4 / F; ++s) {
+        x[u][g][s] = *reinterpret_cast<const u32x4_a2*>(xrow[g] + (int64_t)b * 256 + 8 * F * s - xback);
+        if (LAST && !xin) x[u][g][s] = u32x4{0, 0, 0, 0};
+      }
+  }
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (u >= n) break;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        uint32_t byte;
+        if constexpr (WIDE) {
+          const u32x4 s = wide[u / 2][i][z];
+          byte = ((second ? s[2 * (u % 2) + 1] : s[2 * (u % 2)]) >> (8 * c)) & 0xFFu;
+        } else {
+          byte = e[u][i][z];
+        }
+        const float scale = __uint_as_float(byte << 23);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const bf16x8 a = dequant8(q[u][i][z][d], scale);
+#pragma unroll
+          for (int g = 0; g < TG; ++g)
+            acc[i][z][g][d % F] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                a, __builtin_bit_cast(bf16x8, x[u][g][d / F]), acc[i][z][g][d % F], 0, 0, 0);
+        }
+      }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// One wave's share, as gemv_run: kb0 a multiple of 4, the sums of column t in the lanes of column t.
+template <int NT, int NC, int TG>
+__device__ inline void rows_run(const Tiles<NT>& w, const uint16_t* const (&xrow)[TG], int64_t K, int kb0, int kb1,
+                                v4f (&sum)[NT]) {
+  constexpr int F = 8 / NC;
+  constexpr int U = NT == 1 && TG == 1 ? 2 : 1;
+  v4f acc[NT][2][TG][F];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int z = 0; z < 2; ++z)
+#pragma unroll
+      for (int g = 0; g < TG; ++g)
+#pragma unroll
+        for (int f = 0; f < F; ++f) acc[i][z][g][f] = v4f{0, 0, 0, 0};
+  const int whole = (int64_t)kb1 * 128 <= K ? kb1 / 2 : (kb1 - 1) / 2;   // pairs that K fills
+  int p = kb0 / 2;
+  for (; p + U <= whole; p += U) rows_step<NT, NC, TG, U, U != 1, false>(w, xrow, K, p, U, acc);
+  if constexpr (U == 4) {
+    if (p + 2 <= whole) rows_step<NT, NC, TG, 2, true, false>(w, xrow, K, p, 2, acc), p += 2;
+  }
+  if (U > 1 && p < whole) rows_step<NT, NC, TG, 1, false, false>(w, xrow, K, p, 1, acc), ++p;
+  if (2 * p < kb1) rows_step<NT, NC, TG, 1, false, true>(w, xrow, K, p, 1, acc);
+  // operands (columns 2 NC apart), then the two blocks (columns NC apart, rows 8 apart)
+  const bool low = (threadIdx.x & 63) < 32;
+  const int col = threadIdx.x & 15;
+  const auto pick = [&](const v4f (&z0)[F], const v4f (&z1)[F], int r) {
+    float v0 = z0[0][r], v1 = z1[0][r];
+    if constexpr (F == 2) {
+      v0 = col < 8 ? v0 : z0[1][r];
+      v1 = col < 8 ? v1 : z1[1][r];
+      v0 += dpp_move<0x128>(v0);
+      v1 += dpp_move<0x128>(v1);
+    }
+    const float w0 = dpp_move<0x120 + NC>(v0), w1 = dpp_move<0x120 + NC>(v1);
+    const uint32_t up = __builtin_amdgcn_permlane32_swap(__float_as_uint(w0), __float_as_uint(w0), false, false)[1];
+    const uint32_t dn = __builtin_amdgcn_permlane32_swap(__float_as_uint(v1), __float_as_uint(v1), false, false)[0];
+    return low ? v0 + __uint_as_float(up) : __uint_as_float(dn) + w1;
+  };
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float v = pick(acc[i][0][0], acc[i][1][0], r);
+      if constexpr (TG == 2) {                       // tokens 8-15 to columns 8-15
+        const float t = dpp_move<0x128>(pick(acc[i][0][1], acc[i][1][1], r));
+        v = col < 8 ? v : t;
+      }
+      sum[i][r] = v;
+    }
+}
+
 }  // namespace
 
-template <int MODE, bool TILED, class TX, int NCMAX>
+template <int MODE, bool TILED, class TX, int NCMAX, int RT>
 __global__ void __launch_bounds__(64 * kMaxWaves, 4) gemv_fp4_kernel(GemvArgs a) {
-  constexpr int NT = MODE == kSilu ? 2 : 1;          // row tiles: one, or gate and up
+  constexpr int NT = MODE == kSilu ? 2 * RT : RT;    // row tiles: RT, or RT of gate and RT of up
   __shared__ Items L;
   __shared__ float part[kMaxWaves][NT][16][16];      // [wave][tile][token][row]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, c = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int64_t n0 = (int64_t)blockIdx.x * 16 * RT;
   const int64_t t0 = (int64_t)blockIdx.z * 16;
   const int Tn = a.T - t0 < 16 ? (int)(a.T - t0) : 16;
   const int64_t width = MODE == kSilu ? 2 * a.N : a.N;
@@ -350,26 +480,50 @@ __global__ void __launch_bounds__(64 * kMaxWaves, 4) gemv_fp4_kernel(GemvArgs a)
     if (lane < 16 && j >= 0) L.column[wave][__popc(m & ((1u << lane) - 1))] = (uint16_t)(lane + 16 * j);
     return __popc(m);
   };
+  constexpr bool kPairs = !TILED && sizeof(TX) == 2;
   // K blocks [kb0, kb1) of expert e for the nc tokens of L.column[wave], into sum (column t: the t-th)
   auto visit = [&](int e, int nc, int kb0, int kb1, v4f (&sum)[NT]) {
     Tiles<NT> w;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const int64_t up = i ? a.N : 0;
+      const int64_t up = i >= RT ? a.N : 0, r0 = n0 + 16 * (i % RT);
       if constexpr (TILED) {
-        const int64_t last = a.N / 16 - 1, nb = (n0 / 16 < last ? n0 / 16 : last) + up / 16;
+        const int64_t last = a.N / 16 - 1, nb = (r0 / 16 < last ? r0 / 16 : last) + up / 16;
         w.codes[i] = uniform_ptr(a.b + ((int64_t)e * (width / 16) + nb) * (a.K / 128) * 1024);
         w.scales[i] = uniform_ptr(a.s + ((int64_t)e * (width / 16) + nb) * ((a.K + 511) / 512) * 256);
         w.code_lane[i] = 16 * lane;
         w.scale_lane[i] = 16 * col;
       } else {
-        const int64_t last = a.N - 1, base = n0 < last ? n0 : last;
-        const uint32_t row = (uint32_t)(n0 + col < last ? n0 + col - base : last - base);   // past the end: not stored
+        const int64_t last = a.N - 1, base = r0 < last ? r0 : last;
+        const int rows = (int)(last - base);         // rows past the end: the last one, not stored
         w.codes[i] = uniform_ptr(a.b + ((int64_t)e * width + up + base) * (a.K / 2));
         w.scales[i] = uniform_ptr(a.s + ((int64_t)e * width + up + base) * (a.K / 32));
-        w.code_lane[i] = row * (uint32_t)(a.K / 2) + 16 * c;
+        const uint32_t row = (uint32_t)((kPairs ? col & 7 : col) < rows ? (kPairs ? col & 7 : col) : rows);
+        const uint32_t high = (uint32_t)((col & 7) + 8 < rows ? (col & 7) + 8 : rows);
+        w.code_lane[i] = row * (uint32_t)(a.K / 2) + 16 * c + (kPairs ? 64 * (col >> 3) : 0);
         w.scale_lane[i] = row * (uint32_t)(a.K / 32);
+        w.code_high[i] = (high - row) * (uint32_t)(a.K / 2);
+        w.scale_high[i] = (high - row) * (uint32_t)(a.K / 32);
       }
+    }
+    if constexpr (kPairs) {
+      auto go = [&](auto n, auto g) {
+        constexpr int NC = decltype(n)::value, TG = decltype(g)::value;
+        const TX* row[TG];
+#pragma unroll
+        for (int q = 0; q < TG; ++q) {
+          const int t = col % NC + NC * q, h = col / NC % 2, i = col / (2 * NC);
+          const int tj = L.column[wave][t < nc ? t : 0];
+          const int64_t xr = a.per_slot ? (t0 + (tj & 15)) * a.k + (tj >> 4) : t0 + (tj & 15);
+          row[q] = x + xr * a.ldx + 128 * h + 32 * c + 8 * i;
+        }
+        rows_run<NT, NC, TG>(w, row, a.K, kb0, kb1, sum);
+      };
+      using std::integral_constant;
+      if (NCMAX == 4 || nc <= 4) go(integral_constant<int, 4>(), integral_constant<int, 1>());
+      else if (nc <= 8) go(integral_constant<int, 8>(), integral_constant<int, 1>());
+      else go(integral_constant<int, 8>(), integral_constant<int, 2>());
+      return;
     }
     auto go = [&](auto n) {
       constexpr int NC = decltype(n)::value;
@@ -421,9 +575,10 @@ __global__ void __launch_bounds__(64 * kMaxWaves, 4) gemv_fp4_kernel(GemvArgs a)
       at += s1 - s0;
     }
     __syncthreads();
-    for (int i = tid; i < 256; i += blockDim.x) {
-      const int t = i >> 4, r = i & 15;
-      if (t < Tn && n0 + r < a.N) put(a.out, obf, (t0 + t) * a.ldo + n0 + r, joined(0, t, r));
+    for (int i = tid; i < RT * 256; i += blockDim.x) {
+      const int t = (i >> 4) & 15, r = i & 15;
+      const int64_t n = n0 + 16 * (i >> 8) + r;
+      if (t < Tn && n < a.N) put(a.out, obf, (t0 + t) * a.ldo + n, joined(i >> 8, t, r));
     }
   } else {
     const int kb0 = 4 * (int)((int64_t)spans * wave / waves), end = 4 * (int)((int64_t)spans * (wave + 1) / waves);
@@ -435,21 +590,22 @@ __global__ void __launch_bounds__(64 * kMaxWaves, 4) gemv_fp4_kernel(GemvArgs a)
 #pragma unroll
       for (int i = 0; i < NT; ++i) *reinterpret_cast<v4f*>(&part[wave][i][col][4 * c]) = sum[i];
       __syncthreads();
-      for (int i = tid; i < 256; i += blockDim.x) {
-        const int t = i >> 4, r = i & 15;
-        if (t >= nc || n0 + r >= a.N) continue;
-        float v = joined(0, t, r);
-        if constexpr (MODE == kSilu) v = v / (1.0f + expf(-v)) * joined(1, t, r);
+      for (int i = tid; i < RT * 256; i += blockDim.x) {
+        const int t = (i >> 4) & 15, r = i & 15;
+        const int64_t n = n0 + 16 * (i >> 8) + r;
+        if (t >= nc || n >= a.N) continue;
+        float v = joined(i >> 8, t, r);
+        if constexpr (MODE == kSilu) v = v / (1.0f + expf(-v)) * joined(RT + (i >> 8), t, r);
         const int tj = L.column[wave][t];
-        put(a.out, obf, ((t0 + (tj & 15)) * a.k + (tj >> 4)) * a.ldo + n0 + r, v);
+        put(a.out, obf, ((t0 + (tj & 15)) * a.k + (tj >> 4)) * a.ldo + n, v);
       }
       __syncthreads();
     }
     if (a.ids && blockIdx.y == 0) {                  // slots without an expert
       for (int p = tid >> 4; p < Tn * a.k; p += blockDim.x >> 4) {
         if (L.ids[p] >= 0) continue;
-        const int r = tid & 15;
-        if (n0 + r < a.N) put(a.out, obf, (t0 * a.k + p) * a.ldo + n0 + r, 0.0f);
+        for (int r = tid & 15; r < 16 * RT; r += 16)
+          if (n0 + r < a.N) put(a.out, obf, (t0 * a.k + p) * a.ldo + n0 + r, 0.0f);
       }
     }
   }
@@ -457,34 +613,43 @@ __global__ void __launch_bounds__(64 * kMaxWaves, 4) gemv_fp4_kernel(GemvArgs a)
 
 static constexpr int gemv_lds(int nt) { return (int)sizeof(Items) + kMaxWaves * nt * 1024; }
 const KernelInfo kInfoGemvFp4 = {"gemv_fp4_kernel", "fgg_moe_gemv_fp4", 16, 16, 128, 64 * kMaxWaves, 0, 0, gemv_lds(1),
-                                 gemv_lds(1), (const void*)gemv_fp4_kernel<kPlain, true, uint16_t, 16>};
+                                 gemv_lds(1), (const void*)gemv_fp4_kernel<kPlain, true, uint16_t, 16, 1>};
 const KernelInfo kInfoGemvFp4Silu = {"gemv_fp4_kernel<silu>", "fgg_moe_gemv_fp4", 16, 16, 128, 64 * kMaxWaves, 0, 0,
                                      gemv_lds(2), gemv_lds(2),
-                                     (const void*)gemv_fp4_kernel<kSilu, true, uint16_t, 16>};
+                                     (const void*)gemv_fp4_kernel<kSilu, true, uint16_t, 16, 1>};
 const KernelInfo kInfoGemvFp4Sum = {"gemv_fp4_kernel<sum>", "fgg_moe_gemv_fp4", 16, 16, 128, 64 * kMaxWaves, 0, 0,
-                                    gemv_lds(1), gemv_lds(1), (const void*)gemv_fp4_kernel<kSum, true, uint16_t, 16>};
+                                    gemv_lds(1), gemv_lds(1), (const void*)gemv_fp4_kernel<kSum, true, uint16_t, 16, 1>};
 
 hipError_t launch_gemv_fp4(bool tiled, int32_t G, int64_t T, int32_t k, int64_t N, int64_t K, const void* x,
                            bool x_bf16, int64_t ldx, bool per_slot, const uint8_t* b, const uint8_t* s,
                            const int32_t* ids, const float* w, bool silu, void* out, bool out_bf16, int64_t ldo,
-                           hipStream_t st) {
+                           int num_cus, hipStream_t st) {
   const GemvArgs a = {G, T, k, N, K, x, ldx, per_slot, b, s, ids, w, out, out_bf16, ldo};
   const int64_t pairs = (T < 16 ? T : 16) * k;
   const unsigned visits = ids && !w ? (unsigned)(pairs < G ? pairs : G) : 1;
   const int waves = !w && K <= 2048 ? 4 : kMaxWaves;   // a span of 512 K for each
-  const dim3 grid((unsigned)((N + 15) / 16), visits, (unsigned)((T + 15) / 16));
+  // Two row tiles a wave share the activations' loads, which is worth most of their cost from five
+  // tokens on (tiled: down of 16 tokens, N 7168, 62 -> 53.5 us; 16384 x 7168, 16 tokens, 32 -> 25), as
+  // long as there is a workgroup for most compute units (4096 x 7168, 128 workgroups, 11.4 -> 14.4).
+  // Not with the untiled layout's paired loads (8 tokens 61 -> 65 us: registers spill).
+  const int rt = tiled && x_bf16 && !silu && T > 4 && (N + 31) / 32 * visits >= num_cus * 3 / 4 ? 2 : 1;
+  const dim3 grid((unsigned)((N + 16 * rt - 1) / (16 * rt)), visits, (unsigned)((T + 15) / 16));
   const KernelInfo& info = w ? kInfoGemvFp4Sum : silu ? kInfoGemvFp4Silu : kInfoGemvFp4;
   trace_launch(info, grid, "G=%d T=%lld k=%d N=%lld K=%lld %s %s->%s", (int)G, (long long)T, (int)k, (long long)N,
                (long long)K, tiled ? "tiled" : "rows", x_bf16 ? "bf16" : "fp32", out_bf16 ? "bf16" : "fp32");
-  auto go = [&](auto mode, auto til, auto tx, auto nc) {
-    hipLaunchKernelGGL((gemv_fp4_kernel<decltype(mode)::value, decltype(til)::value, decltype(tx), decltype(nc)::value>),
-                       grid, dim3(64 * waves), 0, st, a);
+  auto go = [&](auto mode, auto til, auto tx, auto nc, auto r) {
+    hipLaunchKernelGGL((gemv_fp4_kernel<decltype(mode)::value, decltype(til)::value, decltype(tx), decltype(nc)::value,
+                                        decltype(r)::value>), grid, dim3(64 * waves), 0, st, a);
   };
   using std::integral_constant;
   auto with_type = [&](auto mode, auto til) {
-    if (!x_bf16) go(mode, til, float(), integral_constant<int, 16>());
-    else if (T <= 4) go(mode, til, uint16_t(), integral_constant<int, 4>());
-    else go(mode, til, uint16_t(), integral_constant<int, 16>());
+    using One = integral_constant<int, 1>;
+    if (!x_bf16) return go(mode, til, float(), integral_constant<int, 16>(), One());
+    if (T <= 4) return go(mode, til, uint16_t(), integral_constant<int, 4>(), One());
+    if constexpr (decltype(mode)::value != kSilu && decltype(til)::value) {
+      if (rt == 2) return go(mode, til, uint16_t(), integral_constant<int, 16>(), integral_constant<int, 2>());
+    }
+    go(mode, til, uint16_t(), integral_constant<int, 16>(), One());
   };
   auto with_mode = [&](auto til) {
     if (w) with_type(integral_constant<int, kSum>(), til);
