@@ -471,14 +471,22 @@ _FLOAT = {torch.float32: FGG_F32, torch.bfloat16: FGG_BF16}
 _GATES = {"softmax": FGG_GATE_SOFTMAX, "sigmoid": FGG_GATE_SIGMOID}
 
 
+# These calls are small enough for the host's share to count (a launch is 3.2 us): the current
+# stream's handle is asked for directly where torch offers that (0.1 us; the Stream object
+# costs 1.9), and outputs made here are not checked.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_QDESC = {}
+
+
 def _call(name, dev, *args):
     """Call the entry point on dev's current stream, with dev as the current device."""
     fn = getattr(_lib or load_library(), name)
     if dev.index == torch.cuda.current_device():
-        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        status = fn(*args, _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            status = fn(*args, _raw_stream(dev.index))
     if status != 0:
         _check(name, status)
 
@@ -489,11 +497,12 @@ def _addr(t):
 
 def _float_rows(t, name, dtype=None):
     """A 2-D fp32/bf16 CUDA tensor with unit column stride and rows that do not overlap; returns its row stride."""
-    assert t.is_cuda and t.dim() == 2 and t.dtype in _FLOAT and (dtype is None or t.dtype == dtype), name
-    n = t.shape[1]
-    assert t.stride(1) == 1 or n <= 1, name
-    ld = t.stride(0)
-    if t.shape[0] <= 1 and ld < n:
+    shape, dt = t.shape, t.dtype
+    assert t.is_cuda and len(shape) == 2 and dt in _FLOAT and (dtype is None or dt == dtype), name
+    ld, unit = t.stride()
+    n = shape[1]
+    assert unit == 1 or n <= 1, name
+    if shape[0] <= 1 and ld < n:
         ld = n
     assert ld >= n, name
     return ld
@@ -516,13 +525,13 @@ def moe_route(logits, k, gate="softmax", bias=None, renormalize=False, scale=1.0
     ld = _float_rows(logits, "logits")
     T, E = logits.shape
     k, dev = int(k), logits.device
+    _dense(bias, "bias", dev, torch.float32, (E,))
+    _dense(ids, "ids", dev, torch.int32, (T, k))
+    _dense(weights, "weights", dev, torch.float32, (T, k))
     if ids is None:
         ids = torch.empty((T, k), dtype=torch.int32, device=dev)
     if weights is None:
         weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-    _dense(bias, "bias", dev, torch.float32, (E,))
-    _dense(ids, "ids", dev, torch.int32, (T, k))
-    _dense(weights, "weights", dev, torch.float32, (T, k))
     _call("fgg_moe_route", dev, logits.data_ptr(), _FLOAT[logits.dtype], T, E, ld, k, _GATES[gate], _addr(bias),
           1 if renormalize else 0, float(scale), ids.data_ptr(), weights.data_ptr())
     return ids, weights
@@ -534,10 +543,7 @@ def moe_route_backward(logits, topk_ids, dtopk_w, gate="softmax", renormalize=Fa
     ld = _float_rows(logits, "logits")
     T, E = logits.shape
     k, dev = topk_ids.shape[1], logits.device
-    if out is None:
-        out = torch.empty((T, E), dtype=logits.dtype, device=dev)
-    ldo = _float_rows(out, "out", logits.dtype)
-    assert out.device == dev and out.shape == logits.shape, "out"
+    out, ldo = _rows_out(out, (T, E), logits, "out")
     _dense(topk_ids, "topk_ids", dev, torch.int32, (T, k))
     _dense(dtopk_w, "dtopk_w", dev, torch.float32, (T, k))
     _call("fgg_moe_route_backward", dev, logits.data_ptr(), _FLOAT[logits.dtype], T, E, ld, k, _GATES[gate],
@@ -556,7 +562,7 @@ def _slots(src_to_row, T, topk_w, dev):
 
 def _rows_out(out, shape, like, name):
     if out is None:
-        out = torch.empty(shape, dtype=like.dtype, device=like.device)
+        return like.new_empty(shape), shape[1]
     ld = _float_rows(out, name, like.dtype)
     assert out.device == like.device and tuple(out.shape) == shape, name
     return out, ld
@@ -645,7 +651,7 @@ def moe_gemv_fp4(x, b, b_scales, topk_ids=None, topk_w=None, b_qdesc=Q_E2M1_E8M0
     topk_ids int32 [T, k]: the result is [T, k, N]; with topk_w (fp32 [T, k]) the
     gate-weighted sum over the slots, [T, N].  Without topk_ids (G = 1): [T, N]."""
     per_slot = x.dim() == 3
-    assert x.is_cuda and x.dim() in (2, 3) and x.dtype in _FLOAT and out_dtype in _FLOAT, "x"
+    assert x.is_cuda and (per_slot or x.dim() == 2) and x.dtype in _FLOAT and out_dtype in _FLOAT, "x"
     T, K = x.shape[0], x.shape[-1]
     dev, G = x.device, b.shape[0]
     k = 1 if topk_ids is None else topk_ids.shape[1]
@@ -668,12 +674,18 @@ def moe_gemv_fp4(x, b, b_scales, topk_ids=None, topk_w=None, b_qdesc=Q_E2M1_E8M0
     _dense(topk_ids, "topk_ids", dev, torch.int32, (T, k))
     _dense(topk_w, "topk_w", dev, torch.float32, (T, k))
     shape = (T, N) if topk_ids is None or topk_w is not None else (T, k, N)
+    ldo = N
     if out is None:
         out = torch.empty(shape, dtype=out_dtype, device=dev)
-    assert out.device == dev and out.dtype in _FLOAT and tuple(out.shape) == shape, "out"
-    assert out.is_contiguous() or out.dim() == 2, "out"
-    ldo = N if out.dim() == 3 else _float_rows(out, "out")
+    else:
+        assert out.device == dev and out.dtype in _FLOAT and tuple(out.shape) == shape, "out"
+        assert out.is_contiguous() or out.dim() == 2, "out"
+        if out.dim() == 2:
+            ldo = _float_rows(out, "out")
+    desc = _QDESC.get(b_qdesc)
+    if desc is None:
+        desc = _QDESC[b_qdesc] = QDesc(*b_qdesc)
     _call("fgg_moe_gemv_fp4", dev, G, T, k, N, K, x.data_ptr(), _FLOAT[x.dtype], ldx, 1 if per_slot else 0,
-          b.data_ptr(), b_scales.data_ptr(), QDesc(*b_qdesc), _addr(topk_ids), _addr(topk_w),
+          b.data_ptr(), b_scales.data_ptr(), desc, _addr(topk_ids), _addr(topk_w),
           FGG_ACT_SILU_MUL if silu_mul else FGG_ACT_NONE, out.data_ptr(), _FLOAT[out.dtype], ldo)
     return out
