@@ -7,7 +7,7 @@
 //   w_j   = scale * s_{ids j}          or, renormalized,   scale * s_{ids j} / sum_m s_{ids m}
 //
 // One group of lanes (16, 32 or 64, the smallest that has a lane for every expert up to
-// 64) owns a token and holds its logits in registers, expert i * GW + lane in register i;
+// 64) owns a token and holds its logits in registers, experts EPL * lane .. in order;
 // a wave takes 64 / GW tokens.  Selection: k rounds of a group-wide maximum over 32-bit
 // keys in integer order.  What depends on every expert (the softmax's normalizer) is
 // computed only when it is asked for: the renormalized softmax is the softmax of the k
@@ -26,15 +26,71 @@ namespace {
 
 constexpr float kInf = __builtin_inff();
 
-template <class T>
-__device__ inline float load_one(const T* p);
-template <>
-__device__ inline float load_one<float>(const float* p) { return *p; }
-template <>
-__device__ inline float load_one<uint16_t>(const uint16_t* p) { return bf16_to_f32(*p); }
+__device__ inline float load_one(const float* p) { return *p; }
+__device__ inline float load_one(const uint16_t* p) { return bf16_to_f32(*p); }
 
-__device__ inline void store_one(float* p, float v) { *p = v; }
-__device__ inline void store_one(uint16_t* p, float v) { *p = bf16_bits_rne(v); }
+// Experts [e, e + EPL) of a row, -inf from E on; and the same elements stored.  Whole groups move as
+// vectors of the element's alignment (this part's vector memory takes any).
+template <int EPL>
+__device__ inline void load_experts(const float* row, int e, int E, float (&x)[EPL]) {
+  typedef float Vec __attribute__((ext_vector_type(EPL), aligned(4)));
+  if (e + EPL <= E) {
+    if constexpr (EPL == 1) {
+      x[0] = row[e];
+    } else {
+      const Vec v = *reinterpret_cast<const Vec*>(row + e);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) x[i] = v[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) x[i] = e + i < E ? row[e + i] : -kInf;
+  }
+}
+template <int EPL>
+__device__ inline void load_experts(const uint16_t* row, int e, int E, float (&x)[EPL]) {
+  typedef uint16_t Vec __attribute__((ext_vector_type(EPL), aligned(2)));
+  if (e + EPL <= E) {
+    if constexpr (EPL == 1) {
+      x[0] = bf16_to_f32(row[e]);
+    } else {
+      const Vec v = *reinterpret_cast<const Vec*>(row + e);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) x[i] = bf16_to_f32(v[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) x[i] = e + i < E ? bf16_to_f32(row[e + i]) : -kInf;
+  }
+}
+template <int EPL>
+__device__ inline void store_experts(float* row, int e, int E, const float (&x)[EPL]) {
+  typedef float Vec __attribute__((ext_vector_type(EPL), aligned(4)));
+  if (EPL > 1 && e + EPL <= E) {
+    Vec v;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) v[i] = x[i];
+    *reinterpret_cast<Vec*>(row + e) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (e + i < E) row[e + i] = x[i];
+  }
+}
+template <int EPL>
+__device__ inline void store_experts(uint16_t* row, int e, int E, const float (&x)[EPL]) {
+  typedef uint16_t Vec __attribute__((ext_vector_type(EPL), aligned(2)));
+  if (EPL > 1 && e + EPL <= E) {
+    Vec v;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) v[i] = bf16_bits_rne(x[i]);
+    *reinterpret_cast<Vec*>(row + e) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (e + i < E) row[e + i] = bf16_bits_rne(x[i]);
+  }
+}
 
 // Floating order as unsigned order; 0 is below every number's key (the key of -inf is
 // 0x007FFFFF) and stands for "cannot be chosen".  Signed zeros are made equal first.
@@ -57,9 +113,14 @@ __device__ inline float sigmoid_scaled(float v, float m) {
   return expf(v - m) / (1.0f + expf(v));
 }
 
-// The group's lane `src` (0 <= src < GW) of v.
+// e^(x - m) for x <= m, as e^-g with g = m - x held to 200 (e^-200 is 0 in fp32; -inf and the
+// difference of far logits end there).
+__device__ inline float exp_below(float x, float m) { return exp_neg(fminf(m - x, 200.0f)); }
+
+// The group's lane `src` (0 <= src < GW, the same in the group) of v.
 template <int GW>
 __device__ inline int group_lane(int v, int src) {
+  if constexpr (GW == 64) return __builtin_amdgcn_readlane(v, src);
   return __shfl(v, src, GW);
 }
 
@@ -75,9 +136,9 @@ __device__ inline float gate_weight(float v, bool on, bool sigmoid, bool renorm,
     if (!renorm) return num;
   } else if (renorm) {
     const float top = group_reduce<GW>(on ? v : -kInf, OpFMax());
-    num = on ? expf(v - top) : 0.0f;
+    num = on ? exp_below(v, top) : 0.0f;
   } else {
-    return on ? expf(v - m_all) / sum_all : 0.0f;
+    return on ? exp_below(v, m_all) / sum_all : 0.0f;
   }
   const float sum = group_reduce<GW>(num, OpAdd());
   return on ? num / sum : 0.0f;
@@ -94,12 +155,11 @@ __global__ void __launch_bounds__(256) route_kernel(const TI* __restrict__ logit
   const bool live = t < T;
   const TI* row = logits + (live ? t : 0) * ld;
   float x[EPL];
-  int bad = 0;                                        // a NaN in the row
+  int bad = 0;                                        // a NaN in the row (or +inf under a softmax)
+  load_experts<EPL>(row, gl * EPL, live ? E : 0, x);
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const int e = i * GW + gl;
-    x[i] = (live && e < E) ? load_one(row + e) : -kInf;
-    bad |= x[i] != x[i];
+    bad |= __builtin_amdgcn_classf(x[i], sigmoid ? 0x003 : 0x203);   // NaN (and +inf)
   }
   bad = group_reduce<GW>(bad, OpMax());
 
@@ -111,7 +171,7 @@ __global__ void __launch_bounds__(256) route_kernel(const TI* __restrict__ logit
     m_all = group_reduce<GW>(m_all, OpFMax());
     if (!renorm) {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) sum_all += x[i] == -kInf ? 0.0f : expf(x[i] - m_all);
+      for (int i = 0; i < EPL; ++i) sum_all += exp_below(x[i], m_all);
       sum_all = group_reduce<GW>(sum_all, OpAdd());
     }
   }
@@ -134,7 +194,7 @@ __global__ void __launch_bounds__(256) route_kernel(const TI* __restrict__ logit
     if (!sigmoid) sum = group_reduce<GW>(sum, OpAdd());
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const int e = i * GW + gl;
+      const int e = gl * EPL + i;
       double c = sigmoid ? s[i] : s[i] / sum;
       if (!(c == c)) c = 0.0;                         // a row with NaN or +inf: by the bias alone
       c += e < E ? (double)bias[e] : 0.0;
@@ -145,32 +205,62 @@ __global__ void __launch_bounds__(256) route_kernel(const TI* __restrict__ logit
     for (int i = 0; i < EPL; ++i) key[i] = x[i] > -kInf ? order_key(x[i]) : 0;
   }
 
+  // k rounds.  The lane's candidate: up to four experts are sorted once (equal keys keep their order)
+  // and the lane that gave the largest moves its queue up; more are searched each round.  Lanes
+  // hold ascending experts, so of equal keys the first lane's is the lower expert.
+  constexpr bool kQueue = EPL <= 4;
+  int at[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) at[i] = gl * EPL + i;
+  if constexpr (kQueue) {
+#pragma unroll
+    for (int end = EPL - 1; end > 0; --end)
+#pragma unroll
+      for (int i = 0; i < end; ++i) {
+        const bool swap = key[i + 1] > key[i];
+        const Key hi = swap ? key[i + 1] : key[i], lo = swap ? key[i] : key[i + 1];
+        const int ahi = swap ? at[i + 1] : at[i], alo = swap ? at[i] : at[i + 1];
+        key[i] = hi, key[i + 1] = lo, at[i] = ahi, at[i + 1] = alo;
+      }
+  }
+  const int base = lane & ~(GW - 1);                  // the group's first lane
   int my_id = -1;
   float my_v = 0.0f;
   for (int j = 0; j < k; ++j) {
-    Key best = 0;
+    Key best = key[0];
     int bi = 0;
+    if constexpr (!kQueue) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (key[i] > best) best = key[i], bi = i;
-    const Key top = group_reduce<GW>(best, OpMax());
-    // the lowest expert among those with the largest key
-    const int e = group_reduce<GW>(best == top ? bi * GW + gl : 0x7FFFFFFF, OpMin());
-    const bool found = top != 0;
-    float v;
-    if constexpr (BIAS) {
-      float mine = x[0];
-#pragma unroll
-      for (int i = 1; i < EPL; ++i) mine = i == e / GW ? x[i] : mine;
-      v = __int_as_float(group_lane<GW>(__float_as_int(mine), e & (GW - 1)));
-    } else {
-      v = order_value(top);
+      for (int i = 1; i < EPL; ++i)
+        if (key[i] > best) best = key[i], bi = i;
     }
-    if (gl == j && found) my_id = e, my_v = v;
+    const Key top = group_reduce<GW>(best, OpMax());
+    const uint64_t heads = __ballot(best == top);
+    int src, e;
+    if constexpr (GW == 64) {
+      src = __ffsll((unsigned long long)heads) - 1;
+      e = __builtin_amdgcn_readlane(kQueue ? at[0] : gl * EPL + bi, src);
+    } else {
+      src = __ffs((uint32_t)(heads >> base) & (uint32_t)((1ull << GW) - 1)) - 1;
+      e = src;                                        // (one expert per lane)
+    }
+    if (gl == j && top != 0) {
+      my_id = e;
+      if constexpr (!BIAS) my_v = order_value(top);
+    }
+    if (gl == src) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (i * GW + gl == e) key[i] = 0;
+      for (int i = 0; i < EPL; ++i) {
+        if constexpr (kQueue) {
+          key[i] = i + 1 < EPL ? key[i + 1 < EPL ? i + 1 : i] : 0;
+          at[i] = at[i + 1 < EPL ? i + 1 : i];
+        } else {
+          if (i == bi) key[i] = 0;
+        }
+      }
+    }
   }
+  if (BIAS && my_id >= 0) my_v = load_one(row + my_id);           // (in the cache: the row was just read)
   const bool on = my_id >= 0;
   float g = gate_weight<GW>(my_v, on, sigmoid, renorm, m_all, sum_all) * scale;
   if (bad) g = __builtin_nanf("");
@@ -200,65 +290,57 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const TI* __restric
   float u = 0.0f, v = -kInf;
   if (live && gl < k) {
     id = ids[t * k + gl];
-    if (id < 0 || id >= E) {
-      id = -1;
-    } else {
-      u = scale * dw[t * k + gl];
-      v = load_one(row + id);
-    }
+    u = scale * dw[t * k + gl];
   }
-  const bool on = id >= 0;
+  const bool whole = !sigmoid && !renorm;
+  const bool on = id >= 0 && id < E;
+  if (!on) id = -1, u = 0.0f;
+  if (!whole && on) v = load_one(row + id);
+  float d = u;
+  if (!whole) {
+    const float p = gate_weight<GW>(v, on && v != -kInf, sigmoid, renorm, 0.0f, 1.0f);
+    const float mean = renorm ? group_reduce<GW>(on ? u * p : 0.0f, OpAdd()) : 0.0f;
+    d = p * (u - mean);
+    if (sigmoid && on) d *= v >= 0.0f ? expf(-v) / (1.0f + expf(-v)) : 1.0f / (1.0f + expf(v));   // 1 - sigma(v)
+  }
   float out[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) out[i] = 0.0f;
-  float d, dot = 0.0f, m = -kInf, sum = 0.0f;
-  const bool whole = !sigmoid && !renorm;
-  float x[EPL];
+  for (int j = 0; j < k; ++j) {
+    const int mine = group_lane<GW>(id, j) - gl * EPL;
+    const float dj = __int_as_float(group_lane<GW>(__float_as_int(d), j));
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) out[i] += mine == i ? dj : 0.0f;
+  }
   if (whole) {
+    float x[EPL], m = -kInf, sum = 0.0f, dot = 0.0f;
     bool bad = false;
+    load_experts<EPL>(row, gl * EPL, live ? E : 0, x);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const int e = i * GW + gl;
-      x[i] = (live && e < E) ? load_one(row + e) : -kInf;
       m = fmaxf(m, x[i]);
-      bad |= x[i] != x[i];
+      bad |= __builtin_amdgcn_classf(x[i], 0x203);    // NaN, +inf
     }
     m = group_reduce<GW>(m, OpFMax());
+    const bool none = m == -kInf;                     // a row without any expert: all zero
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      x[i] = x[i] == -kInf ? 0.0f : expf(x[i] - m);   // 0 for closed experts, also in a row of them
+      x[i] = exp_below(x[i], m);
       sum += x[i];
+      dot = fmaf(out[i], x[i], dot);
     }
     if (bad) sum = __builtin_nanf("");
     sum = group_reduce<GW>(sum, OpAdd());
-    const float inv_ok = sum > 0.0f || sum != sum ? sum : 1.0f;   // a row without any expert: all zero
+    const float inv = none ? 0.0f : 1.0f / sum;
+    dot = group_reduce<GW>(dot, OpAdd()) * inv;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) x[i] = x[i] / inv_ok;
-    const float s = on && v > -kInf ? expf(v - m) / inv_ok : (on && v != v ? v : 0.0f);
-    dot = group_reduce<GW>(on ? u * s : 0.0f, OpAdd());
-    d = u;
-  } else {
-    float p = gate_weight<GW>(v, on && v != -kInf, sigmoid, renorm, 0.0f, 1.0f);
-    if (renorm) {
-      const float mean = group_reduce<GW>(on ? u * p : 0.0f, OpAdd());
-      d = p * (u - mean);
-    } else {
-      d = u * p;
+    for (int i = 0; i < EPL; ++i) out[i] = x[i] * inv * (out[i] - dot);
+    if (none) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) out[i] = 0.0f;
     }
-    if (sigmoid && on) d *= v >= 0.0f ? expf(-v) / (1.0f + expf(-v)) : 1.0f / (1.0f + expf(v));   // 1 - sigma(v)
   }
-  for (int j = 0; j < k; ++j) {
-    const int ej = group_lane<GW>(id, j);
-    const float dj = __int_as_float(group_lane<GW>(__float_as_int(d), j));
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (i * GW + gl == ej) out[i] += dj;
-  }
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = i * GW + gl;
-    if (live && e < E) store_one(dlogits + t * ldd + e, whole ? x[i] * (out[i] - dot) : out[i]);
-  }
+  if (live) store_experts<EPL>(dlogits + t * ldd, gl * EPL, E, out);
 }
 
 const KernelInfo kInfoRoute = {"route_kernel", "fgg_moe_route", 0, 0, 0, 256, 0, 0, 0, 0,
