@@ -107,8 +107,31 @@ __device__ inline void clear_padding(const int32_t* row_to_src, int64_t total, i
 
 }  // namespace
 
+namespace {
+
+// The rows of token t, slot j in lane j (k <= 64), and which slots have one: every wave on its
+// own, so that all of a token's rows are known before the first is touched.
+__device__ inline uint64_t token_rows(const int32_t* src_to_row, int64_t t, int k, int64_t M, int& row) {
+  const int lane = threadIdx.x & 63;
+  row = lane < k ? src_to_row[t * k + lane] : -1;
+  return __ballot(row >= 0 && row < M);
+}
+__device__ inline int lane_int(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+__device__ inline float lane_float(float v, int lane) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
+}
+// The lowest slot of the mask, taken out of it.
+__device__ inline int next_slot(uint64_t& m) {
+  const int j = __ffsll((unsigned long long)m) - 1;
+  m &= m - 1;
+  return j;
+}
+
+}  // namespace
+
 // Scatter: block (t, y) takes columns [y * C * 256 vectors) of token t, one pass, and writes them
-// to each of the token's rows; the blocks behind the last token clear padding rows.
+// to each of the token's rows (a token without a row is not read); the blocks behind the last
+// token clear padding rows.
 template <class T, bool W, int C>
 __global__ void __launch_bounds__(256) rows_scatter_kernel(const T* __restrict__ tok, int64_t ldt,
                                                            const float* __restrict__ w,
@@ -127,16 +150,21 @@ __global__ void __launch_bounds__(256) rows_scatter_kernel(const T* __restrict__
     return;
   }
   const int64_t t = blockIdx.x;
+  int row;
+  uint64_t live = token_rows(src_to_row, t, k, M, row);
+  if (live == 0) return;
+  float wt = 1.0f;
+  if constexpr (W) wt = (int)(threadIdx.x & 63) < k ? w[t * k + (threadIdx.x & 63)] : 0.0f;
   u32x4 x[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int64_t col = col0 + ((int64_t)c * 256 + threadIdx.x) * V;
     if (col < N) x[c] = load_vec<T>(tok + t * ldt, col, N);
   }
-  for (int j = 0; j < k; ++j) {
-    const int64_t r = src_to_row[t * k + j];
-    if (r < 0 || r >= M) continue;
-    const float wj = W ? w[t * k + j] : 1.0f;
+  while (live) {
+    const int j = next_slot(live);
+    T* out = rows + (int64_t)lane_int(row, j) * ldr;
+    const float wj = lane_float(wt, j);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int64_t col = col0 + ((int64_t)c * 256 + threadIdx.x) * V;
@@ -145,15 +173,41 @@ __global__ void __launch_bounds__(256) rows_scatter_kernel(const T* __restrict__
         float f[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) f[i] = wj * Elem<T>::get(x[c], i);
-        store_vec<T>(rows + r * ldr, col, N, Elem<T>::pack(f));
+        store_vec<T>(out, col, N, Elem<T>::pack(f));
       } else {
-        store_vec<T>(rows + r * ldr, col, N, x[c]);
+        store_vec<T>(out, col, N, x[c]);
       }
     }
   }
 }
 
-// Collect: block (t, y) sums the token's rows over columns [y * C * 256 vectors).
+// Collect: block (t, y) sums the token's rows over columns [y * C * 256 vectors), B rows' loads at
+// a time, added in slot order.
+template <class T, bool W, int C, int B>
+__device__ inline void collect_rows(const T* rows, int64_t ldr, int64_t col0, int64_t N, int row, float wt,
+                                    uint64_t& live, float (&acc)[C][Elem<T>::kVec]) {
+  constexpr int V = Elem<T>::kVec;
+  u32x4 y[B][C];
+  float wj[B];
+#pragma unroll
+  for (int b = 0; b < B; ++b) {
+    const int j = next_slot(live);
+    const T* in = rows + (int64_t)lane_int(row, j) * ldr;
+    wj[b] = lane_float(wt, j);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int64_t col = col0 + ((int64_t)c * 256 + threadIdx.x) * V;
+      if (col < N) y[b][c] = load_vec<T>(in, col, N);
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < B; ++b)
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[c][i] = fmaf(wj[b], Elem<T>::get(y[b][c], i), acc[c][i]);
+}
+
 template <class T, bool W, int C>
 __global__ void __launch_bounds__(256) rows_collect_kernel(const T* __restrict__ rows, int64_t ldr,
                                                            const float* __restrict__ w,
@@ -161,26 +215,18 @@ __global__ void __launch_bounds__(256) rows_collect_kernel(const T* __restrict__
                                                            int64_t M, T* __restrict__ tok, int64_t ldt) {
   constexpr int V = Elem<T>::kVec;
   const int64_t t = blockIdx.x, col0 = (int64_t)blockIdx.y * C * 256 * V;
+  int row;
+  uint64_t live = token_rows(src_to_row, t, k, M, row);
+  float wt = 1.0f;
+  if constexpr (W) wt = (int)(threadIdx.x & 63) < k ? w[t * k + (threadIdx.x & 63)] : 0.0f;
   float acc[C][V];
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[c][i] = 0.0f;
-  for (int j = 0; j < k; ++j) {
-    const int64_t r = src_to_row[t * k + j];
-    if (r < 0 || r >= M) continue;
-    const float wj = W ? w[t * k + j] : 1.0f;
-    u32x4 y[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int64_t col = col0 + ((int64_t)c * 256 + threadIdx.x) * V;
-      if (col < N) y[c] = load_vec<T>(rows + r * ldr, col, N);
-    }
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int i = 0; i < V; ++i) acc[c][i] = fmaf(wj, Elem<T>::get(y[c], i), acc[c][i]);
-  }
+  while (__popcll(live) >= 4) collect_rows<T, W, C, 4>(rows, ldr, col0, N, row, wt, live, acc);
+  if (__popcll(live) >= 2) collect_rows<T, W, C, 2>(rows, ldr, col0, N, row, wt, live, acc);
+  if (live) collect_rows<T, W, C, 1>(rows, ldr, col0, N, row, wt, live, acc);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int64_t col = col0 + ((int64_t)c * 256 + threadIdx.x) * V;
@@ -193,6 +239,48 @@ __global__ void __launch_bounds__(256) rows_collect_kernel(const T* __restrict__
 // forward's rows.  Otherwise the rows (gradients) are summed into the token's gradient `out`,
 // each dotted with the forward's token.  Partial dots: per thread, then per wave, then the four
 // waves of LDS in order.
+template <class T, bool SCATTER, int C, int B>
+__device__ inline void dot_rows(const T* rows, int64_t ldr, T* out, int64_t ldo, int64_t col0, int64_t N, int row,
+                                float wt, const u32x4 (&x)[C], uint64_t& live, float (&acc)[C][Elem<T>::kVec],
+                                float* part) {
+  constexpr int V = Elem<T>::kVec;
+  u32x4 y[B][C];
+  int slot[B];
+#pragma unroll
+  for (int b = 0; b < B; ++b) {
+    slot[b] = next_slot(live);
+    const T* in = rows + (int64_t)lane_int(row, slot[b]) * ldr;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int64_t col = col0 + ((int64_t)c * 256 + threadIdx.x) * V;
+      y[b][c] = u32x4{0, 0, 0, 0};
+      if (col < N) y[b][c] = load_vec<T>(in, col, N);
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < B; ++b) {
+    const float wj = lane_float(wt, slot[b]);
+    float dot = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int64_t col = col0 + ((int64_t)c * 256 + threadIdx.x) * V;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        dot = fmaf(Elem<T>::get(x[c], i), Elem<T>::get(y[b][c], i), dot);
+        if constexpr (!SCATTER) acc[c][i] = fmaf(wj, Elem<T>::get(y[b][c], i), acc[c][i]);
+      }
+      if constexpr (SCATTER) {
+        float f[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = wj * Elem<T>::get(x[c], i);
+        if (col < N) store_vec<T>(out + (int64_t)lane_int(row, slot[b]) * ldo, col, N, Elem<T>::pack(f));
+      }
+    }
+    dot = group_reduce<64>(dot, OpAdd());
+    if ((threadIdx.x & 63) == 0) part[slot[b]] += dot;
+  }
+}
+
 template <class T, bool W, bool SCATTER, int C>
 __global__ void __launch_bounds__(256) rows_dot_kernel(const T* __restrict__ tok, int64_t ldt,
                                                        const T* __restrict__ rows, int64_t ldr,
@@ -212,47 +300,27 @@ __global__ void __launch_bounds__(256) rows_dot_kernel(const T* __restrict__ tok
   }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t = blockIdx.x;
-  for (int i = threadIdx.x; i < 256; i += 256) part[i >> 6][i & 63] = 0.0f;
-  __syncthreads();
+  int row;
+  const uint64_t slots = token_rows(src_to_row, t, k, M, row);
+  float wt = 1.0f;
+  if constexpr (W) wt = lane < k ? w[t * k + lane] : 0.0f;
+  part[wave][lane] = 0.0f;                            // (each wave its own row: in order with its sums)
   for (int64_t col0 = 0; col0 < N; col0 += (int64_t)C * 256 * V) {
+    if (SCATTER && slots == 0) break;
     u32x4 x[C];
     float acc[C][V];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int64_t col = col0 + ((int64_t)c * 256 + threadIdx.x) * V;
-      x[c] = col < N ? load_vec<T>(tok + t * ldt, col, N) : u32x4{0, 0, 0, 0};
+      x[c] = u32x4{0, 0, 0, 0};
+      if (col < N && slots != 0) x[c] = load_vec<T>(tok + t * ldt, col, N);
 #pragma unroll
       for (int i = 0; i < V; ++i) acc[c][i] = 0.0f;
     }
-    for (int j = 0; j < k; ++j) {
-      const int64_t r = src_to_row[t * k + j];
-      if (r < 0 || r >= M) continue;
-      const float wj = W ? w[t * k + j] : 1.0f;
-      u32x4 y[C];
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int64_t col = col0 + ((int64_t)c * 256 + threadIdx.x) * V;
-        y[c] = col < N ? load_vec<T>(rows + r * ldr, col, N) : u32x4{0, 0, 0, 0};
-      }
-      float dot = 0.0f;
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int64_t col = col0 + ((int64_t)c * 256 + threadIdx.x) * V;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          dot = fmaf(Elem<T>::get(x[c], i), Elem<T>::get(y[c], i), dot);
-          if constexpr (!SCATTER) acc[c][i] = fmaf(wj, Elem<T>::get(y[c], i), acc[c][i]);
-        }
-        if constexpr (SCATTER) {
-          float f[V];
-#pragma unroll
-          for (int i = 0; i < V; ++i) f[i] = wj * Elem<T>::get(x[c], i);
-          if (col < N) store_vec<T>(out + r * ldo, col, N, Elem<T>::pack(f));
-        }
-      }
-      dot = group_reduce<64>(dot, OpAdd());
-      if (lane == 0) part[wave][j] += dot;
-    }
+    uint64_t live = slots;
+    while (__popcll(live) >= 4) dot_rows<T, SCATTER, C, 4>(rows, ldr, out, ldo, col0, N, row, wt, x, live, acc, part[wave]);
+    if (__popcll(live) >= 2) dot_rows<T, SCATTER, C, 2>(rows, ldr, out, ldo, col0, N, row, wt, x, live, acc, part[wave]);
+    if (live) dot_rows<T, SCATTER, C, 1>(rows, ldr, out, ldo, col0, N, row, wt, x, live, acc, part[wave]);
     if constexpr (!SCATTER) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
