@@ -58,10 +58,15 @@ struct Elem<float> {
 };
 
 // Elements [col, col + kVec) of a row of N; those at or past N are zero.  col < N.
-template <class T>
+// ONCE: nothing else reads them (no place in the caches is asked for).
+template <class T, bool ONCE = false>
 __device__ inline u32x4 load_vec(const T* row, int64_t col, int64_t N) {
   constexpr int V = Elem<T>::kVec;
-  if (col + V <= N) return *reinterpret_cast<const typename Elem<T>::Packed*>(row + col);
+  if (col + V <= N) {
+    const auto* p = reinterpret_cast<const typename Elem<T>::Packed*>(row + col);
+    if constexpr (ONCE) return __builtin_nontemporal_load(p);
+    else return *p;
+  }
   union {
     u32x4 v;
     T e[V];
@@ -254,7 +259,7 @@ __device__ inline void dot_rows(const T* rows, int64_t ldr, T* out, int64_t ldo,
     for (int c = 0; c < C; ++c) {
       const int64_t col = col0 + ((int64_t)c * 256 + threadIdx.x) * V;
       y[b][c] = u32x4{0, 0, 0, 0};
-      if (col < N) y[b][c] = load_vec<T>(in, col, N);
+      if (col < N) y[b][c] = load_vec<T, true>(in, col, N);
     }
   }
 #pragma unroll
