@@ -514,8 +514,8 @@ fgg_status fgg_moe_unpermute_rows_backward(const void* dout, fgg_dtype dtype, in
  *                                  out[t·k + j][n] = g / (1 + e^-g) * u,  g = y[t][j][n], u = y[t][j][N + n]
  *   topk_w given (FGG_ACT_NONE):   out[t][n] = sum_j topk_w[t][j] * y[t][j][n]
  * and rounded once to out_dtype (FGG_BF16 or FGG_F32; row stride ldo >= N).  A slot whose id is
- * outside [0, G) has no expert: its output row is 0, and the sum skips it (its weight and x are
- * not read).  An id may stand twice in a token.  topk_ids NULL: one set of weights for every
+ * outside [0, G) has no expert: its output row is 0, and the sum skips it, whatever its weight
+ * and x hold.  An id may stand twice in a token.  topk_ids NULL: one set of weights for every
  * token (G = 1, k = 1, topk_w NULL).
  * x: fp32 or bf16, [T][ldx], or with x_per_slot != 0 [T·k][ldx] (row t·k + j for slot j);
  * ldx >= K, any alignment of the element.  bq: {E2M1X2,E8M0,1,32} (b [G][N][K/2], b_scales
