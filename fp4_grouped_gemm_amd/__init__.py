@@ -476,17 +476,19 @@ _GATES = {"softmax": FGG_GATE_SOFTMAX, "sigmoid": FGG_GATE_SIGMOID}
 # costs 1.9), and outputs made here are not checked.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _QDESC = {}
 
 
 def _call(name, dev, *args):
     """Call the entry point on dev's current stream, with dev as the current device."""
     fn = getattr(_lib or load_library(), name)
-    if dev.index == torch.cuda.current_device():
-        status = fn(*args, _raw_stream(dev.index))
+    index = dev.index
+    if index == _current_device():
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, _raw_stream(dev.index))
+            status = fn(*args, _raw_stream(index))
     if status != 0:
         _check(name, status)
 
@@ -512,8 +514,8 @@ def _dense(t, name, dev, dtype, shape=None, numel=None):
     """A contiguous tensor of the given type and shape (or number of elements) on dev, or None."""
     if t is None:
         return
-    assert t.device == dev and t.dtype == dtype and t.is_contiguous(), name
-    assert (shape is None or tuple(t.shape) == shape) and (numel is None or t.numel() == numel), name
+    assert t.dtype == dtype and t.is_contiguous() and t.device == dev, name
+    assert (shape is None or t.shape == shape) and (numel is None or t.numel() == numel), name
 
 
 def moe_route(logits, k, gate="softmax", bias=None, renormalize=False, scale=1.0, ids=None, weights=None):
@@ -564,7 +566,7 @@ def _rows_out(out, shape, like, name):
     if out is None:
         return like.new_empty(shape), shape[1]
     ld = _float_rows(out, name, like.dtype)
-    assert out.device == like.device and tuple(out.shape) == shape, name
+    assert out.shape == shape and out.device == like.device, name
     return out, ld
 
 
@@ -598,7 +600,7 @@ def moe_permute_rows_backward(drows, src_to_row, T, topk_w=None, x=None, out=Non
     dw, ldx = None, 0
     if x is not None:
         ldx = _float_rows(x, "x", drows.dtype)
-        assert x.device == dev and tuple(x.shape) == (T, N), "x"
+        assert x.device == dev and x.shape == (T, N), "x"
         dw = torch.empty((T, k), dtype=torch.float32, device=dev)
     _call("fgg_moe_permute_rows_backward", dev, drows.data_ptr(), _FLOAT[drows.dtype], M, lddr, _addr(x), ldx,
           _addr(topk_w), src_to_row.data_ptr(), T, k, N, dx.data_ptr(), lddx, _addr(dw))
@@ -633,7 +635,7 @@ def moe_unpermute_rows_backward(dout, src_to_row, row_to_src, offsets, topk_w=No
     dw, ldr = None, 0
     if rows is not None:
         ldr = _float_rows(rows, "rows", dout.dtype)
-        assert rows.device == dev and tuple(rows.shape) == (M, N), "rows"
+        assert rows.device == dev and rows.shape == (M, N), "rows"
         dw = torch.empty((T, k), dtype=torch.float32, device=dev)
     _call("fgg_moe_unpermute_rows_backward", dev, dout.data_ptr(), _FLOAT[dout.dtype], T, k, N, lddo, _addr(rows), ldr,
           _addr(topk_w), src_to_row.data_ptr(), row_to_src.data_ptr(), offsets.data_ptr(), offsets.numel() - 1, M,
@@ -678,7 +680,7 @@ def moe_gemv_fp4(x, b, b_scales, topk_ids=None, topk_w=None, b_qdesc=Q_E2M1_E8M0
     if out is None:
         out = torch.empty(shape, dtype=out_dtype, device=dev)
     else:
-        assert out.device == dev and out.dtype in _FLOAT and tuple(out.shape) == shape, "out"
+        assert out.device == dev and out.dtype in _FLOAT and out.shape == shape, "out"
         assert out.is_contiguous() or out.dim() == 2, "out"
         if out.dim() == 2:
             ldo = _float_rows(out, "out")
