@@ -13,6 +13,12 @@
 // computed only when it is asked for: the renormalized softmax is the softmax of the k
 // chosen logits.
 //
+// Bound by instruction issue, not by memory: one token is one wave's few hundred vector
+// instructions.  8192 tokens x 256 experts, bf16, top-8 (4.7 MB, 1 us at a large copy's rate):
+// 7.7 us; with a search and two reductions a round 10.1 (a round is one reduction now, the tie
+// being the first lane of a ballot, and a queue step).  Gradient, 16384 x 160 fp32, top-6 (21.8 MB):
+// 10 us (12.8 with gathered scores and element-wise loads).  One token: 4.7 us, a launch.
+//
 // With a bias the keys are sums of rounded scores, and two experts whose keys differ by
 // less than the rounding of 32 bits would be ordered by it: keys are formed in 64 bits
 // (the sigmoid or exponential of every logit in double), and ranked as 64-bit integers.
