@@ -64,6 +64,13 @@ __device__ inline T swap_reduce(T v, Op op) {
   }
 }
 
+// Between LDS accesses of one wave that pass values from lane to lane: the hardware runs them in
+// order, and this keeps the compiler from moving one across (no instruction, no wait).
+__device__ inline void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // Reduction over aligned groups of GW lanes (16, 32 or 64), the result in every lane.
 // Data-parallel moves inside the 16-lane rows (quad swaps, then mirrors of 8 and 16
 // lanes) and the row swaps of gfx950 above them: no LDS permute.  Both halves of each

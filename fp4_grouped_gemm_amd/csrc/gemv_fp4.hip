@@ -63,7 +63,7 @@ struct GemvArgs {
   int64_t ldo;
 };
 
-// Four codes pairs of one 32-bit word, times 2^(byte - 127), as eight bf16.
+// The eight codes of one 32-bit word, times 2^(byte - 127), as bf16.
 __device__ inline bf16x8 dequant8(uint32_t codes, float scale) {
   const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0);
   const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1);
@@ -115,10 +115,12 @@ struct Frag<uint16_t, NC> {
         const int t = 4 * s + c;
         *reinterpret_cast<u32x4*>(xs + t * 256 + 16 * (col ^ key(t))) = v[s];
       }
+      wave_sync();
       const int t = col / F;
 #pragma unroll
       for (int s = 0; s < S; ++s)
         v[s] = *reinterpret_cast<const u32x4*>(xs + t * 256 + 16 * ((4 * c + F * s + col % F) ^ key(t)));
+      wave_sync();
     }
   }
   __device__ void mul(int d, bf16x8 a, v4f (&acc)[F]) const {
@@ -203,6 +205,7 @@ __device__ inline int list_few_items(Items& L, const int32_t* ids, int64_t t0, i
     L.again[p] = (uint8_t)again;
     if (lead) L.item[__popcll(m & ((1ull << p) - 1))] = (uint16_t)p;
   }
+  wave_sync();
   return __popcll(m);
 }
 
@@ -268,8 +271,9 @@ struct Tiles {
 // n <= U K blocks from kb on of NT row tiles of one expert, added to acc: every load is issued
 // before the first is used, and none is conditional (a load under a branch is waited for at
 // the branch's end; past n the last block is read again).  WIDE (U >= 2, kb a multiple of U): the scale
-// bytes of a span of four blocks in one load; a byte per block otherwise.  LAST (U = 1): the block that K ends in, whose lanes past the end read the block's first
-// piece, with zeros for activations.
+// bytes of a span of four blocks in one load; a byte per block otherwise.  FULL: n is U.  LAST (U = 1):
+// the block that K ends in, whose lanes past the end read the block's first piece, with zeros for
+// activations.
 template <class TX, bool TILED, int NT, int NC, int U, bool WIDE, bool FULL, bool LAST>
 __device__ inline void gemv_step(const Tiles<NT>& w, const TX* const (&xrow)[Frag<TX, NC>::S], uint8_t* scratch,
                                  int lane, int64_t K, int kb, int n, v4f (&acc)[NT][Frag<TX, NC>::F]) {
@@ -422,14 +426,18 @@ __global__ void __launch_bounds__(64 * kMaxWaves, 4) gemv_fp4_kernel(GemvArgs a)
 
   // The tokens of visit p0, one a column: returns their number, and in L.column[wave] which.
   auto columns = [&](int p0) -> int {
+    int nc = Tn;
+    wave_sync();
     if (!a.ids) {
       if (lane < 16) L.column[wave][lane] = (uint16_t)(lane < Tn ? lane : 0);
-      return Tn;
+    } else {
+      const int j = slot_of(L, p0, col, Tn, a.k);
+      const uint32_t m = (uint32_t)__ballot(lane < 16 && j >= 0);
+      if (lane < 16 && j >= 0) L.column[wave][__popc(m & ((1u << lane) - 1))] = (uint16_t)(lane + 16 * j);
+      nc = __popc(m);
     }
-    const int j = slot_of(L, p0, col, Tn, a.k);
-    const uint32_t m = (uint32_t)__ballot(lane < 16 && j >= 0);
-    if (lane < 16 && j >= 0) L.column[wave][__popc(m & ((1u << lane) - 1))] = (uint16_t)(lane + 16 * j);
-    return __popc(m);
+    wave_sync();
+    return nc;
   };
   // K blocks [kb0, kb1) of expert e for the nc tokens of L.column[wave], into sum; returns the number of
   // columns of a token (the t-th one's sums are in the lanes of column t times that)

@@ -314,7 +314,8 @@ __global__ void __launch_bounds__(256) rows_dot_kernel(const T* __restrict__ tok
   const uint64_t slots = token_rows(src_to_row, t, k, M, row);
   float wt = 1.0f;
   if constexpr (W) wt = lane < k ? w[t * k + lane] : 0.0f;
-  part[wave][lane] = 0.0f;                            // (each wave its own row: in order with its sums)
+  part[wave][lane] = 0.0f;                            // (each wave its own row)
+  wave_sync();
   for (int64_t col0 = 0; col0 < N; col0 += (int64_t)C * 256 * V) {
     if (SCATTER && slots == 0) break;
     u32x4 x[C];

@@ -520,8 +520,9 @@ fgg_status fgg_moe_unpermute_rows_backward(const void* dout, fgg_dtype dtype, in
  * x: fp32 or bf16, [T][ldx], or with x_per_slot != 0 [T·k][ldx] (row t·k + j for slot j);
  * ldx >= K, any alignment of the element.  bq: {E2M1X2,E8M0,1,32} (b [G][N][K/2], b_scales
  * [G][N][K/32], any N, K % 32 == 0) or {E2M1X2_TILED,E8M0,1,32} (from fgg_pack_fp4_weights:
- * N % 16 == 0, K % 128 == 0), b 16-byte aligned.  Scale bytes up to 252 are exact (6 times a
- * larger power of two is beyond the bf16 and fp32 range).
+ * N % 16 == 0, K % 128 == 0), b 16-byte aligned.  Scale bytes 2 to 252 are exact (6 times a
+ * larger power of two is beyond the bf16 and fp32 range, half of a smaller one subnormal, which
+ * the matrix core may take as zero).
  * Each expert that tokens 16i .. 16i + 15 name is read once for the 16 of them, so the call
  * is meant for up to 16 tokens; more are taken 16 by 16.  No result depends on an order of
  * arrival: the same call gives the same bits.  1 <= G <= 1024, 1 <= k <= 64, K >= 32;
