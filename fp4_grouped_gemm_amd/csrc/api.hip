@@ -97,7 +97,7 @@ int kernel_table(const KernelInfo* const** out) {
       &kInfoW4a4LowRank,     &kInfoW4a4Gemm,         &kInfoMxfp4Gemm,
       &kInfoRoute,           &kInfoRouteBackward,     &kInfoRowsScatter,    &kInfoRowsCollect,
       &kInfoRowsScatterDot,  &kInfoRowsCollectDot,    &kInfoGemvFp4,        &kInfoGemvFp4Silu,
-      &kInfoGemvFp4Sum,
+      &kInfoGemvFp4Sum,      &kInfoGemvFp4Sum2,
   };
   *out = table;
   return (int)(sizeof table / sizeof table[0]);

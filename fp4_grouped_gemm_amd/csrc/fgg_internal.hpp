@@ -39,7 +39,7 @@ extern const KernelInfo kInfoQuantE4m3_1x128, kInfoQuantE4m3_128x128, kInfoQuant
     kInfoFp8ContigSilu, kInfoFp8ContigCombine, kInfoFp8Dense,
     kInfoMaskedFp4Tiled, kInfoMaskedFp4, kInfoMaskedFp8, kInfoPackFp4, kInfoPackFp4Scales, kInfoW4a4Prep, kInfoW4a4LowRank,
     kInfoW4a4Gemm, kInfoMxfp4Gemm, kInfoRoute, kInfoRouteBackward, kInfoRowsScatter, kInfoRowsCollect,
-    kInfoRowsScatterDot, kInfoRowsCollectDot, kInfoGemvFp4, kInfoGemvFp4Silu, kInfoGemvFp4Sum;
+    kInfoRowsScatterDot, kInfoRowsCollectDot, kInfoGemvFp4, kInfoGemvFp4Silu, kInfoGemvFp4Sum, kInfoGemvFp4Sum2;
 
 enum class QuantKind { E4M3_1x128, E4M3_128x128, E2M1_1x16, E2M1_E8M0_1x32 };
 

@@ -10,8 +10,7 @@
 // Bound by the weights' bytes: every distinct expert of up to 16 tokens is read once, whatever
 // number of them chose it.  Measured: gate-up of one token's 8 experts (N 2048, K 7168, tiled,
 // 125 MB) 23.2 us, 5.4 TB/s, of 32 experts 85.7 us, 5.8 TB/s; of 16 tokens 94.7 us, 5.2 TB/s; down of
-// 16 tokens (N 7168, K 2048, 248 MB) 58 us tiled, 63 us untiled (the summed form has one workgroup
-// a tile, 448 for 256 compute units, and waits for its own loads more); a 4096 x 7168 matrix and
+// 16 tokens (N 7168, K 2048, 248 MB) 49 us tiled, 63 us untiled (half lines); a 4096 x 7168 matrix and
 // one token 6.1 us, of which a launch and two memory latencies are most.  An E2M1 code times a power of two is a bf16 number, so the weights
 // go through v_cvt_scalef32_pk_bf16_fp4 (two codes and their scale per instruction) into the
 // bf16 matrix instruction 16x16x32 with 16 weight rows as its rows and the tokens as its
@@ -40,7 +39,7 @@ typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kMaxWaves = 8;
+constexpr int kMaxWaves = 16;       // (of one workgroup; eight except in the summed form's two-tile variant)
 constexpr int kMaxPairs = 1024;    // 16 tokens x 64 slots
 constexpr int kMaxGroups = 1024;
 
@@ -265,7 +264,7 @@ template <int NT>
 struct Tiles {
   const uint8_t* codes[NT];
   const uint8_t* scales[NT];
-  uint32_t code_lane, scale_lane, byte_lane;
+  uint32_t code_lane[NT], scale_lane[NT], byte_lane[NT];
 };
 
 // n <= U K blocks from kb on of NT row tiles of one expert, added to acc: every load is issued
@@ -307,17 +306,17 @@ __device__ inline void gemv_step(const Tiles<NT>& w, const TX* const (&xrow)[Fra
     const int b = FULL || u < n ? u : n - 1;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const auto* at = reinterpret_cast<const u32x4*>(wb[i] + (w.code_lane - 16 * cback) + b * code_step);
+      const auto* at = reinterpret_cast<const u32x4*>(wb[i] + (w.code_lane[i] - 16 * cback) + b * code_step);
       // Whole lines, read once: past the caches.  Untiled, a load takes half of each line and the next
       // block's load the other half, from the cache (8 experts' gate-up 35 -> 28 us).
       if constexpr (TILED) q[u][i] = __builtin_nontemporal_load(at);
       else q[u][i] = *at;
       if constexpr (!WIDE) {
         const int in_span = TILED ? ((kb & 3) + b) * 4 : b * 4;   // (tiled: the step stays in its span)
-        e[u][i] = (sb[i] + (w.byte_lane - sback))[in_span];
+        e[u][i] = (sb[i] + (w.byte_lane[i] - sback))[in_span];
       } else if (u % 4 == 0) {
-        if constexpr (TILED) wide[u / 4][i] = *reinterpret_cast<const u32x4*>(sb[i] + w.scale_lane);
-        else wide[u / 4][i] = *reinterpret_cast<const u32_a1*>(sb[i] + w.scale_lane);
+        if constexpr (TILED) wide[u / 4][i] = *reinterpret_cast<const u32x4*>(sb[i] + w.scale_lane[i]);
+        else wide[u / 4][i] = *reinterpret_cast<const u32_a1*>(sb[i] + w.scale_lane[i]);
       }
     }
     f[u].load(xb, b * 128, xin);
@@ -401,17 +400,18 @@ __device__ inline void gemv_run(const Tiles<NT>& w, const TX* const (&xrow)[Frag
 
 }  // namespace
 
-template <int MODE, bool TILED, class TX, int NCMAX>
-__global__ void __launch_bounds__(64 * kMaxWaves, 4) gemv_fp4_kernel(GemvArgs a) {
-  constexpr int NT = MODE == kSilu ? 2 : 1;          // row tiles: one, or gate and up
+template <int MODE, bool TILED, class TX, int NCMAX, int RT>
+__global__ void __launch_bounds__(RT == 2 ? 1024 : 512, 4) gemv_fp4_kernel(GemvArgs a) {
+  constexpr int NT = MODE == kSilu ? 2 : RT;         // row tiles: gate and up, or RT one below the other
+  constexpr int kWaves = RT == 2 ? 16 : 8;
   __shared__ Items L;
-  __shared__ float part[kMaxWaves][NT][16][16];      // [wave][tile][token][row]
+  __shared__ float part[kWaves][NT][16][16];         // [wave][tile][token][row]
   constexpr bool kXs = NCMAX > 4 && sizeof(TX) == 2;
   constexpr int kScratch = kXs ? kXsBytes : 0;       // a wave's own
-  __shared__ __attribute__((aligned(16))) uint8_t scratch[kScratch ? kMaxWaves * kScratch : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t scratch[kScratch ? kWaves * kScratch : 16];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, c = lane >> 4;
-  int64_t n0 = (int64_t)blockIdx.x * 16;             // first output column of the tile at work
+  int64_t n0 = (int64_t)blockIdx.x * (16 * RT);             // first output column of the tile at work
   const int64_t t0 = (int64_t)blockIdx.z * 16;
   const int Tn = a.T - t0 < 16 ? (int)(a.T - t0) : 16;
   const int64_t width = MODE == kSilu ? 2 * a.N : a.N;
@@ -450,23 +450,24 @@ __global__ void __launch_bounds__(64 * kMaxWaves, 4) gemv_fp4_kernel(GemvArgs a)
     Tiles<NT> w;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const int64_t up = i ? a.N : 0;
+      // (gate and up are N rows apart, tiles of one matrix 16; a tile past the end is the last one again)
+      const int64_t up = MODE == kSilu && i ? a.N : 0, r0 = n0 + (MODE == kSilu ? 0 : 16 * i);
       if constexpr (TILED) {
-        const int64_t last = a.N / 16 - 1, nb = (n0 / 16 < last ? n0 / 16 : last) + up / 16;
+        const int64_t last = a.N / 16 - 1, nb = (r0 / 16 < last ? r0 / 16 : last) + up / 16;
         w.codes[i] = uniform_ptr(a.b + ((int64_t)e * (width / 16) + nb) * (a.K / 128) * 1024);
         w.scales[i] = uniform_ptr(a.s + ((int64_t)e * (width / 16) + nb) * ((a.K + 511) / 512) * 256);
-        w.code_lane = 16 * lane;
-        w.scale_lane = 16 * col;
-        w.byte_lane = 16 * col + c;
+        w.code_lane[i] = 16 * lane;
+        w.scale_lane[i] = 16 * col;
+        w.byte_lane[i] = 16 * col + c;
       } else {
-        const int64_t last = a.N - 1, base = n0 < last ? n0 : last;
-        const int rows = (int)(last - base);         // rows past the end: the last one, not stored
+        const int64_t last = a.N - 1, base = r0 < last ? r0 : last;
+        const int rows = (int)(last - base < 15 ? last - base : 15);   // rows past the end: the last one, not stored
         const uint32_t row = lane >> 2 < rows ? lane >> 2 : rows, row_c = col < rows ? col : rows;
         w.codes[i] = uniform_ptr(a.b + ((int64_t)e * width + up + base) * (a.K / 2));
         w.scales[i] = uniform_ptr(a.s + ((int64_t)e * width + up + base) * (a.K / 32));
-        w.code_lane = row * (uint32_t)(a.K / 2) + 16 * (lane & 3);
-        w.scale_lane = row * (uint32_t)(a.K / 32) + 4 * (lane & 3);
-        w.byte_lane = row_c * (uint32_t)(a.K / 32) + c;
+        w.code_lane[i] = row * (uint32_t)(a.K / 2) + 16 * (lane & 3);
+        w.scale_lane[i] = row * (uint32_t)(a.K / 32) + 4 * (lane & 3);
+        w.byte_lane[i] = row_c * (uint32_t)(a.K / 32) + c;
       }
     }
     auto go = [&](auto n) -> int {
@@ -525,9 +526,10 @@ __global__ void __launch_bounds__(64 * kMaxWaves, 4) gemv_fp4_kernel(GemvArgs a)
       at += s1 - s0;
     }
     __syncthreads();
-    for (int i = tid; i < 256; i += blockDim.x) {
-      const int t = i >> 4, r = i & 15;
-      if (t < Tn && n0 + r < a.N) put(a.out, obf, (t0 + t) * a.ldo + n0 + r, joined(0, t, r));
+    for (int i = tid; i < RT * 256; i += blockDim.x) {
+      const int t = (i >> 4) & 15, r = i & 15;
+      const int64_t n = n0 + 16 * (i >> 8) + r;
+      if (t < Tn && n < a.N) put(a.out, obf, (t0 + t) * a.ldo + n, joined(i >> 8, t, r));
     }
   } else {
     const int kb0 = 4 * (int)((int64_t)spans * wave / waves), end = 4 * (int)((int64_t)spans * (wave + 1) / waves);
@@ -535,7 +537,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves, 4) gemv_fp4_kernel(GemvArgs a)
     for (int it = blockIdx.y; it < items; it += gridDim.y) {
       const int p0 = a.ids ? __builtin_amdgcn_readfirstlane(L.item[it]) : 0, nc = columns(p0);
       const int e = a.ids ? __builtin_amdgcn_readfirstlane(L.ids[p0]) : 0;
-      for (n0 = (int64_t)blockIdx.x * 16; n0 < a.N; n0 += (int64_t)gridDim.x * 16) {
+      for (n0 = (int64_t)blockIdx.x * (16 * RT); n0 < a.N; n0 += (int64_t)gridDim.x * 16) {
         v4f sum[NT];
         const int f = visit(e, nc, kb0, kb1, sum);
         if (col % f == 0) {
@@ -558,21 +560,24 @@ __global__ void __launch_bounds__(64 * kMaxWaves, 4) gemv_fp4_kernel(GemvArgs a)
       for (int p = tid >> 4; p < Tn * a.k; p += blockDim.x >> 4) {
         if (L.ids[p] >= 0) continue;
         const int r = tid & 15;
-        for (n0 = (int64_t)blockIdx.x * 16; n0 < a.N; n0 += (int64_t)gridDim.x * 16)
+        for (n0 = (int64_t)blockIdx.x * (16 * RT); n0 < a.N; n0 += (int64_t)gridDim.x * 16)
           if (n0 + r < a.N) put(a.out, obf, (t0 * a.k + p) * a.ldo + n0 + r, 0.0f);
       }
     }
   }
 }
 
-static constexpr int gemv_lds(int nt) { return (int)sizeof(Items) + kMaxWaves * (nt * 1024 + kXsBytes); }
-const KernelInfo kInfoGemvFp4 = {"gemv_fp4_kernel", "fgg_moe_gemv_fp4", 16, 16, 128, 64 * kMaxWaves, 0, 0, gemv_lds(1),
-                                 gemv_lds(1), (const void*)gemv_fp4_kernel<kPlain, true, uint16_t, 16>};
-const KernelInfo kInfoGemvFp4Silu = {"gemv_fp4_kernel<silu>", "fgg_moe_gemv_fp4", 16, 16, 128, 64 * kMaxWaves, 0, 0,
+static constexpr int gemv_lds(int nt, int waves = 8) { return (int)sizeof(Items) + waves * (nt * 1024 + kXsBytes); }
+const KernelInfo kInfoGemvFp4 = {"gemv_fp4_kernel", "fgg_moe_gemv_fp4", 16, 16, 128, 512, 0, 0, gemv_lds(1),
+                                 gemv_lds(1), (const void*)gemv_fp4_kernel<kPlain, true, uint16_t, 16, 1>};
+const KernelInfo kInfoGemvFp4Silu = {"gemv_fp4_kernel<silu>", "fgg_moe_gemv_fp4", 16, 16, 128, 512, 0, 0,
                                      gemv_lds(2), gemv_lds(2),
-                                     (const void*)gemv_fp4_kernel<kSilu, true, uint16_t, 16>};
-const KernelInfo kInfoGemvFp4Sum = {"gemv_fp4_kernel<sum>", "fgg_moe_gemv_fp4", 16, 16, 128, 64 * kMaxWaves, 0, 0,
-                                    gemv_lds(1), gemv_lds(1), (const void*)gemv_fp4_kernel<kSum, true, uint16_t, 16>};
+                                     (const void*)gemv_fp4_kernel<kSilu, true, uint16_t, 16, 1>};
+const KernelInfo kInfoGemvFp4Sum = {"gemv_fp4_kernel<sum>", "fgg_moe_gemv_fp4", 16, 16, 128, 512, 0, 0,
+                                    gemv_lds(1), gemv_lds(1), (const void*)gemv_fp4_kernel<kSum, true, uint16_t, 16, 1>};
+const KernelInfo kInfoGemvFp4Sum2 = {"gemv_fp4_kernel<sum, two tiles>", "fgg_moe_gemv_fp4", 32, 16, 128, 1024, 0, 0,
+                                     gemv_lds(2, 16), gemv_lds(2, 16),
+                                     (const void*)gemv_fp4_kernel<kSum, true, uint16_t, 16, 2>};
 
 hipError_t launch_gemv_fp4(bool tiled, int32_t G, int64_t T, int32_t k, int64_t N, int64_t K, const void* x,
                            bool x_bf16, int64_t ldx, bool per_slot, const uint8_t* b, const uint8_t* s,
@@ -581,20 +586,34 @@ hipError_t launch_gemv_fp4(bool tiled, int32_t G, int64_t T, int32_t k, int64_t 
   const GemvArgs a = {G, T, k, N, K, x, ldx, per_slot, b, s, ids, w, out, out_bf16, ldo};
   const int64_t pairs = (T < 16 ? T : 16) * k;
   const unsigned visits = ids && !w ? (unsigned)(pairs < G ? pairs : G) : 1;
-  const int waves = !w && K <= 2048 ? 4 : kMaxWaves;   // a span of 512 K for each
+  // The summed form with many tokens: two row tiles a wave (twice the bytes in flight, half the
+  // activations' loads) and sixteen waves a workgroup, one of which fills a compute unit.  Down of
+  // 16 tokens over 32 experts (N 7168, K 2048), tiled, 57.6 -> 49.3 us, of 8 tokens 46.9 -> 45.3; of one
+  // token 15.3 -> 15.5; untiled 16 tokens 64.1 -> 63.4 among other calls, 8 tokens 54.7 -> 59.0.
+  const int rt = w && x_bf16 && tiled && T > 4 && (N + 31) / 32 >= num_cus * 3 / 4 ? 2 : 1;
+  const int waves = rt == 2 ? 16 : !w && K <= 2048 ? 4 : 8;   // a span of 512 K for each
   // Tiles per workgroup: two workgroups fill a compute unit, and more of them than that only repeat the
   // start (the list, the first loads).  Gate-up of one token, 8 and 32 experts: 25.1 -> 24.0 and
   // 100 -> 86 us; 8 tokens 129 -> 102; with fewer workgroups the loop would cost 4 us a tile.
-  const int64_t tiles = (N + 15) / 16;
+  const int64_t tiles = (N + 16 * rt - 1) / (16 * rt);
   int64_t loop = w ? 1 : tiles * visits / (2 * num_cus);
   loop = loop < 1 ? 1 : loop > 4 ? 4 : loop;
   const dim3 grid((unsigned)((tiles + loop - 1) / loop), visits, (unsigned)((T + 15) / 16));
-  const KernelInfo& info = w ? kInfoGemvFp4Sum : silu ? kInfoGemvFp4Silu : kInfoGemvFp4;
+  const KernelInfo& info = w && rt == 2 ? kInfoGemvFp4Sum2 : w ? kInfoGemvFp4Sum : silu ? kInfoGemvFp4Silu : kInfoGemvFp4;
   trace_launch(info, grid, "G=%d T=%lld k=%d N=%lld K=%lld %s %s->%s", (int)G, (long long)T, (int)k, (long long)N,
                (long long)K, tiled ? "tiled" : "rows", x_bf16 ? "bf16" : "fp32", out_bf16 ? "bf16" : "fp32");
   auto go = [&](auto mode, auto til, auto tx, auto nc) {
-    hipLaunchKernelGGL((gemv_fp4_kernel<decltype(mode)::value, decltype(til)::value, decltype(tx), decltype(nc)::value>),
-                       grid, dim3(64 * waves), 0, st, a);
+    constexpr int M = decltype(mode)::value;
+    using TX = decltype(tx);
+    if constexpr (M == kSum && decltype(til)::value && sizeof(TX) == 2 && decltype(nc)::value == 16) {
+      if (rt == 2) {
+        hipLaunchKernelGGL((gemv_fp4_kernel<M, decltype(til)::value, TX, decltype(nc)::value, 2>), grid,
+                           dim3(64 * waves), 0, st, a);
+        return;
+      }
+    }
+    hipLaunchKernelGGL((gemv_fp4_kernel<M, decltype(til)::value, TX, decltype(nc)::value, 1>), grid, dim3(64 * waves),
+                       0, st, a);
   };
   using std::integral_constant;
   auto with_type = [&](auto mode, auto til) {

@@ -48,7 +48,17 @@ CASES = [  # T, G, k, N, K, tiled
     (16, 1, 1, 528, 1024, True), (17, 1, 1, 100, 2080, False), (40, 1, 1, 64, 256, True),
     (1, 32, 8, 256, 512, True), (2, 4, 3, 33, 96, False), (16, 8, 2, 160, 640, True), (13, 32, 8, 77, 1312, False),
     (5, 1024, 4, 16, 128, True), (16, 70, 64, 18, 64, False), (33, 6, 2, 48, 384, True),
+    (12, 3, 3, 97, 2656, False), (10, 40, 5, 1040, 1152, True), (16, 2, 1, 31, 4096, False),
 ]
+
+
+@pytest.fixture(params=[0, 1], ids=["all CUs", "1 CU"], autouse=True)
+def cus(request):
+    """Also with the launch rules of a single compute unit: several tiles a workgroup, and two tiles
+    a wave in the summed form whatever the number of columns."""
+    fgg.set_num_cus(request.param)
+    yield request.param
+    fgg.set_num_cus(0)
 
 
 def _ids(seed, T, G, k, drop=0.15):
