@@ -19,7 +19,8 @@ from _util import cuda, to_np
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
 SHAPES = [(1, 1, 1, 1), (1, 8, 256, 2048), (5, 2, 3, 7), (33, 3, 5, 515), (64, 2, 4, 4096), (17, 64, 90, 129),
-          (300, 4, 16, 1001), (9, 8, 64, 8200), (130, 6, 8, 1023), (3, 1, 2, 16384)]
+          (300, 4, 16, 1001), (9, 8, 64, 8200), (130, 6, 8, 1023), (3, 1, 2, 16384), (41, 5, 7, 8), (70, 2, 3, 12), (66, 8, 9, 500), (10, 3, 4, 513),
+          (10, 3, 4, 1025)]
 
 
 def _half(dtype):
@@ -108,6 +109,31 @@ def test_gradients(T, k, E, N, dtype):
         alone, none = fgg.moe_unpermute_rows_backward(xd, p["src_to_row"], p["row_to_src"], p["offsets"], topk_w=wg,
                                                       out=out)
         assert none is None and torch.equal(alone, dr)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N", [1, 3, 5, 9, 13, 250, 500, 515, 1027, 2049])
+def test_infinities_at_every_end_of_a_row(N, dtype):
+    """One row holds an infinity in column c, the token a one everywhere: the product is that
+    infinity, not a NaN, whichever columns are loaded twice; the other way round alike."""
+    cols = sorted({c for c in [0, 1, 2] + list(range(N - 18, N)) if 0 <= c < N})
+    T = len(cols)
+    p = fgg.moe_permute(cuda(np.zeros((T, 1), np.int32)), 1)
+    s2r = p["src_to_row"]
+    x, rows = torch.ones(T, N, device="cuda"), torch.ones(p["m_cap"], N, device="cuda")
+    w = torch.ones(T, 1, device="cuda")
+    for inf_in_rows in (True, False):
+        a, b = x.clone(), rows.clone()
+        for t, c in enumerate(cols):
+            if inf_in_rows:
+                b[s2r[t].long(), c] = float("inf")
+            else:
+                a[t, c] = float("inf")
+        a, b = a.to(dtype), b.to(dtype)
+        _, dw = fgg.moe_permute_rows_backward(b, s2r, T, topk_w=w, x=a)
+        assert (dw == float("inf")).all()
+        _, dw = fgg.moe_unpermute_rows_backward(a, s2r, p["row_to_src"], p["offsets"], topk_w=w, rows=b)
+        assert (dw == float("inf")).all()
 
 
 def test_combine_bit_for_bit():
