@@ -123,6 +123,40 @@ __device__ inline float sigmoid_scaled(float v, float m) {
 // difference of far logits end there).
 __device__ inline float exp_below(float x, float m) { return exp_neg(fminf(m - x, 200.0f)); }
 
+// e^x in 64 bits for x <= 0 (a NaN stays one): x = n ln 2 + r with |r| <= ln 2 / 2, and Taylor's polynomial to
+// r^13 / 13! (the next term is 4e-18).  Below -750 all is 0.
+__device__ inline double exp64_nonpos(double x) {
+  x = x < -750.0 ? -750.0 : x;
+  const double n = __builtin_rint(x * 1.4426950408889634074);
+  double r = fma(n, -0.69314718055994530942, x);
+  r = fma(n, -2.3190468138462996e-17, r);             // (ln 2 beyond its first 53 bits)
+  double p = 1.0 / 6227020800.0;
+  p = fma(p, r, 1.0 / 479001600.0);
+  p = fma(p, r, 1.0 / 39916800.0);
+  p = fma(p, r, 1.0 / 3628800.0);
+  p = fma(p, r, 1.0 / 362880.0);
+  p = fma(p, r, 1.0 / 40320.0);
+  p = fma(p, r, 1.0 / 5040.0);
+  p = fma(p, r, 1.0 / 720.0);
+  p = fma(p, r, 1.0 / 120.0);
+  p = fma(p, r, 1.0 / 24.0);
+  p = fma(p, r, 1.0 / 6.0);
+  p = fma(p, r, 0.5);
+  p = fma(p, r, 1.0);
+  p = fma(p, r, 1.0);
+  return __builtin_amdgcn_ldexp(p, (int)n);
+}
+
+// The sigmoid in 64 bits: e^-|x| is at most 1, so nothing overflows; the reciprocal of 1 + e^-|x|, in [1/2, 1],
+// is the hardware's estimate with two Newton steps.
+__device__ inline double sigmoid64(float x) {
+  const double e = exp64_nonpos(-(double)fabsf(x)), a = 1.0 + e;
+  double y = __builtin_amdgcn_rcp(a);
+  y = fma(fma(-a, y, 1.0), y, y);
+  y = fma(fma(-a, y, 1.0), y, y);
+  return x < 0.0f ? e * y : y;
+}
+
 // The group's lane `src` (0 <= src < GW, the same in the group) of v.
 template <int GW>
 __device__ inline int group_lane(int v, int src) {
@@ -163,6 +197,8 @@ __global__ void __launch_bounds__(256) route_kernel(const TI* __restrict__ logit
   float x[EPL];
   int bad = 0;                                        // a NaN in the row (or +inf under a softmax)
   load_experts<EPL>(row, gl * EPL, live ? E : 0, x);
+  float add[EPL];
+  if constexpr (BIAS) load_experts<EPL>(bias, gl * EPL, E, add);
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     bad |= __builtin_amdgcn_classf(x[i], sigmoid ? 0x003 : 0x203);   // NaN (and +inf)
@@ -189,21 +225,21 @@ __global__ void __launch_bounds__(256) route_kernel(const TI* __restrict__ logit
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const bool shut = !(x[i] > -kInf);
       if (sigmoid) {
-        s[i] = 1.0 / (1.0 + exp(-(double)x[i]));
+        s[i] = sigmoid64(x[i]);
       } else {
-        s[i] = shut ? 0.0 : exp((double)x[i] - (double)m_all);
+        s[i] = x[i] > -kInf ? exp64_nonpos((double)x[i] - (double)m_all) : 0.0;
         sum += s[i];
       }
     }
-    if (!sigmoid) sum = group_reduce<GW>(sum, OpAdd());
+    if (!sigmoid) {
+      const double inv = 1.0 / group_reduce<GW>(sum, OpAdd());
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) s[i] *= inv;
+    }
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const int e = gl * EPL + i;
-      double c = sigmoid ? s[i] : s[i] / sum;
-      if (!(c == c)) c = 0.0;                         // a row with NaN or +inf: by the bias alone
-      c += e < E ? (double)bias[e] : 0.0;
+      const double c = (s[i] == s[i] ? s[i] : 0.0) + (double)add[i];   // a row with NaN or +inf: by the bias alone
       key[i] = (x[i] > -kInf && c > -(double)kInf) ? order_key(c) : 0;
     }
   } else {
@@ -211,41 +247,60 @@ __global__ void __launch_bounds__(256) route_kernel(const TI* __restrict__ logit
     for (int i = 0; i < EPL; ++i) key[i] = x[i] > -kInf ? order_key(x[i]) : 0;
   }
 
-  // k rounds.  The lane's candidate: up to four experts are sorted once (equal keys keep their order)
-  // and the lane that gave the largest moves its queue up; more are searched each round.  Lanes
-  // hold ascending experts, so of equal keys the first lane's is the lower expert.
-  constexpr bool kQueue = EPL <= 4;
-  int at[EPL];
+  // k rounds.  A lane's experts are sorted once, in queues of up to four (equal keys keep their order), the
+  // places of a queue in the bytes of one word; the lane's candidate is the largest head, and the lane that gave
+  // the largest of all moves that queue up.  Queues and lanes hold ascending experts, so of equal keys the
+  // first is the lower expert.
+  constexpr int Q = EPL < 4 ? EPL : 4, NQ = EPL / Q;
+  uint32_t at[NQ];
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) at[i] = gl * EPL + i;
-  if constexpr (kQueue) {
+  for (int q = 0; q < NQ; ++q) {
+    uint32_t p[Q];
 #pragma unroll
-    for (int end = EPL - 1; end > 0; --end)
+    for (int i = 0; i < Q; ++i) p[i] = q * Q + i;
+#pragma unroll
+    for (int end = Q - 1; end > 0; --end)
 #pragma unroll
       for (int i = 0; i < end; ++i) {
-        const bool swap = key[i + 1] > key[i];
-        const Key hi = swap ? key[i + 1] : key[i], lo = swap ? key[i] : key[i + 1];
-        const int ahi = swap ? at[i + 1] : at[i], alo = swap ? at[i] : at[i + 1];
-        key[i] = hi, key[i + 1] = lo, at[i] = ahi, at[i + 1] = alo;
+        Key &ka = key[q * Q + i], &kb = key[q * Q + i + 1];
+        const bool swap = kb > ka;
+        const Key hi = swap ? kb : ka, lo = swap ? ka : kb;
+        const uint32_t phi = swap ? p[i + 1] : p[i], plo = swap ? p[i] : p[i + 1];
+        ka = hi, kb = lo, p[i] = phi, p[i + 1] = plo;
       }
+    at[q] = p[0];
+#pragma unroll
+    for (int i = 1; i < Q; ++i) at[q] |= p[i] << (8 * i);
   }
   const int base = lane & ~(GW - 1);                  // the group's first lane
   int my_id = -1;
   float my_v = 0.0f;
   for (int j = 0; j < k; ++j) {
     Key best = key[0];
-    int bi = 0;
-    if constexpr (!kQueue) {
+    uint32_t place = at[0];
+    int bq = 0;
 #pragma unroll
-      for (int i = 1; i < EPL; ++i)
-        if (key[i] > best) best = key[i], bi = i;
+    for (int q = 1; q < NQ; ++q)
+      if (key[q * Q] > best) best = key[q * Q], place = at[q], bq = q;
+    uint32_t top;                                     // (of 64-bit keys the upper half: 0 only if all is)
+    uint64_t heads;
+    if constexpr (BIAS) {
+      const uint32_t hi = (uint32_t)(best >> 32);
+      top = group_reduce<GW>(hi, OpMax());
+      heads = __ballot(hi == top);
+      if (__popcll(heads) > 64 / GW) {                // some group has equal upper halves
+        const uint32_t lo = hi == top ? (uint32_t)best : 0u;
+        const uint32_t top_lo = group_reduce<GW>(lo, OpMax());
+        heads = __ballot(hi == top && lo == top_lo);
+      }
+    } else {
+      top = group_reduce<GW>(best, OpMax());
+      heads = __ballot(best == top);
     }
-    const Key top = group_reduce<GW>(best, OpMax());
-    const uint64_t heads = __ballot(best == top);
     int src, e;
     if constexpr (GW == 64) {
       src = __ffsll((unsigned long long)heads) - 1;
-      e = __builtin_amdgcn_readlane(kQueue ? at[0] : gl * EPL + bi, src);
+      e = EPL == 1 ? src : src * EPL + (__builtin_amdgcn_readlane((int)place, src) & 0xFF);
     } else {
       src = __ffs((uint32_t)(heads >> base) & (uint32_t)((1ull << GW) - 1)) - 1;
       e = src;                                        // (one expert per lane)
@@ -256,12 +311,11 @@ __global__ void __launch_bounds__(256) route_kernel(const TI* __restrict__ logit
     }
     if (gl == src) {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        if constexpr (kQueue) {
-          key[i] = i + 1 < EPL ? key[i + 1 < EPL ? i + 1 : i] : 0;
-          at[i] = at[i + 1 < EPL ? i + 1 : i];
-        } else {
-          if (i == bi) key[i] = 0;
+      for (int q = 0; q < NQ; ++q) {
+        if (q == bq) {
+#pragma unroll
+          for (int i = 0; i < Q; ++i) key[q * Q + i] = i + 1 < Q ? key[q * Q + (i + 1 < Q ? i + 1 : i)] : 0;
+          at[q] >>= 8;
         }
       }
     }

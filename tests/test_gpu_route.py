@@ -77,6 +77,36 @@ def test_ties_go_to_the_lower_expert():
         assert got[5].tolist() == [-1] * 5
 
 
+@pytest.mark.parametrize("E", [3, 16, 30, 61, 100, 250, 500, 1000])
+@pytest.mark.parametrize("gate", ["softmax", "sigmoid"])
+def test_keys_that_differ_in_their_low_bits(E, gate):
+    """Equal scores, biases 2^-24 apart in [0.5, 1): 32 bits would hold them, the keys' upper halves (20 bits of
+    fraction) do not; every third bias repeats the one before, a tie for the lower expert."""
+    g = synth.rng(E)
+    step = g.permutation(E)
+    step[2::3] = step[1::3][:len(step[2::3])]
+    bias = (0.5 + step * 2.0 ** -24).astype(np.float32)
+    x = np.full((5, E), -1.5, np.float32)
+    x[1, E // 2] = 4.0
+    x[2, ::2] = -np.inf
+    k = min(E, 20)
+    ids, w = fgg.moe_route(cuda(x), k, gate, bias=cuda(bias), renormalize=True)
+    ref_ids, ref_w = oracle.moe_route(x, k, gate, bias, True, 1.0)
+    assert np.array_equal(to_np(ids), ref_ids)
+    _check_weights(to_np(w), ref_w, x, gate)
+
+
+def test_saturated_scores_with_a_bias():
+    """Scores that round to 0 or 1, or lie far apart: the bias orders them."""
+    x = np.array([[100.0, 50.0, -800.0, -1000.0, 3e38, -3e38, 0.0, 1.0]], np.float32)
+    bias = np.array([0.1, 0.2, 0.05, 0.06, 0.15, 0.07, -0.6, -0.7], np.float32)
+    for gate in ("softmax", "sigmoid"):
+        ids, w = fgg.moe_route(cuda(x), 8, gate, bias=cuda(bias))
+        ref_ids, ref_w = oracle.moe_route(x, 8, gate, bias, False, 1.0)
+        assert np.array_equal(to_np(ids), ref_ids)
+        _check_weights(to_np(w), ref_w, np.array([0.0, 104.0]), gate)
+
+
 def test_extreme_logits():
     low, top = np.float32(-3e38), np.float32(3e38)
     x = np.array([[low, low, 0, 0], [top, low, 0, 0], [-200, -201, -300, -250], [low, -np.inf, -np.inf, -np.inf],
