@@ -15,13 +15,15 @@
 //
 // Bound by instruction issue, not by memory: one token is one wave's few hundred vector
 // instructions.  8192 tokens x 256 experts, bf16, top-8 (4.7 MB, 1 us at a large copy's rate):
-// 7.7 us; with a search and two reductions a round 10.1 (a round is one reduction now, the tie
-// being the first lane of a ballot, and a queue step).  Gradient, 16384 x 160 fp32, top-6 (21.8 MB):
-// 10 us (12.8 with gathered scores and element-wise loads).  One token: 4.7 us, a launch.
+// 7.1 us; with a search and two reductions a round 10.1 (a round is one reduction, the tie being the first lane of
+// a ballot, and a queue step); 16384 x 384 fp32 16.0 us, 19.6 with a search over eight.  Gradient, 16384 x 160
+// fp32, top-6 (21.8 MB): 9 us (12.8 with gathered scores and element-wise loads).  One token: 3.9 us, a launch.
 //
 // With a bias the keys are sums of rounded scores, and two experts whose keys differ by
-// less than the rounding of 32 bits would be ordered by it: keys are formed in 64 bits
-// (the sigmoid or exponential of every logit in double), and ranked as 64-bit integers.
+// less than the rounding of 32 bits would be ordered by it.  The experts are chosen in 32 bits, and a wave in
+// which some token has two of its first k + 1 keys closer than those roundings forms its keys in 64 bits (the sigmoid
+// or exponential of every logit in double) and chooses again.  16384 x 384 fp32, top-8, sigmoid: 23.2 us, with all keys
+// in 64 bits 35.6 (48.2 with the library's exponential and reductions of 64-bit keys).
 #include "fgg_device.hpp"
 #include "fgg_internal.hpp"
 #include "fgg_wave.hpp"
@@ -36,39 +38,47 @@ __device__ inline float load_one(const float* p) { return *p; }
 __device__ inline float load_one(const uint16_t* p) { return bf16_to_f32(*p); }
 
 // Experts [e, e + EPL) of a row, -inf from E on; and the same elements stored.  Whole groups move as
-// vectors of the element's alignment (this part's vector memory takes any).
-template <int EPL>
-__device__ inline void load_experts(const float* row, int e, int E, float (&x)[EPL]) {
-  typedef float Vec __attribute__((ext_vector_type(EPL), aligned(4)));
-  if (e + EPL <= E) {
-    if constexpr (EPL == 1) {
-      x[0] = row[e];
-    } else {
-      const Vec v = *reinterpret_cast<const Vec*>(row + e);
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) x[i] = v[i];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) x[i] = e + i < E ? row[e + i] : -kInf;
+// vectors of the element's alignment (this part's vector memory takes any).  A load has no branch around it (the
+// row's last EPL experts are read instead of what is behind the row, E >= EPL), so several stay in flight; its
+// elements are put in place after it.
+template <int EPL, class T>
+struct Experts {
+  typedef T Vec __attribute__((ext_vector_type(EPL), aligned(sizeof(T))));
+  Vec v;
+  __device__ void load(const T* row, int e, int E) {
+    const int at = e + EPL <= E ? e : E - EPL;
+    v = *reinterpret_cast<const Vec*>(row + at);
   }
-}
-template <int EPL>
-__device__ inline void load_experts(const uint16_t* row, int e, int E, float (&x)[EPL]) {
-  typedef uint16_t Vec __attribute__((ext_vector_type(EPL), aligned(2)));
-  if (e + EPL <= E) {
-    if constexpr (EPL == 1) {
-      x[0] = bf16_to_f32(row[e]);
-    } else {
-      const Vec v = *reinterpret_cast<const Vec*>(row + e);
+  __device__ void get(int e, int E, float (&x)[EPL]) const {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) x[i] = bf16_to_f32(v[i]);
+    for (int i = 0; i < EPL; ++i) {
+      if constexpr (sizeof(T) == 2) x[i] = bf16_to_f32(v[i]);
+      else x[i] = v[i];
     }
-  } else {
+    if (e + EPL > E) {
+      const int down = e + EPL - E;                   // (EPL and more: none is in the row)
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) x[i] = e + i < E ? bf16_to_f32(row[e + i]) : -kInf;
+      for (int d = 1; d < EPL; d *= 2)
+        if (down & d) {
+#pragma unroll
+          for (int i = 0; i < EPL; ++i) x[i] = i + d < EPL ? x[i + d < EPL ? i + d : i] : -kInf;
+        }
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) x[i] = e + i < E ? x[i] : -kInf;
+    }
   }
-}
+};
+template <class T>
+struct Experts<1, T> {
+  T v;
+  __device__ void load(const T* row, int e, int E) { v = row[e < E ? e : E - 1]; }
+  __device__ void get(int e, int E, float (&x)[1]) const {
+    float f;
+    if constexpr (sizeof(T) == 2) f = bf16_to_f32(v);
+    else f = v;
+    x[0] = e < E ? f : -kInf;
+  }
+};
 template <int EPL>
 __device__ inline void store_experts(float* row, int e, int E, const float (&x)[EPL]) {
   typedef float Vec __attribute__((ext_vector_type(EPL), aligned(4)));
@@ -184,73 +194,13 @@ __device__ inline float gate_weight(float v, bool on, bool sigmoid, bool renorm,
   return on ? num / sum : 0.0f;
 }
 
-}  // namespace
-
-template <class TI, int GW, int EPL, bool BIAS>
-__global__ void __launch_bounds__(256) route_kernel(const TI* __restrict__ logits, int64_t T, int E, int64_t ld, int k,
-                                                    bool sigmoid, const float* __restrict__ bias, bool renorm,
-                                                    float scale, int32_t* __restrict__ ids, float* __restrict__ w) {
-  const int lane = threadIdx.x & 63, gl = lane & (GW - 1);
-  const int64_t t = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * (64 / GW) + lane / GW;
-  const bool live = t < T;
-  const TI* row = logits + (live ? t : 0) * ld;
-  float x[EPL];
-  int bad = 0;                                        // a NaN in the row (or +inf under a softmax)
-  load_experts<EPL>(row, gl * EPL, live ? E : 0, x);
-  float add[EPL];
-  if constexpr (BIAS) load_experts<EPL>(bias, gl * EPL, E, add);
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    bad |= __builtin_amdgcn_classf(x[i], sigmoid ? 0x003 : 0x203);   // NaN (and +inf)
-  }
-  bad = group_reduce<GW>(bad, OpMax());
-
-  // the softmax's maximum and normalizer, where something depends on every expert
-  float m_all = -kInf, sum_all = 0.0f;
-  if (!sigmoid && (BIAS || !renorm)) {
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) m_all = fmaxf(m_all, x[i]);
-    m_all = group_reduce<GW>(m_all, OpFMax());
-    if (!renorm) {
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) sum_all += exp_below(x[i], m_all);
-      sum_all = group_reduce<GW>(sum_all, OpAdd());
-    }
-  }
-
-  using Key = typename std::conditional<BIAS, uint64_t, uint32_t>::type;
-  Key key[EPL];
-  if constexpr (BIAS) {
-    double s[EPL];
-    double sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      if (sigmoid) {
-        s[i] = sigmoid64(x[i]);
-      } else {
-        s[i] = x[i] > -kInf ? exp64_nonpos((double)x[i] - (double)m_all) : 0.0;
-        sum += s[i];
-      }
-    }
-    if (!sigmoid) {
-      const double inv = 1.0 / group_reduce<GW>(sum, OpAdd());
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) s[i] *= inv;
-    }
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const double c = (s[i] == s[i] ? s[i] : 0.0) + (double)add[i];   // a row with NaN or +inf: by the bias alone
-      key[i] = (x[i] > -kInf && c > -(double)kInf) ? order_key(c) : 0;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) key[i] = x[i] > -kInf ? order_key(x[i]) : 0;
-  }
-
-  // k rounds.  A lane's experts are sorted once, in queues of up to four (equal keys keep their order), the
-  // places of a queue in the bytes of one word; the lane's candidate is the largest head, and the lane that gave
-  // the largest of all moves that queue up.  Queues and lanes hold ascending experts, so of equal keys the
-  // first is the lower expert.
+// The k largest keys of a group, in `rounds` >= k rounds: lane j gets round j's key (of 64-bit keys the upper half,
+// 0 only where the whole is) and expert, -1 where none is left.  A lane's experts are sorted once, in queues of up to
+// four (equal keys keep their order), the places of a queue in the bytes of one word; the lane's candidate is the
+// largest head, and the lane that gave the largest of all moves that queue up.  Queues and lanes hold ascending
+// experts, so of equal keys the first is the lower expert.  Consumes the keys.
+template <int GW, int EPL, class Key>
+__device__ inline void select_largest(Key (&key)[EPL], int rounds, int gl, int& my_id, uint32_t& my_key) {
   constexpr int Q = EPL < 4 ? EPL : 4, NQ = EPL / Q;
   uint32_t at[NQ];
 #pragma unroll
@@ -272,19 +222,18 @@ __global__ void __launch_bounds__(256) route_kernel(const TI* __restrict__ logit
 #pragma unroll
     for (int i = 1; i < Q; ++i) at[q] |= p[i] << (8 * i);
   }
-  const int base = lane & ~(GW - 1);                  // the group's first lane
-  int my_id = -1;
-  float my_v = 0.0f;
-  for (int j = 0; j < k; ++j) {
+  const int base = (threadIdx.x & 63) & ~(GW - 1);    // the group's first lane
+  my_id = -1, my_key = 0;
+  for (int j = 0; j < rounds; ++j) {
     Key best = key[0];
     uint32_t place = at[0];
     int bq = 0;
 #pragma unroll
     for (int q = 1; q < NQ; ++q)
       if (key[q * Q] > best) best = key[q * Q], place = at[q], bq = q;
-    uint32_t top;                                     // (of 64-bit keys the upper half: 0 only if all is)
+    uint32_t top;
     uint64_t heads;
-    if constexpr (BIAS) {
+    if constexpr (sizeof(Key) == 8) {
       const uint32_t hi = (uint32_t)(best >> 32);
       top = group_reduce<GW>(hi, OpMax());
       heads = __ballot(hi == top);
@@ -305,10 +254,7 @@ __global__ void __launch_bounds__(256) route_kernel(const TI* __restrict__ logit
       src = __ffs((uint32_t)(heads >> base) & (uint32_t)((1ull << GW) - 1)) - 1;
       e = src;                                        // (one expert per lane)
     }
-    if (gl == j && top != 0) {
-      my_id = e;
-      if constexpr (!BIAS) my_v = order_value(top);
-    }
+    if (gl == j && top != 0) my_id = e, my_key = top;
     if (gl == src) {
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
@@ -320,6 +266,100 @@ __global__ void __launch_bounds__(256) route_kernel(const TI* __restrict__ logit
       }
     }
   }
+}
+
+}  // namespace
+
+template <class TI, int GW, int EPL, bool BIAS>
+__global__ void __launch_bounds__(256) route_kernel(const TI* __restrict__ logits, int64_t T, int E, int64_t ld, int k,
+                                                    bool sigmoid, const float* __restrict__ bias, bool renorm,
+                                                    float scale, int32_t* __restrict__ ids, float* __restrict__ w) {
+  const int lane = threadIdx.x & 63, gl = lane & (GW - 1);
+  const int64_t t = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * (64 / GW) + lane / GW;
+  const bool live = t < T;
+  const TI* row = logits + (live ? t : 0) * ld;
+  float x[EPL], add[EPL];
+  int bad = 0;                                        // a NaN in the row (or +inf under a softmax)
+  Experts<EPL, TI> in;
+  Experts<EPL, float> in_bias;
+  in.load(row, gl * EPL, E);
+  if constexpr (BIAS) in_bias.load(bias, gl * EPL, E);
+  in.get(gl * EPL, E, x);
+  if constexpr (BIAS) in_bias.get(gl * EPL, E, add);
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    bad |= __builtin_amdgcn_classf(x[i], sigmoid ? 0x003 : 0x203);   // NaN (and +inf)
+  }
+  bad = group_reduce<GW>(bad, OpMax());
+
+  // the softmax's maximum and normalizer, where something depends on every expert
+  float m_all = -kInf, sum_all = 0.0f, s[EPL];
+  if (!sigmoid && (BIAS || !renorm)) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) m_all = fmaxf(m_all, x[i]);
+    m_all = group_reduce<GW>(m_all, OpFMax());
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) sum_all += s[i] = exp_below(x[i], m_all);
+    sum_all = group_reduce<GW>(sum_all, OpAdd());
+    const float inv = __builtin_amdgcn_rcpf(sum_all);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) s[i] *= inv;
+  } else if (BIAS) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) s[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x[i] * -1.44269504f));
+  }
+
+  int my_id;
+  uint32_t my_key, key[EPL];
+  if constexpr (BIAS) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const float c = s[i] + add[i];
+      key[i] = (x[i] > -kInf && c > -kInf) ? order_key(c) : 0;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = x[i] > -kInf ? order_key(x[i]) : 0;
+  }
+  if constexpr (BIAS) {
+    // One more round than k, where a lane is left for it, shows what the last was chosen over.  A 32-bit key is off
+    // by at most 2^-21 (sigmoid: a few roundings of a number up to 1, and of x, worth |x| s (1 - s) < 1/4 of one) or
+    // 2^-18 of the largest score (softmax: the sum's 22 roundings), and 2^-23 of itself: an order with gaps of twice
+    // that is the order of the exact keys.
+    select_largest<GW, EPL>(key, k < GW ? k + 1 : k, gl, my_id, my_key);
+    const uint32_t next = __shfl_down(my_key, 1, GW);
+    const float v = order_value(my_key);
+    const float apart = (sigmoid ? 0x1p-19f : 0x1p-17f * __builtin_amdgcn_rcpf(sum_all)) + fabsf(v) * 0x1p-21f;
+    const bool close = gl == GW - 1 ? E > GW : next != 0 && !(v - order_value(next) > apart);
+    const bool again = bad || (gl < k && my_key != 0 && close);
+    if (__any(again)) {
+      uint64_t key64[EPL];
+      double sum = 0.0, d[EPL];
+      if (sigmoid) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) d[i] = sigmoid64(x[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          d[i] = x[i] > -kInf ? exp64_nonpos((double)x[i] - (double)m_all) : 0.0;
+          sum += d[i];
+        }
+        const double inv = 1.0 / group_reduce<GW>(sum, OpAdd());
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) d[i] *= inv;
+      }
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const double c = (d[i] == d[i] ? d[i] : 0.0) + (double)add[i];   // a row with NaN or +inf: by the bias alone
+        key64[i] = (x[i] > -kInf && c > -(double)kInf) ? order_key(c) : 0;
+      }
+      select_largest<GW, EPL>(key64, k, gl, my_id, my_key);
+    }
+    if (gl >= k) my_id = -1;
+  } else {
+    select_largest<GW, EPL>(key, k, gl, my_id, my_key);
+  }
+  float my_v = BIAS ? 0.0f : order_value(my_key);
   if (BIAS && my_id >= 0) my_v = load_one(row + my_id);           // (in the cache: the row was just read)
   const bool on = my_id >= 0;
   float g = gate_weight<GW>(my_v, on, sigmoid, renorm, m_all, sum_all) * scale;
@@ -375,7 +415,9 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const TI* __restric
   if (whole) {
     float x[EPL], m = -kInf, sum = 0.0f, dot = 0.0f;
     bool bad = false;
-    load_experts<EPL>(row, gl * EPL, live ? E : 0, x);
+    Experts<EPL, TI> in;
+    in.load(row, gl * EPL, E);
+    in.get(gl * EPL, E, x);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
       m = fmaxf(m, x[i]);
