@@ -182,27 +182,28 @@ struct Items {
   float gate[kMaxPairs];            // gate weights (the summed form)
 };
 
-// The list of at most 64 pairs, by each wave on its own: lane p holds pair p and looks at the
-// pairs before it one by one.  Every wave writes the same values to LDS and reads only what it
+// The list of at most 64 pairs, by each wave on its own: lane p holds pair p, and each distinct expert's
+// pairs are one ballot.  Every wave writes the same values to LDS and reads only what it
 // wrote itself, so there is no barrier.
 __device__ inline int list_few_items(Items& L, const int32_t* ids, int64_t t0, int P, int k, int G) {
-  const int p = threadIdx.x & 63, t = p / k;
+  const int p = threadIdx.x & 63;
   int e = p < P ? ids[t0 * k + p] : -1;
   if (e < 0 || e >= G) e = -1;
-  int again = 0, covered = 0;
-  for (int q = 0; q + 1 < P; ++q) {
-    const int eq = __builtin_amdgcn_readlane(e, q), aq = __builtin_amdgcn_readlane(again, q);
-    if (p > q && e == eq) {
-      if (t == q / k) again = 1;
-      else if (!aq) covered = 1;
-    }
+  uint64_t same = 0;                                  // the pairs that name this pair's expert
+  for (uint64_t left = __ballot(e >= 0); left;) {
+    const int head = __builtin_amdgcn_readlane(e, __ffsll((unsigned long long)left) - 1);
+    const uint64_t m = __ballot(e == head);
+    if (e == head) same = m;
+    left &= ~m;
   }
-  const bool lead = e >= 0 && (again || !covered);
+  const uint64_t before = (1ull << p) - 1, token = ~0ull << (p / k * k);   // (p / k * k <= p < 64)
+  const bool again = (same & before & token) != 0;
+  const bool lead = e >= 0 && (again || (same & before) == 0);
   const uint64_t m = __ballot(lead);
   if (p < P) {
     L.ids[p] = e;
     L.again[p] = (uint8_t)again;
-    if (lead) L.item[__popcll(m & ((1ull << p) - 1))] = (uint16_t)p;
+    if (lead) L.item[__popcll(m & before)] = (uint16_t)p;
   }
   wave_sync();
   return __popcll(m);
@@ -241,16 +242,6 @@ __device__ inline int list_items(Items& L, const int32_t* ids, int64_t t0, int T
     __syncthreads();
   }
   return __builtin_amdgcn_readfirstlane(total);
-}
-
-// The slot of token `t` (of the workgroup's) that visit `p0` serves, -1: none.
-__device__ inline int slot_of(const Items& L, int p0, int t, int Tn, int k) {
-  const int e = L.ids[p0];
-  if (L.again[p0]) return p0 / k == t ? p0 % k : -1;
-  if (t >= Tn) return -1;
-  for (int j = 0; j < k; ++j)
-    if (L.ids[t * k + j] == e) return j;
-  return -1;
 }
 
 // The weights of NT row tiles of one expert: wave-uniform pointers to each tile's first K block,
@@ -400,10 +391,9 @@ __device__ inline void gemv_run(const Tiles<NT>& w, const TX* const (&xrow)[Frag
 
 }  // namespace
 
-template <int MODE, bool TILED, class TX, int NCMAX, int RT>
-__global__ void __launch_bounds__(RT == 2 ? 1024 : 512, 4) gemv_fp4_kernel(GemvArgs a) {
+template <int MODE, bool TILED, class TX, int NCMAX, int RT, int kWaves>
+__global__ void __launch_bounds__(kWaves == 16 ? 1024 : 512, 4) gemv_fp4_kernel(GemvArgs a) {
   constexpr int NT = MODE == kSilu ? 2 : RT;         // row tiles: gate and up, or RT one below the other
-  constexpr int kWaves = RT == 2 ? 16 : 8;
   __shared__ Items L;
   __shared__ float part[kWaves][NT][16][16];         // [wave][tile][token][row]
   constexpr bool kXs = NCMAX > 4 && sizeof(TX) == 2;
@@ -416,7 +406,8 @@ __global__ void __launch_bounds__(RT == 2 ? 1024 : 512, 4) gemv_fp4_kernel(GemvA
   const int Tn = a.T - t0 < 16 ? (int)(a.T - t0) : 16;
   const int64_t width = MODE == kSilu ? 2 * a.N : a.N;
   // the waves share the K blocks in spans of four
-  const int nkb = (int)((a.K + 127) / 128), spans = (nkb + 3) / 4, waves = blockDim.x >> 6;
+  const int nkb = (int)((a.K + 127) / 128), spans = (nkb + 3) / 4;
+  constexpr int waves = kWaves;
   const TX* x = (const TX*)a.x;
   const bool obf = a.out_bf16;
 
@@ -431,9 +422,19 @@ __global__ void __launch_bounds__(RT == 2 ? 1024 : 512, 4) gemv_fp4_kernel(GemvA
     if (!a.ids) {
       if (lane < 16) L.column[wave][lane] = (uint16_t)(lane < Tn ? lane : 0);
     } else {
-      const int j = slot_of(L, p0, col, Tn, a.k);
-      const uint32_t m = (uint32_t)__ballot(lane < 16 && j >= 0);
-      if (lane < 16 && j >= 0) L.column[wave][__popc(m & ((1u << lane) - 1))] = (uint16_t)(lane + 16 * j);
+      // a token has one slot for a visit: the four lanes of its column look for it.  A pair that is named
+      // again is a visit of its own.
+      const int e = L.ids[p0];
+      const bool alone = L.again[p0];
+      int mine = -1;
+      if (alone) mine = lane == p0 / a.k ? p0 % a.k : -1;
+      else if (col < Tn) {
+        for (int j = c; j < a.k; j += 4)
+          if (L.ids[col * a.k + j] == e && !L.again[col * a.k + j]) mine = j;
+      }
+      const uint64_t found = __ballot(mine >= 0);
+      const uint32_t m = (uint32_t)(found | found >> 16 | found >> 32 | found >> 48) & 0xFFFFu;
+      if (mine >= 0) L.column[wave][__popc(m & ((1u << col) - 1))] = (uint16_t)(col + 16 * mine);
       nc = __popc(m);
     }
     wave_sync();
@@ -569,15 +570,15 @@ __global__ void __launch_bounds__(RT == 2 ? 1024 : 512, 4) gemv_fp4_kernel(GemvA
 
 static constexpr int gemv_lds(int nt, int waves = 8) { return (int)sizeof(Items) + waves * (nt * 1024 + kXsBytes); }
 const KernelInfo kInfoGemvFp4 = {"gemv_fp4_kernel", "fgg_moe_gemv_fp4", 16, 16, 128, 512, 0, 0, gemv_lds(1),
-                                 gemv_lds(1), (const void*)gemv_fp4_kernel<kPlain, true, uint16_t, 16, 1>};
+                                 gemv_lds(1), (const void*)gemv_fp4_kernel<kPlain, true, uint16_t, 16, 1, 8>};
 const KernelInfo kInfoGemvFp4Silu = {"gemv_fp4_kernel<silu>", "fgg_moe_gemv_fp4", 16, 16, 128, 512, 0, 0,
                                      gemv_lds(2), gemv_lds(2),
-                                     (const void*)gemv_fp4_kernel<kSilu, true, uint16_t, 16, 1>};
+                                     (const void*)gemv_fp4_kernel<kSilu, true, uint16_t, 16, 1, 8>};
 const KernelInfo kInfoGemvFp4Sum = {"gemv_fp4_kernel<sum>", "fgg_moe_gemv_fp4", 16, 16, 128, 512, 0, 0,
-                                    gemv_lds(1), gemv_lds(1), (const void*)gemv_fp4_kernel<kSum, true, uint16_t, 16, 1>};
+                                    gemv_lds(1), gemv_lds(1), (const void*)gemv_fp4_kernel<kSum, true, uint16_t, 16, 1, 8>};
 const KernelInfo kInfoGemvFp4Sum2 = {"gemv_fp4_kernel<sum, two tiles>", "fgg_moe_gemv_fp4", 32, 16, 128, 1024, 0, 0,
                                      gemv_lds(2, 16), gemv_lds(2, 16),
-                                     (const void*)gemv_fp4_kernel<kSum, true, uint16_t, 16, 2>};
+                                     (const void*)gemv_fp4_kernel<kSum, true, uint16_t, 16, 2, 16>};
 
 hipError_t launch_gemv_fp4(bool tiled, int32_t G, int64_t T, int32_t k, int64_t N, int64_t K, const void* x,
                            bool x_bf16, int64_t ldx, bool per_slot, const uint8_t* b, const uint8_t* s,
@@ -591,7 +592,7 @@ hipError_t launch_gemv_fp4(bool tiled, int32_t G, int64_t T, int32_t k, int64_t 
   // 16 tokens over 32 experts (N 7168, K 2048), tiled, 57.6 -> 49.3 us, of 8 tokens 46.9 -> 45.3; of one
   // token 15.3 -> 15.5; untiled 16 tokens 64.1 -> 63.4 among other calls, 8 tokens 54.7 -> 59.0.
   const int rt = w && x_bf16 && tiled && T > 4 && (N + 31) / 32 >= num_cus * 3 / 4 ? 2 : 1;
-  const int waves = rt == 2 ? 16 : !w && K <= 2048 ? 4 : 8;   // a span of 512 K for each
+  const int waves = w ? (rt == 2 || (N + 15) / 16 <= num_cus ? 16 : 8) : K <= 2048 ? 4 : 8;   // a span of 512 K for each
   // Tiles per workgroup: two workgroups fill a compute unit, and more of them than that only repeat the
   // start (the list, the first loads).  Gate-up of one token, 8 and 32 experts: 25.1 -> 24.0 and
   // 100 -> 86 us; 8 tokens 129 -> 102; with fewer workgroups the loop would cost 4 us a tile.
@@ -603,17 +604,22 @@ hipError_t launch_gemv_fp4(bool tiled, int32_t G, int64_t T, int32_t k, int64_t 
   trace_launch(info, grid, "G=%d T=%lld k=%d N=%lld K=%lld %s %s->%s", (int)G, (long long)T, (int)k, (long long)N,
                (long long)K, tiled ? "tiled" : "rows", x_bf16 ? "bf16" : "fp32", out_bf16 ? "bf16" : "fp32");
   auto go = [&](auto mode, auto til, auto tx, auto nc) {
-    constexpr int M = decltype(mode)::value;
+    constexpr int M = decltype(mode)::value, NC = decltype(nc)::value;
+    constexpr bool TILED = decltype(til)::value;
     using TX = decltype(tx);
-    if constexpr (M == kSum && decltype(til)::value && sizeof(TX) == 2 && decltype(nc)::value == 16) {
-      if (rt == 2) {
-        hipLaunchKernelGGL((gemv_fp4_kernel<M, decltype(til)::value, TX, decltype(nc)::value, 2>), grid,
-                           dim3(64 * waves), 0, st, a);
-        return;
-      }
+    auto launch = [&](auto row_tiles, auto nwaves) {
+      hipLaunchKernelGGL((gemv_fp4_kernel<M, TILED, TX, NC, decltype(row_tiles)::value, decltype(nwaves)::value>), grid,
+                         dim3(64 * waves), 0, st, a);
+    };
+    using One = std::integral_constant<int, 1>;
+    if constexpr (M == kSum) {
+      if constexpr (TILED && sizeof(TX) == 2 && NC == 16)
+        if (rt == 2) return launch(std::integral_constant<int, 2>(), std::integral_constant<int, 16>());
+      if (waves == 16) return launch(One(), std::integral_constant<int, 16>());
+    } else {
+      if (waves == 4) return launch(One(), std::integral_constant<int, 4>());
     }
-    hipLaunchKernelGGL((gemv_fp4_kernel<M, decltype(til)::value, TX, decltype(nc)::value, 1>), grid, dim3(64 * waves),
-                       0, st, a);
+    launch(One(), std::integral_constant<int, 8>());
   };
   using std::integral_constant;
   auto with_type = [&](auto mode, auto til) {
