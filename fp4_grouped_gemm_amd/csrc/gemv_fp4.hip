@@ -19,7 +19,7 @@
 // instructions in that order on both operands.  fp32 activations are split into three bf16 parts
 // (8 + 8 + 8 bits, exact) and take three instructions.
 //
-// A workgroup owns a tile of weight rows; its eight waves split the K blocks (of every expert,
+// A workgroup owns a tile of weight rows; its four, eight or sixteen waves split the K blocks (of every expert,
 // in the summed form) and their partial sums are joined through LDS in a fixed order, so no
 // result depends on the order of arrival.  Tokens are columns: the experts to visit are the
 // distinct ids among the tokens' slots, found per workgroup by an LDS table of first
@@ -39,7 +39,7 @@ typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kMaxWaves = 16;       // (of one workgroup; eight except in the summed form's two-tile variant)
+constexpr int kMaxWaves = 16;       // (of one workgroup)
 constexpr int kMaxPairs = 1024;    // 16 tokens x 64 slots
 constexpr int kMaxGroups = 1024;
 
@@ -592,12 +592,18 @@ hipError_t launch_gemv_fp4(bool tiled, int32_t G, int64_t T, int32_t k, int64_t 
   // 16 tokens over 32 experts (N 7168, K 2048), tiled, 57.6 -> 49.3 us, of 8 tokens 46.9 -> 45.3; of one
   // token 15.3 -> 15.5; untiled 16 tokens 64.1 -> 63.4 among other calls, 8 tokens 54.7 -> 59.0.
   const int rt = w && x_bf16 && tiled && T > 4 && (N + 31) / 32 >= num_cus * 3 / 4 ? 2 : 1;
-  const int waves = w ? (rt == 2 || (N + 15) / 16 <= num_cus ? 16 : 8) : K <= 2048 ? 4 : 8;   // a span of 512 K for each
-  // Tiles per workgroup: two workgroups fill a compute unit, and more of them than that only repeat the
-  // start (the list, the first loads).  Gate-up of one token, 8 and 32 experts: 25.1 -> 24.0 and
-  // 100 -> 86 us; 8 tokens 129 -> 102; with fewer workgroups the loop would cost 4 us a tile.
   const int64_t tiles = (N + 16 * rt - 1) / (16 * rt);
-  int64_t loop = w ? 1 : tiles * visits / (2 * num_cus);
+  // Waves: a span of 512 K for each, four to K 2048.  To K 4096 four with two spans each do better than eight where the
+  // tiles are many (two experts of eight, N 14336, K 4096, tiled: 1 token 18.5 -> 14.6 us, 8 tokens 55.9 -> 48.5)
+  // and worse where they are few (one matrix, 4096 rows: 5.1 -> 5.5).  The summed form takes sixteen where there are no
+  // more tiles than compute units (N 3328, K 1152, 3 experts, 16 tokens: 12.9 -> 7.6).
+  const bool few_spans = K <= 2048 || (K <= 4096 && tiles * visits > 4 * num_cus);
+  const int waves = w ? (rt == 2 || tiles <= num_cus ? 16 : 8) : few_spans ? 4 : 8;
+  // Tiles per workgroup: two workgroups of eight waves fill a compute unit, or four of four waves, and more of them
+  // only repeat the start (the list, the first loads).  Gate-up of one token, 8 and 32 experts: 25.1 -> 24.0 and
+  // 100 -> 86 us; 8 tokens 129 -> 102; with fewer workgroups the loop would cost 4 us a tile.  Of four waves
+  // against two workgroups' worth of tiles: one token's 8 experts, N 2048, K 2048, SiLU, untiled 12.3 -> 10.9.
+  int64_t loop = w ? 1 : tiles * visits / ((waves == 4 ? 4 : 2) * num_cus);
   loop = loop < 1 ? 1 : loop > 4 ? 4 : loop;
   const dim3 grid((unsigned)((tiles + loop - 1) / loop), visits, (unsigned)((T + 15) / 16));
   const KernelInfo& info = w && rt == 2 ? kInfoGemvFp4Sum2 : w ? kInfoGemvFp4Sum : silu ? kInfoGemvFp4Silu : kInfoGemvFp4;
