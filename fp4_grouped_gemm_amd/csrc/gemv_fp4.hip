@@ -60,6 +60,7 @@ struct GemvArgs {
   void* out;
   int out_bf16;
   int64_t ldo;
+  int group;             // tokens of a workgroup, at most 16
 };
 
 // The eight codes of one 32-bit word, times 2^(byte - 127), as bf16.
@@ -402,8 +403,8 @@ __global__ void __launch_bounds__(kWaves == 16 ? 1024 : 512, 4) gemv_fp4_kernel(
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, c = lane >> 4;
   int64_t n0 = (int64_t)blockIdx.x * (16 * RT);             // first output column of the tile at work
-  const int64_t t0 = (int64_t)blockIdx.z * 16;
-  const int Tn = a.T - t0 < 16 ? (int)(a.T - t0) : 16;
+  const int64_t t0 = (int64_t)blockIdx.z * a.group;
+  const int Tn = a.T - t0 < a.group ? (int)(a.T - t0) : a.group;
   const int64_t width = MODE == kSilu ? 2 * a.N : a.N;
   // the waves share the K blocks in spans of four
   const int nkb = (int)((a.K + 127) / 128), spans = (nkb + 3) / 4;
@@ -584,7 +585,7 @@ hipError_t launch_gemv_fp4(bool tiled, int32_t G, int64_t T, int32_t k, int64_t 
                            bool x_bf16, int64_t ldx, bool per_slot, const uint8_t* b, const uint8_t* s,
                            const int32_t* ids, const float* w, bool silu, void* out, bool out_bf16, int64_t ldo,
                            int num_cus, hipStream_t st) {
-  const GemvArgs a = {G, T, k, N, K, x, ldx, per_slot, b, s, ids, w, out, out_bf16, ldo};
+  GemvArgs a = {G, T, k, N, K, x, ldx, per_slot, b, s, ids, w, out, out_bf16, ldo, 16};
   const int64_t pairs = (T < 16 ? T : 16) * k;
   const unsigned visits = ids && !w ? (unsigned)(pairs < G ? pairs : G) : 1;
   // The summed form with many tokens: two row tiles a wave (twice the bytes in flight, half the
@@ -599,13 +600,22 @@ hipError_t launch_gemv_fp4(bool tiled, int32_t G, int64_t T, int32_t k, int64_t 
   // more tiles than compute units (N 3328, K 1152, 3 experts, 16 tokens: 12.9 -> 7.6).
   const bool few_spans = K <= 2048 || (K <= 4096 && tiles * visits > 4 * num_cus);
   const int waves = w ? (rt == 2 || tiles <= num_cus ? 16 : 8) : few_spans ? 4 : 8;
+  // Tokens per workgroup.  The summed form has one workgroup per row tile, which visits every expert of its tokens in
+  // turn; where the tiles are few, fewer tokens each leave it fewer activations (a K block of 16 tokens is 4 KB, of a
+  // tile 1 KB) and, below four, fewer experts if the tokens choose different ones: as long as every workgroup has a
+  // compute unit to itself (with two on each it loses: N 2048, 16 tokens, 26 -> 40 us).  32 experts, top-8, K 2048,
+  // tiled: N 512 of 16 tokens 26.1 -> 13.6 us, N 1024 of 4 tokens 16.8 -> 10.1, N 2048 of 8 tokens 24.3 -> 21.3;
+  // 10 experts, top-8, groups of two or one instead of four: 10.4 -> 11.1.
+  if (w && x_bf16)
+    for (const int few : {8, 4, 2, 1})
+      if (T > few && tiles * ((T + few - 1) / few) <= num_cus && (few >= 4 || G >= 2 * k)) a.group = few;
   // Tiles per workgroup: two workgroups of eight waves fill a compute unit, or four of four waves, and more of them
   // only repeat the start (the list, the first loads).  Gate-up of one token, 8 and 32 experts: 25.1 -> 24.0 and
   // 100 -> 86 us; 8 tokens 129 -> 102; with fewer workgroups the loop would cost 4 us a tile.  Of four waves
   // against two workgroups' worth of tiles: one token's 8 experts, N 2048, K 2048, SiLU, untiled 12.3 -> 10.9.
   int64_t loop = w ? 1 : tiles * visits / ((waves == 4 ? 4 : 2) * num_cus);
   loop = loop < 1 ? 1 : loop > 4 ? 4 : loop;
-  const dim3 grid((unsigned)((tiles + loop - 1) / loop), visits, (unsigned)((T + 15) / 16));
+  const dim3 grid((unsigned)((tiles + loop - 1) / loop), visits, (unsigned)((T + a.group - 1) / a.group));
   const KernelInfo& info = w && rt == 2 ? kInfoGemvFp4Sum2 : w ? kInfoGemvFp4Sum : silu ? kInfoGemvFp4Silu : kInfoGemvFp4;
   trace_launch(info, grid, "G=%d T=%lld k=%d N=%lld K=%lld %s %s->%s", (int)G, (long long)T, (int)k, (long long)N,
                (long long)K, tiled ? "tiled" : "rows", x_bf16 ? "bf16" : "fp32", out_bf16 ? "bf16" : "fp32");
@@ -630,7 +640,7 @@ hipError_t launch_gemv_fp4(bool tiled, int32_t G, int64_t T, int32_t k, int64_t 
   using std::integral_constant;
   auto with_type = [&](auto mode, auto til) {
     if (!x_bf16) return go(mode, til, float(), integral_constant<int, 16>());
-    if (T <= 4) return go(mode, til, uint16_t(), integral_constant<int, 4>());
+    if (T <= 4 || a.group <= 4) return go(mode, til, uint16_t(), integral_constant<int, 4>());
     go(mode, til, uint16_t(), integral_constant<int, 16>());
   };
   auto with_mode = [&](auto til) {

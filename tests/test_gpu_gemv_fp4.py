@@ -1,10 +1,13 @@
 """GPU parity of the few-token FP4 products against the float64 oracle.
 
-Tolerance: the products are exact; sums run in fp32 over at most K/256 + 1
-matrix instructions a wave, each counted as 5 levels of 32 products and one
-addition, joined over 8 waves and k experts: depth = K/256 + 1 + 5 + 8 + 2k
-roundings (2^-23 each, for sums that truncate) of the sum of the products'
-magnitudes; three instructions a step with fp32 activations.  SiLU is
+Tolerance: the products are exact; sums run in fp32, an instruction (32 of K)
+counted as 5 levels of 32 products and one addition to the chain before it.  Where
+K is split over 4 or 8 waves a chain has at most K/128 + 1 instructions and 8
+partial sums are joined: depth = K/128 + 1 + 5 + 8.  In the summed form one wave
+may take an expert's whole K, K/32 instructions, the experts are added with two
+roundings each and 16 waves joined: depth = K/32 + 5 + 16 + 2k.  Each is 2^-23 (for
+sums that truncate) of the sum of the products' magnitudes; fp32 activations take
+three instructions a step.  SiLU is
 |d silu| <= 1.1 |dg|, and 16 roundings of its own.  A bf16 result adds half a
 step, 2^-8."""
 
@@ -35,8 +38,9 @@ def _x(seed, shape, dtype):
     return synth.to_bf16_values(x) if dtype == torch.bfloat16 else x
 
 
-def _tol(mag, K, k, dtype):
-    return (K / 256 * (3 if dtype == torch.float32 else 1) + 1 + 5 + 8 + 2 * k) * 2.0 ** -23 * mag
+def _tol(mag, K, k, dtype, summed=False):
+    chain = (K / 32 if summed else K / 128 + 1) * (3 if dtype == torch.float32 else 1)
+    return (chain + 5 + (16 + 2 * k if summed else 8)) * 2.0 ** -23 * mag
 
 
 def _half(dtype, ref):
@@ -49,6 +53,7 @@ CASES = [  # T, G, k, N, K, tiled
     (1, 32, 8, 256, 512, True), (2, 4, 3, 33, 96, False), (16, 8, 2, 160, 640, True), (13, 32, 8, 77, 1312, False),
     (5, 1024, 4, 16, 128, True), (16, 70, 64, 18, 64, False), (33, 6, 2, 48, 384, True),
     (12, 3, 3, 97, 2656, False), (10, 40, 5, 1040, 1152, True), (16, 2, 1, 31, 4096, False),
+    (17, 32, 8, 2560, 256, True), (21, 20, 4, 1000, 288, False), (7, 24, 2, 500, 512, False), (6, 9, 4, 64, 1664, True),
 ]
 
 
@@ -119,7 +124,7 @@ def test_sum(T, G, k, N, K, tiled, dtype):
         for od in (torch.float32, torch.bfloat16):
             got = to_np(fgg.moe_gemv_fp4(cuda(x, dtype), b, s, cuda(ids), cuda(w), b_qdesc=q, n=N, out_dtype=od))
             err = np.abs(got - ref)
-            assert np.all(err <= _tol(mag, K, k, dtype) * (1 + 2.0 ** -8) + _half(od, ref)), err.max()
+            assert np.all(err <= _tol(mag, K, k, dtype, True) * (1 + 2.0 ** -8) + _half(od, ref)), err.max()
 
 
 @pytest.mark.parametrize("tiled", [True, False])
