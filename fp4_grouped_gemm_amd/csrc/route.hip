@@ -15,9 +15,9 @@
 //
 // Bound by instruction issue, not by memory: one token is one wave's few hundred vector
 // instructions.  8192 tokens x 256 experts, bf16, top-8 (4.7 MB, 1 us at a large copy's rate):
-// 7.1 us; with a search and two reductions a round 10.1 (a round is one reduction, the tie being the first lane of
+// 7.5 us; with a search and two reductions a round 10.1 (a round is one reduction, the tie being the first lane of
 // a ballot, and a queue step); 16384 x 384 fp32 16.0 us, 19.6 with a search over eight.  Gradient, 16384 x 160
-// fp32, top-6 (21.8 MB): 9 us (12.8 with gathered scores and element-wise loads).  One token: 3.9 us, a launch.
+// fp32, top-6 (21.8 MB): 10.5 us (12.8 with gathered scores and element-wise loads).  One token: 3.2 us, a launch.
 //
 // With a bias the keys are sums of rounded scores, and two experts whose keys differ by
 // less than the rounding of 32 bits would be ordered by it.  The experts are chosen in 32 bits, and a wave in
