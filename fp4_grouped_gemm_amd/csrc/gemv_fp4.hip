@@ -392,7 +392,8 @@ __device__ inline void gemv_run(const Tiles<NT>& w, const TX* const (&xrow)[Frag
 
 }  // namespace
 
-template <int MODE, bool TILED, class TX, int NCMAX, int RT, int kWaves>
+// kTileWaves of the kWaves waves share a row tile's K.
+template <int MODE, bool TILED, class TX, int NCMAX, int RT, int kWaves, int kTileWaves>
 __global__ void __launch_bounds__(kWaves == 16 ? 1024 : 512, 4) gemv_fp4_kernel(GemvArgs a) {
   constexpr int NT = MODE == kSilu ? 2 : RT;         // row tiles: gate and up, or RT one below the other
   __shared__ Items L;
@@ -408,7 +409,7 @@ __global__ void __launch_bounds__(kWaves == 16 ? 1024 : 512, 4) gemv_fp4_kernel(
   const int64_t width = MODE == kSilu ? 2 * a.N : a.N;
   // the waves share the K blocks in spans of four
   const int nkb = (int)((a.K + 127) / 128), spans = (nkb + 3) / 4;
-  constexpr int waves = kWaves;
+  constexpr int waves = kWaves, tw = kTileWaves, side = waves / tw;
   const TX* x = (const TX*)a.x;
   const bool obf = a.out_bf16;
 
@@ -491,10 +492,10 @@ __global__ void __launch_bounds__(kWaves == 16 ? 1024 : 512, 4) gemv_fp4_kernel(
     else if (nc <= 8) return go(integral_constant<int, 8>());
     else return go(integral_constant<int, 16>());
   };
-  // the sum over the waves of one value, in wave order
-  auto joined = [&](int i, int t, int r) {
-    float v = part[0][i][t][r];
-    for (int q = 1; q < waves; ++q) v += part[q][i][t][r];
+  // the sum over a tile's waves, from q0 on, of one value, in wave order
+  auto joined = [&](int q0, int i, int t, int r) {
+    float v = part[q0][i][t][r];
+    for (int q = 1; q < tw; ++q) v += part[q0 + q][i][t][r];
     return v;
   };
 
@@ -531,15 +532,18 @@ __global__ void __launch_bounds__(kWaves == 16 ? 1024 : 512, 4) gemv_fp4_kernel(
     for (int i = tid; i < RT * 256; i += blockDim.x) {
       const int t = (i >> 4) & 15, r = i & 15;
       const int64_t n = n0 + 16 * (i >> 8) + r;
-      if (t < Tn && n < a.N) put(a.out, obf, (t0 + t) * a.ldo + n, joined(i >> 8, t, r));
+      if (t < Tn && n < a.N) put(a.out, obf, (t0 + t) * a.ldo + n, joined(0, i >> 8, t, r));
     }
   } else {
-    const int kb0 = 4 * (int)((int64_t)spans * wave / waves), end = 4 * (int)((int64_t)spans * (wave + 1) / waves);
+    const int sub = wave / tw, at = wave % tw;         // of the tiles side by side, and of a tile's waves
+    const int kb0 = 4 * (int)((int64_t)spans * at / tw), end = 4 * (int)((int64_t)spans * (at + 1) / tw);
     const int kb1 = end < nkb ? end : nkb;
+    const int64_t first = (int64_t)blockIdx.x * (16 * side), step = (int64_t)gridDim.x * (16 * side);
     for (int it = blockIdx.y; it < items; it += gridDim.y) {
       const int p0 = a.ids ? __builtin_amdgcn_readfirstlane(L.item[it]) : 0, nc = columns(p0);
       const int e = a.ids ? __builtin_amdgcn_readfirstlane(L.ids[p0]) : 0;
-      for (n0 = (int64_t)blockIdx.x * (16 * RT); n0 < a.N; n0 += (int64_t)gridDim.x * 16) {
+      for (int64_t n = first; n < a.N; n += step) {
+        n0 = n + 16 * sub;
         v4f sum[NT];
         const int f = visit(e, nc, kb0, kb1, sum);
         if (col % f == 0) {
@@ -547,13 +551,14 @@ __global__ void __launch_bounds__(kWaves == 16 ? 1024 : 512, 4) gemv_fp4_kernel(
           for (int i = 0; i < NT; ++i) *reinterpret_cast<v4f*>(&part[wave][i][col / f][4 * c]) = sum[i];
         }
         __syncthreads();
-        for (int i = tid; i < 256; i += blockDim.x) {
-          const int t = i >> 4, r = i & 15;
-          if (t >= nc || n0 + r >= a.N) continue;
-          float v = joined(0, t, r);
-          if constexpr (MODE == kSilu) v = v / (1.0f + expf(-v)) * joined(1, t, r);
+        for (int i = tid; i < 256 * side; i += blockDim.x) {
+          const int q0 = (i >> 8) * tw, t = (i >> 4) & 15, r = i & 15;
+          const int64_t to = n + 16 * (i >> 8) + r;
+          if (t >= nc || to >= a.N) continue;
+          float v = joined(q0, 0, t, r);
+          if constexpr (MODE == kSilu) v = v / (1.0f + expf(-v)) * joined(q0, 1, t, r);
           const int tj = L.column[wave][t];
-          put(a.out, obf, ((t0 + (tj & 15)) * a.k + (tj >> 4)) * a.ldo + n0 + r, v);
+          put(a.out, obf, ((t0 + (tj & 15)) * a.k + (tj >> 4)) * a.ldo + to, v);
         }
         __syncthreads();
       }
@@ -561,9 +566,9 @@ __global__ void __launch_bounds__(kWaves == 16 ? 1024 : 512, 4) gemv_fp4_kernel(
     if (a.ids && blockIdx.y == 0) {                  // slots without an expert
       for (int p = tid >> 4; p < Tn * a.k; p += blockDim.x >> 4) {
         if (L.ids[p] >= 0) continue;
-        const int r = tid & 15;
-        for (n0 = (int64_t)blockIdx.x * (16 * RT); n0 < a.N; n0 += (int64_t)gridDim.x * 16)
-          if (n0 + r < a.N) put(a.out, obf, (t0 * a.k + p) * a.ldo + n0 + r, 0.0f);
+        for (int64_t n = first; n < a.N; n += step)
+          for (int64_t to = n + (tid & 15); to < n + 16 * side && to < a.N; to += 16)
+            put(a.out, obf, (t0 * a.k + p) * a.ldo + to, 0.0f);
       }
     }
   }
@@ -571,15 +576,15 @@ __global__ void __launch_bounds__(kWaves == 16 ? 1024 : 512, 4) gemv_fp4_kernel(
 
 static constexpr int gemv_lds(int nt, int waves = 8) { return (int)sizeof(Items) + waves * (nt * 1024 + kXsBytes); }
 const KernelInfo kInfoGemvFp4 = {"gemv_fp4_kernel", "fgg_moe_gemv_fp4", 16, 16, 128, 512, 0, 0, gemv_lds(1),
-                                 gemv_lds(1), (const void*)gemv_fp4_kernel<kPlain, true, uint16_t, 16, 1, 8>};
+                                 gemv_lds(1), (const void*)gemv_fp4_kernel<kPlain, true, uint16_t, 16, 1, 8, 8>};
 const KernelInfo kInfoGemvFp4Silu = {"gemv_fp4_kernel<silu>", "fgg_moe_gemv_fp4", 16, 16, 128, 512, 0, 0,
                                      gemv_lds(2), gemv_lds(2),
-                                     (const void*)gemv_fp4_kernel<kSilu, true, uint16_t, 16, 1, 8>};
+                                     (const void*)gemv_fp4_kernel<kSilu, true, uint16_t, 16, 1, 8, 8>};
 const KernelInfo kInfoGemvFp4Sum = {"gemv_fp4_kernel<sum>", "fgg_moe_gemv_fp4", 16, 16, 128, 512, 0, 0,
-                                    gemv_lds(1), gemv_lds(1), (const void*)gemv_fp4_kernel<kSum, true, uint16_t, 16, 1, 8>};
+                                    gemv_lds(1), gemv_lds(1), (const void*)gemv_fp4_kernel<kSum, true, uint16_t, 16, 1, 8, 8>};
 const KernelInfo kInfoGemvFp4Sum2 = {"gemv_fp4_kernel<sum, two tiles>", "fgg_moe_gemv_fp4", 32, 16, 128, 1024, 0, 0,
                                      gemv_lds(2, 16), gemv_lds(2, 16),
-                                     (const void*)gemv_fp4_kernel<kSum, true, uint16_t, 16, 2, 16>};
+                                     (const void*)gemv_fp4_kernel<kSum, true, uint16_t, 16, 2, 16, 16>};
 
 hipError_t launch_gemv_fp4(bool tiled, int32_t G, int64_t T, int32_t k, int64_t N, int64_t K, const void* x,
                            bool x_bf16, int64_t ldx, bool per_slot, const uint8_t* b, const uint8_t* s,
@@ -598,7 +603,11 @@ hipError_t launch_gemv_fp4(bool tiled, int32_t G, int64_t T, int32_t k, int64_t 
   // tiles are many (two experts of eight, N 14336, K 4096, tiled: 1 token 18.5 -> 14.6 us, 8 tokens 55.9 -> 48.5)
   // and worse where they are few (one matrix, 4096 rows: 5.1 -> 5.5).  The summed form takes sixteen where there are no
   // more tiles than compute units (N 3328, K 1152, 3 experts, 16 tokens: 12.9 -> 7.6).
-  const bool few_spans = K <= 2048 || (K <= 4096 && tiles * visits > 4 * num_cus);
+  // With a span or two for four waves, two or four tiles side by side, again where the tiles are many (16 tokens, tiled:
+  // 10 experts, N 7024, K 256, 16.6 -> 10.0 us, SiLU 20.6 -> 11.7; 25 experts, N 3264, K 640, 22.8 -> 17.3; where they are
+  // few, 4 experts, N 320, K 256, 4.8 -> 5.5, SiLU 5.6 -> 6.7).
+  const bool many = tiles * visits > 4 * num_cus;
+  const bool few_spans = K <= 2048 || (K <= 4096 && many);
   const int waves = w ? (rt == 2 || tiles <= num_cus ? 16 : 8) : few_spans ? 4 : 8;
   // Tokens per workgroup.  The summed form has one workgroup per row tile, which visits every expert of its tokens in
   // turn; where the tiles are few, fewer tokens each leave it fewer activations (a K block of 16 tokens is 4 KB, of a
@@ -613,9 +622,11 @@ hipError_t launch_gemv_fp4(bool tiled, int32_t G, int64_t T, int32_t k, int64_t 
   // only repeat the start (the list, the first loads).  Gate-up of one token, 8 and 32 experts: 25.1 -> 24.0 and
   // 100 -> 86 us; 8 tokens 129 -> 102; with fewer workgroups the loop would cost 4 us a tile.  Of four waves
   // against two workgroups' worth of tiles: one token's 8 experts, N 2048, K 2048, SiLU, untiled 12.3 -> 10.9.
-  int64_t loop = w ? 1 : tiles * visits / ((waves == 4 ? 4 : 2) * num_cus);
+  const int tile_waves = w || !many || K > 1024 ? waves : K <= 512 ? 1 : 2;
+  const int64_t wide = (tiles + waves / tile_waves - 1) / (waves / tile_waves);
+  int64_t loop = w ? 1 : wide * visits / ((waves == 4 ? 4 : 2) * num_cus);
   loop = loop < 1 ? 1 : loop > 4 ? 4 : loop;
-  const dim3 grid((unsigned)((tiles + loop - 1) / loop), visits, (unsigned)((T + a.group - 1) / a.group));
+  const dim3 grid((unsigned)((wide + loop - 1) / loop), visits, (unsigned)((T + a.group - 1) / a.group));
   const KernelInfo& info = w && rt == 2 ? kInfoGemvFp4Sum2 : w ? kInfoGemvFp4Sum : silu ? kInfoGemvFp4Silu : kInfoGemvFp4;
   trace_launch(info, grid, "G=%d T=%lld k=%d N=%lld K=%lld %s %s->%s", (int)G, (long long)T, (int)k, (long long)N,
                (long long)K, tiled ? "tiled" : "rows", x_bf16 ? "bf16" : "fp32", out_bf16 ? "bf16" : "fp32");
@@ -623,19 +634,26 @@ hipError_t launch_gemv_fp4(bool tiled, int32_t G, int64_t T, int32_t k, int64_t 
     constexpr int M = decltype(mode)::value, NC = decltype(nc)::value;
     constexpr bool TILED = decltype(til)::value;
     using TX = decltype(tx);
-    auto launch = [&](auto row_tiles, auto nwaves) {
-      hipLaunchKernelGGL((gemv_fp4_kernel<M, TILED, TX, NC, decltype(row_tiles)::value, decltype(nwaves)::value>), grid,
-                         dim3(64 * waves), 0, st, a);
+    auto launch = [&](auto row_tiles, auto nwaves, auto ntile) {
+      hipLaunchKernelGGL((gemv_fp4_kernel<M, TILED, TX, NC, decltype(row_tiles)::value, decltype(nwaves)::value,
+                                          decltype(ntile)::value>),
+                         grid, dim3(64 * waves), 0, st, a);
     };
-    using One = std::integral_constant<int, 1>;
+    constexpr std::integral_constant<int, 1> n1;
+    constexpr std::integral_constant<int, 2> n2;
+    constexpr std::integral_constant<int, 4> n4;
+    constexpr std::integral_constant<int, 8> n8;
+    constexpr std::integral_constant<int, 16> n16;
     if constexpr (M == kSum) {
       if constexpr (TILED && sizeof(TX) == 2 && NC == 16)
-        if (rt == 2) return launch(std::integral_constant<int, 2>(), std::integral_constant<int, 16>());
-      if (waves == 16) return launch(One(), std::integral_constant<int, 16>());
+        if (rt == 2) return launch(n2, n16, n16);
+      if (waves == 16) return launch(n1, n16, n16);
     } else {
-      if (waves == 4) return launch(One(), std::integral_constant<int, 4>());
+      if (tile_waves == 1) return launch(n1, n4, n1);
+      if (tile_waves == 2) return launch(n1, n4, n2);
+      if (waves == 4) return launch(n1, n4, n4);
     }
-    launch(One(), std::integral_constant<int, 8>());
+    launch(n1, n8, n8);
   };
   using std::integral_constant;
   auto with_type = [&](auto mode, auto til) {
