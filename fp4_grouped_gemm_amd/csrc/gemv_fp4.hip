@@ -7,23 +7,24 @@
 // plain (y per slot), with SiLU(gate)*up (B holds [gate | up] rows), or summed over the
 // token's slots with the gate weights.
 //
-// Bound by the weights' bytes: every distinct expert of up to 16 tokens is read once, whatever
-// number of them chose it.  Measured: gate-up of one token's 8 experts (N 2048, K 7168, tiled,
-// 125 MB) 22.8 us, 5.5 TB/s, of 32 experts 85.7 us, 5.8 TB/s; of 16 tokens 94.7 us, 5.2 TB/s; down of
-// 16 tokens (N 7168, K 2048, 248 MB) 49 us tiled, 62 us untiled (half lines); a 4096 x 7168 matrix and
-// one token 6.0 us, of which a launch and two memory latencies are most.  An E2M1 code times a power of two is a bf16 number, so the weights
-// go through v_cvt_scalef32_pk_bf16_fp4 (two codes and their scale per instruction) into the
-// bf16 matrix instruction 16x16x32 with 16 weight rows as its rows and the tokens as its
-// columns: products are exact, sums in fp32.  One 16-byte load per lane (row lane % 16, 32
-// consecutive K at 32 * (lane / 16): one scale) feeds four of them; K runs through the
-// instructions in that order on both operands.  fp32 activations are split into three bf16 parts
-// (8 + 8 + 8 bits, exact) and take three instructions.
+// Bound by the weights' bytes: every distinct expert of up to 16 tokens is read once, whatever number
+// of them chose it.  Measured: gate-up of one token's 8 experts (N 2048, K 7168, tiled, 125 MB) 22.8
+// us, 5.5 TB/s, of 32 experts 85.7 us, 5.8 TB/s; of 16 tokens 94.7 us, 5.2 TB/s; down of 16 tokens (N
+// 7168, K 2048, 248 MB) 49 us tiled, 62 us untiled (half lines); a 4096 x 7168 matrix and one token 6.0
+// us, of which a launch and two memory latencies are most.  An E2M1 code times a power of two is a bf16
+// number, so the weights go through v_cvt_scalef32_pk_bf16_fp4 (two codes and their scale per
+// instruction) into the bf16 matrix instruction 16x16x32 with 16 weight rows as its rows and the tokens
+// as its columns: products are exact, sums in fp32.  One 16-byte load per lane (row lane % 16, 32
+// consecutive K at 32 * (lane / 16): one scale) feeds four of them; K runs through the instructions in
+// that order on both operands.  fp32 activations are split into three bf16 parts (8 + 8 + 8 bits,
+// exact) and take three instructions.
 //
-// A workgroup owns a tile of weight rows; its four, eight or sixteen waves split the K blocks (of every expert,
-// in the summed form) and their partial sums are joined through LDS in a fixed order, so no
-// result depends on the order of arrival.  Tokens are columns: the experts to visit are the
-// distinct ids among the tokens' slots, found per workgroup by an LDS table of first
-// occurrences; a token that names one expert twice has its second slot visited on its own.
+// A workgroup owns a tile of weight rows; its four, eight or sixteen waves split the K blocks (of every
+// expert, in the summed form), or with little K own a tile for each one or two, and their partial sums
+// are joined through LDS in a fixed order, so no result depends on the order of arrival.  Tokens are
+// columns: the experts to visit are the distinct ids among the tokens' slots, found per workgroup by an
+// LDS table of first occurrences; a token that names one expert twice has its second slot visited on
+// its own.
 #include "fgg_device.hpp"
 #include "fgg_internal.hpp"
 #include "fgg_wave.hpp"

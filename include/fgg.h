@@ -435,7 +435,7 @@ fgg_status fgg_moe_down_combine(int32_t G, int64_t M, int64_t N, int64_t K, cons
  * gate weights that fgg_moe_permute, fgg_moe_combine and fgg_moe_gemv_fp4 take.
  *   s[t][e]     = softmax(logits[t])[e]  or  1 / (1 + e^-logits[t][e])
  *   key[t][e]   = logits[t][e] when bias is NULL (both gates grow with the logit),
- *                 s[t][e] + bias[e] otherwise (formed in 64 bits)
+ *                 s[t][e] + bias[e] otherwise (ordered as formed in 64 bits)
  *   topk_ids[t] = the experts of the k largest keys, in decreasing order, ties to the
  *                 lower expert
  *   topk_w[t][j] = scale * s[t][id_j], or with renormalize != 0
@@ -523,8 +523,9 @@ fgg_status fgg_moe_unpermute_rows_backward(const void* dout, fgg_dtype dtype, in
  * N % 16 == 0, K % 128 == 0), b 16-byte aligned.  Scale bytes 2 to 252 are exact (6 times a
  * larger power of two is beyond the bf16 and fp32 range, half of a smaller one subnormal, which
  * the matrix core may take as zero).
- * Each expert that tokens 16i .. 16i + 15 name is read once for the 16 of them, so the call
- * is meant for up to 16 tokens; more are taken 16 by 16.  No result depends on an order of
+ * Each expert that tokens 16i .. 16i + 15 name is read once for the 16 of them (for fewer of
+ * them in the summed form with few columns), so the call is meant for up to 16 tokens; more
+ * are taken 16 by 16.  No result depends on an order of
  * arrival: the same call gives the same bits.  1 <= G <= 1024, 1 <= k <= 64, K >= 32;
  * N, K <= 2^26, T <= 1048560.  T == 0 or N == 0 is a no-op.
  */
