@@ -615,8 +615,9 @@ hipError_t launch_gemv_fp4(bool tiled, int32_t G, int64_t T, int32_t k, int64_t 
   // tile 1 KB) and, below four, fewer experts if the tokens choose different ones: as long as every workgroup has a
   // compute unit to itself (with two on each it loses: N 2048, 16 tokens, 26 -> 40 us).  32 experts, top-8, K 2048,
   // tiled: N 512 of 16 tokens 26.1 -> 13.6 us, N 1024 of 4 tokens 16.8 -> 10.1, N 2048 of 8 tokens 24.3 -> 21.3;
-  // 10 experts, top-8, groups of two or one instead of four: 10.4 -> 11.1.
-  if (w && x_bf16)
+  // 10 experts, top-8, groups of two or one instead of four: 10.4 -> 11.1.  (Two row tiles a wave are for many tokens:
+  // their kernel has sixteen columns.)
+  if (w && x_bf16 && rt == 1)
     for (const int few : {8, 4, 2, 1})
       if (T > few && tiles * ((T + few - 1) / few) <= num_cus && (few >= 4 || G >= 2 * k)) a.group = few;
   // Tiles per workgroup: two workgroups of eight waves fill a compute unit, or four of four waves, and more of them
@@ -624,21 +625,22 @@ hipError_t launch_gemv_fp4(bool tiled, int32_t G, int64_t T, int32_t k, int64_t 
   // 100 -> 86 us; 8 tokens 129 -> 102; with fewer workgroups the loop would cost 4 us a tile.  Of four waves
   // against two workgroups' worth of tiles: one token's 8 experts, N 2048, K 2048, SiLU, untiled 12.3 -> 10.9.
   const int tile_waves = w || !many || K > 1024 ? waves : K <= 512 ? 1 : 2;
-  const int64_t wide = (tiles + waves / tile_waves - 1) / (waves / tile_waves);
-  int64_t loop = w ? 1 : wide * visits / ((waves == 4 ? 4 : 2) * num_cus);
-  loop = loop < 1 ? 1 : loop > 4 ? 4 : loop;
-  const dim3 grid((unsigned)((wide + loop - 1) / loop), visits, (unsigned)((T + a.group - 1) / a.group));
-  const KernelInfo& info = w && rt == 2 ? kInfoGemvFp4Sum2 : w ? kInfoGemvFp4Sum : silu ? kInfoGemvFp4Silu : kInfoGemvFp4;
-  trace_launch(info, grid, "G=%d T=%lld k=%d N=%lld K=%lld %s %s->%s", (int)G, (long long)T, (int)k, (long long)N,
-               (long long)K, tiled ? "tiled" : "rows", x_bf16 ? "bf16" : "fp32", out_bf16 ? "bf16" : "fp32");
   auto go = [&](auto mode, auto til, auto tx, auto nc) {
     constexpr int M = decltype(mode)::value, NC = decltype(nc)::value;
     constexpr bool TILED = decltype(til)::value;
     using TX = decltype(tx);
+    // The grid and the block are those of the kernel that is launched, whatever led to it.
     auto launch = [&](auto row_tiles, auto nwaves, auto ntile) {
-      hipLaunchKernelGGL((gemv_fp4_kernel<M, TILED, TX, NC, decltype(row_tiles)::value, decltype(nwaves)::value,
-                                          decltype(ntile)::value>),
-                         grid, dim3(64 * waves), 0, st, a);
+      constexpr int RT = decltype(row_tiles)::value, W = decltype(nwaves)::value, TW = decltype(ntile)::value;
+      constexpr int kRows = 16 * RT * (W / TW);        // of a workgroup at a time
+      const int64_t wide = (N + kRows - 1) / kRows;
+      int64_t loop = w ? 1 : wide * visits / ((W == 4 ? 4 : 2) * num_cus);
+      loop = loop < 1 ? 1 : loop > 4 ? 4 : loop;
+      const dim3 grid((unsigned)((wide + loop - 1) / loop), visits, (unsigned)((T + a.group - 1) / a.group));
+      const KernelInfo& info = w && RT == 2 ? kInfoGemvFp4Sum2 : w ? kInfoGemvFp4Sum : silu ? kInfoGemvFp4Silu : kInfoGemvFp4;
+      trace_launch(info, grid, "G=%d T=%lld k=%d N=%lld K=%lld %s %s->%s", (int)G, (long long)T, (int)k, (long long)N,
+                   (long long)K, tiled ? "tiled" : "rows", x_bf16 ? "bf16" : "fp32", out_bf16 ? "bf16" : "fp32");
+      hipLaunchKernelGGL((gemv_fp4_kernel<M, TILED, TX, NC, RT, W, TW>), grid, dim3(64 * W), 0, st, a);
     };
     constexpr std::integral_constant<int, 1> n1;
     constexpr std::integral_constant<int, 2> n2;
