@@ -345,13 +345,15 @@ __global__ void __launch_bounds__(256) route_kernel(const TI* __restrict__ logit
           d[i] = x[i] > -kInf ? exp64_nonpos((double)x[i] - (double)m_all) : 0.0;
           sum += d[i];
         }
-        const double inv = 1.0 / group_reduce<GW>(sum, OpAdd());
+        // a row with NaN or +inf has no scores: by the bias alone
+        sum = group_reduce<GW>(sum, OpAdd());
+        const double inv = bad ? 0.0 : 1.0 / sum;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) d[i] *= inv;
       }
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
-        const double c = (d[i] == d[i] ? d[i] : 0.0) + (double)add[i];   // a row with NaN or +inf: by the bias alone
+        const double c = (d[i] == d[i] ? d[i] : 0.0) + (double)add[i];   // (d of a +inf is a NaN)
         key64[i] = (x[i] > -kInf && c > -(double)kInf) ? order_key(c) : 0;
       }
       select_largest<GW, EPL>(key64, k, gl, my_id, my_key);

@@ -215,3 +215,44 @@ def test_route_in_a_graph_and_on_another_stream():
         assert torch.equal(d, fgg.moe_route_backward(held, a, b, "sigmoid", True))
         if seed == 0:
             assert torch.equal(d, grad)
+
+
+def _by_key(key, k):
+    """The k largest keys that are numbers above -inf, ties to the lower expert."""
+    key = np.where(np.isnan(key), -np.inf, key)
+    ids = np.argsort(-key, kind="stable")[:k]
+    return np.where(np.isneginf(key[ids]), -1, ids)
+
+
+@pytest.mark.parametrize("E", [6, 29, 60, 100, 200, 400, 1000])
+@pytest.mark.parametrize("gate", ["softmax", "sigmoid"])
+def test_order_of_rows_with_nan_and_inf_and_a_bias(E, gate):
+    """Under a softmax a NaN or +inf leaves no score: the other experts are ranked by the bias alone, here
+    against the logits' order.  A sigmoid's scores do not depend on one another: the NaN is left out, the
+    rest are ranked by score + bias."""
+    g = synth.rng(E)
+    rise = np.sort(g.standard_normal(E)).astype(np.float32)
+    x = np.tile(rise, (6, 1))
+    x[0, E // 2] = np.nan
+    x[1, E // 3] = np.inf
+    x[2, 1], x[2, E - 1] = np.nan, np.inf
+    x[3, 0], x[3, 2], x[3, 4] = np.nan, -np.inf, np.nan
+    x[4, :E - 2] = np.nan
+    bias = np.linspace(0.02, -0.02, E).astype(np.float32)    # (less than the spread of the scores)
+    bias[3] = -np.inf
+    k = min(E, 12)
+    ids, w = fgg.moe_route(cuda(x), k, gate, bias=cuda(bias), renormalize=True)
+    ids, w = to_np(ids), to_np(w)
+    for t in range(6):
+        row = x[t].astype(np.float64)
+        if gate == "sigmoid":
+            score = oracle.routing.scores(row[None], gate)[0]
+        elif np.isnan(row).any() or np.isposinf(row).any():
+            score = np.zeros(E)
+        else:
+            score = oracle.routing.scores(row[None], gate)[0]
+        key = np.where(np.isnan(row) | np.isneginf(row), -np.inf, score + bias.astype(np.float64))
+        want = _by_key(key, k)
+        assert ids[t].tolist() == want.tolist(), t
+        nan = np.isnan(row).any() or (gate == "softmax" and np.isposinf(row).any())
+        assert (np.isnan(w[t]) if nan else np.isfinite(w[t]))[want >= 0].all() and (w[t][want < 0] == 0).all(), t
