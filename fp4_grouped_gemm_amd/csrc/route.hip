@@ -399,6 +399,7 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const TI* __restric
   const bool on = id >= 0 && id < E;
   if (!on) id = -1, u = 0.0f;
   if (!whole && on) v = load_one(row + id);
+  if (v != v) u = v;                                  // (a maximum and a clamped difference drop a NaN)
   float d = u;
   if (!whole) {
     const float p = gate_weight<GW>(v, on && v != -kInf, sigmoid, renorm, 0.0f, 1.0f);

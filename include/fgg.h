@@ -457,7 +457,8 @@ fgg_status fgg_moe_down_combine(int32_t G, int64_t M, int64_t N, int64_t K, cons
  * Every element of the [T][E] gradient is written (in the logits' type, row stride
  * ldd >= E; it must not overlap the inputs).  Ids outside [0, E) contribute nothing; an
  * id that stands twice in a row contributes twice.  Closed experts (-inf) get 0.  Rounded
- * once from fp32.
+ * once from fp32.  NaN and +inf logits act where the formula reads them: the whole row for the
+ * softmax, the chosen experts' own logits otherwise (together when renormalized).
  */
 fgg_status fgg_moe_route(const void* logits, fgg_dtype dtype, int64_t T, int32_t E, int64_t ld, int32_t k,
                          fgg_gate gate, const float* bias, int32_t renormalize, float scale, int32_t* topk_ids,

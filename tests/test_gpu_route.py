@@ -256,3 +256,29 @@ def test_order_of_rows_with_nan_and_inf_and_a_bias(E, gate):
         assert ids[t].tolist() == want.tolist(), t
         nan = np.isnan(row).any() or (gate == "softmax" and np.isposinf(row).any())
         assert (np.isnan(w[t]) if nan else np.isfinite(w[t]))[want >= 0].all() and (w[t][want < 0] == 0).all(), t
+
+
+@pytest.mark.parametrize("E,k", [(6, 3), (29, 4), (60, 5), (100, 8), (400, 8)])
+@pytest.mark.parametrize("gate", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_gradient_of_a_nan_that_was_chosen(E, k, gate, renorm):
+    """Ids that name a NaN logit (the router gives none, a caller may): its weight is a NaN, and so is
+    every gradient that the weight enters, all of the token's chosen experts where their weights share a sum."""
+    g = synth.rng(E + k)
+    x = g.standard_normal((3, E)).astype(np.float32)
+    ids = np.stack([g.permutation(E)[:k] for _ in range(3)]).astype(np.int32)
+    x[1, ids[1, 1]] = np.nan
+    dw = g.standard_normal((3, k)).astype(np.float32)
+    got = to_np(fgg.moe_route_backward(cuda(x), cuda(ids), cuda(dw), gate, renorm))
+    nan = np.zeros(x.shape, bool)
+    if renorm:
+        nan[1, ids[1]] = True
+    elif gate == "softmax":
+        nan[1] = True
+    else:
+        nan[1, ids[1, 1]] = True
+    assert np.array_equal(np.isnan(got), nan)
+    clean = x.copy()
+    clean[1] = 0
+    rest = to_np(fgg.moe_route_backward(cuda(clean), cuda(ids), cuda(dw), gate, renorm))
+    assert np.array_equal(got[[0, 2]], rest[[0, 2]])
