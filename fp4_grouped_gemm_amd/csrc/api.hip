@@ -3,6 +3,7 @@
 // anything or enqueues its kernels on the caller's stream and returns.
 #include <hip/hip_runtime.h>
 
+#include <array>
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
@@ -87,7 +88,7 @@ void trace_launch(const KernelInfo& k, dim3 grid, const char* fmt, ...) {
 }
 
 int kernel_table(const KernelInfo* const** out) {
-  static const KernelInfo* const table[] = {
+  static const KernelInfo* const single[] = {
       &kInfoQuantE4m3_1x128, &kInfoQuantE4m3_128x128, &kInfoQuantE2m1_1x16, &kInfoQuantE2m1E8m0_1x32,
       &kInfoPermuteHist,     &kInfoPermuteScan,       &kInfoPermuteScatter, &kInfoPermuteGather,
       &kInfoPermuteQuantize, &kInfoFill,              &kInfoCombine,        &kInfoCombineRows,
@@ -95,12 +96,20 @@ int kernel_table(const KernelInfo* const** out) {
       &kInfoFp8Dense,        &kInfoMaskedFp4Tiled,    &kInfoMaskedFp4,
       &kInfoMaskedFp8,       &kInfoPackFp4,           &kInfoPackFp4Scales,  &kInfoW4a4Prep,
       &kInfoW4a4LowRank,     &kInfoW4a4Gemm,         &kInfoMxfp4Gemm,
-      &kInfoRoute,           &kInfoRouteBackward,     &kInfoRowsScatter,    &kInfoRowsCollect,
-      &kInfoRowsScatterDot,  &kInfoRowsCollectDot,    &kInfoGemvFp4,        &kInfoGemvFp4Silu,
-      &kInfoGemvFp4Sum,      &kInfoGemvFp4Sum2,
+      &kInfoRoute,           &kInfoRowsScatter,       &kInfoRowsCollect,    &kInfoRowsScatterDot,
+      &kInfoRowsCollectDot,
   };
-  *out = table;
-  return (int)(sizeof table / sizeof table[0]);
+  constexpr int kSingle = (int)(sizeof single / sizeof single[0]);
+  static const auto table = [] {
+    std::array<const KernelInfo*, kSingle + kRouteBackwardForms + kGemvForms> t{};
+    int n = 0;
+    for (const KernelInfo* k : single) t[n++] = k;
+    for (const KernelInfo& k : kInfoRouteBackward) t[n++] = &k;
+    for (const KernelInfo& k : kInfoGemvFp4) t[n++] = &k;
+    return t;
+  }();
+  *out = table.data();
+  return (int)table.size();
 }
 
 }  // namespace fgg

@@ -38,8 +38,11 @@ extern const KernelInfo kInfoQuantE4m3_1x128, kInfoQuantE4m3_128x128, kInfoQuant
     kInfoPermuteQuantize, kInfoFill, kInfoCombine, kInfoCombineRows, kInfoCombineRest, kInfoFp8Contig,
     kInfoFp8ContigSilu, kInfoFp8ContigCombine, kInfoFp8Dense,
     kInfoMaskedFp4Tiled, kInfoMaskedFp4, kInfoMaskedFp8, kInfoPackFp4, kInfoPackFp4Scales, kInfoW4a4Prep, kInfoW4a4LowRank,
-    kInfoW4a4Gemm, kInfoMxfp4Gemm, kInfoRoute, kInfoRouteBackward, kInfoRowsScatter, kInfoRowsCollect,
-    kInfoRowsScatterDot, kInfoRowsCollectDot, kInfoGemvFp4, kInfoGemvFp4Silu, kInfoGemvFp4Sum, kInfoGemvFp4Sum2;
+    kInfoW4a4Gemm, kInfoMxfp4Gemm, kInfoRoute, kInfoRowsScatter, kInfoRowsCollect, kInfoRowsScatterDot,
+    kInfoRowsCollectDot;
+// (kernels with several forms: one entry for each that differs in its workgroup)
+constexpr int kRouteBackwardForms = 7, kGemvForms = 21;
+extern const KernelInfo kInfoRouteBackward[kRouteBackwardForms], kInfoGemvFp4[kGemvForms];
 
 enum class QuantKind { E4M3_1x128, E4M3_128x128, E2M1_1x16, E2M1_E8M0_1x32 };
 

@@ -168,6 +168,10 @@ struct Frag<float, 16> {
   }
 };
 
+// Whether more than four tokens' bf16 activations are turned into operands through LDS.
+template <class TX, int NC>
+constexpr bool stages_activations() { return NC > 4 && sizeof(TX) == 2; }
+
 __device__ inline void put(void* out, bool bf16, int64_t i, float v) {
   if (bf16) ((uint16_t*)out)[i] = bf16_bits_rne(v);
   else ((float*)out)[i] = v;
@@ -399,7 +403,7 @@ __global__ void __launch_bounds__(kWaves == 16 ? 1024 : 512, 4) gemv_fp4_kernel(
   constexpr int NT = MODE == kSilu ? 2 : RT;         // row tiles: gate and up, or RT one below the other
   __shared__ Items L;
   __shared__ float part[kWaves][NT][16][16];         // [wave][tile][token][row]
-  constexpr bool kXs = NCMAX > 4 && sizeof(TX) == 2;
+  constexpr bool kXs = stages_activations<TX, NCMAX>();
   constexpr int kScratch = kXs ? kXsBytes : 0;       // a wave's own
   __shared__ __attribute__((aligned(16))) uint8_t scratch[kScratch ? kWaves * kScratch : 16];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -575,17 +579,43 @@ __global__ void __launch_bounds__(kWaves == 16 ? 1024 : 512, 4) gemv_fp4_kernel(
   }
 }
 
-static constexpr int gemv_lds(int nt, int waves = 8) { return (int)sizeof(Items) + waves * (nt * 1024 + kXsBytes); }
-const KernelInfo kInfoGemvFp4 = {"gemv_fp4_kernel", "fgg_moe_gemv_fp4", 16, 16, 128, 512, 0, 0, gemv_lds(1),
-                                 gemv_lds(1), (const void*)gemv_fp4_kernel<kPlain, true, uint16_t, 16, 1, 8, 8>};
-const KernelInfo kInfoGemvFp4Silu = {"gemv_fp4_kernel<silu>", "fgg_moe_gemv_fp4", 16, 16, 128, 512, 0, 0,
-                                     gemv_lds(2), gemv_lds(2),
-                                     (const void*)gemv_fp4_kernel<kSilu, true, uint16_t, 16, 1, 8, 8>};
-const KernelInfo kInfoGemvFp4Sum = {"gemv_fp4_kernel<sum>", "fgg_moe_gemv_fp4", 16, 16, 128, 512, 0, 0,
-                                    gemv_lds(1), gemv_lds(1), (const void*)gemv_fp4_kernel<kSum, true, uint16_t, 16, 1, 8, 8>};
-const KernelInfo kInfoGemvFp4Sum2 = {"gemv_fp4_kernel<sum, two tiles>", "fgg_moe_gemv_fp4", 32, 16, 128, 1024, 0, 0,
-                                     gemv_lds(2, 16), gemv_lds(2, 16),
-                                     (const void*)gemv_fp4_kernel<kSum, true, uint16_t, 16, 2, 16, 16>};
+// The forms by what differs in their workgroups: output, row tiles of a wave, waves, waves of a tile (the others
+// take tiles beside it), and whether activations are staged (the weights' layout changes neither threads nor LDS).
+template <int MODE, int RT, int W, int TW, bool STAGED>
+static KernelInfo gemv_form(const char* name) {
+  constexpr int kLds = (int)sizeof(Items) + W * 1024 * (MODE == kSilu ? 2 : RT) + (STAGED ? W * kXsBytes : 0);
+  return {name, "fgg_moe_gemv_fp4", 16 * RT * (W / TW), 16, 128, 64 * W, 0, 0, kLds, kLds,
+          (const void*)gemv_fp4_kernel<MODE, true, uint16_t, STAGED ? 16 : 4, RT, W, TW>};
+}
+const KernelInfo kInfoGemvFp4[kGemvForms] = {
+    gemv_form<kPlain, 1, 8, 8, false>("gemv_fp4_kernel<plain, 8 waves>"),
+    gemv_form<kPlain, 1, 8, 8, true>("gemv_fp4_kernel<plain, 8 waves, staged>"),
+    gemv_form<kPlain, 1, 4, 4, false>("gemv_fp4_kernel<plain, 4 waves>"),
+    gemv_form<kPlain, 1, 4, 4, true>("gemv_fp4_kernel<plain, 4 waves, staged>"),
+    gemv_form<kPlain, 1, 4, 2, false>("gemv_fp4_kernel<plain, 4 waves, 2 tiles>"),
+    gemv_form<kPlain, 1, 4, 2, true>("gemv_fp4_kernel<plain, 4 waves, 2 tiles, staged>"),
+    gemv_form<kPlain, 1, 4, 1, false>("gemv_fp4_kernel<plain, 4 waves, 4 tiles>"),
+    gemv_form<kPlain, 1, 4, 1, true>("gemv_fp4_kernel<plain, 4 waves, 4 tiles, staged>"),
+    gemv_form<kSilu, 1, 8, 8, false>("gemv_fp4_kernel<silu, 8 waves>"),
+    gemv_form<kSilu, 1, 8, 8, true>("gemv_fp4_kernel<silu, 8 waves, staged>"),
+    gemv_form<kSilu, 1, 4, 4, false>("gemv_fp4_kernel<silu, 4 waves>"),
+    gemv_form<kSilu, 1, 4, 4, true>("gemv_fp4_kernel<silu, 4 waves, staged>"),
+    gemv_form<kSilu, 1, 4, 2, false>("gemv_fp4_kernel<silu, 4 waves, 2 tiles>"),
+    gemv_form<kSilu, 1, 4, 2, true>("gemv_fp4_kernel<silu, 4 waves, 2 tiles, staged>"),
+    gemv_form<kSilu, 1, 4, 1, false>("gemv_fp4_kernel<silu, 4 waves, 4 tiles>"),
+    gemv_form<kSilu, 1, 4, 1, true>("gemv_fp4_kernel<silu, 4 waves, 4 tiles, staged>"),
+    gemv_form<kSum, 1, 8, 8, false>("gemv_fp4_kernel<sum, 8 waves>"),
+    gemv_form<kSum, 1, 8, 8, true>("gemv_fp4_kernel<sum, 8 waves, staged>"),
+    gemv_form<kSum, 1, 16, 16, false>("gemv_fp4_kernel<sum, 16 waves>"),
+    gemv_form<kSum, 1, 16, 16, true>("gemv_fp4_kernel<sum, 16 waves, staged>"),
+    gemv_form<kSum, 2, 16, 16, true>("gemv_fp4_kernel<sum, 16 waves, 2 tiles a wave, staged>"),
+};
+// The entry of a form above.
+static constexpr int gemv_index(int mode, int rt, int waves, int tile_waves, bool staged) {
+  if (rt == 2) return kGemvForms - 1;
+  const int shape = mode == kSum ? waves == 16 : waves == 8 ? 0 : tile_waves == 4 ? 1 : tile_waves == 2 ? 2 : 3;
+  return mode * 8 + shape * 2 + staged;
+}
 
 hipError_t launch_gemv_fp4(bool tiled, int32_t G, int64_t T, int32_t k, int64_t N, int64_t K, const void* x,
                            bool x_bf16, int64_t ldx, bool per_slot, const uint8_t* b, const uint8_t* s,
@@ -637,7 +667,7 @@ hipError_t launch_gemv_fp4(bool tiled, int32_t G, int64_t T, int32_t k, int64_t 
       int64_t loop = w ? 1 : wide * visits / ((W == 4 ? 4 : 2) * num_cus);
       loop = loop < 1 ? 1 : loop > 4 ? 4 : loop;
       const dim3 grid((unsigned)((wide + loop - 1) / loop), visits, (unsigned)((T + a.group - 1) / a.group));
-      const KernelInfo& info = w && RT == 2 ? kInfoGemvFp4Sum2 : w ? kInfoGemvFp4Sum : silu ? kInfoGemvFp4Silu : kInfoGemvFp4;
+      const KernelInfo& info = kInfoGemvFp4[gemv_index(M, RT, W, TW, stages_activations<TX, NC>())];
       trace_launch(info, grid, "G=%d T=%lld k=%d N=%lld K=%lld %s %s->%s", (int)G, (long long)T, (int)k, (long long)N,
                    (long long)K, tiled ? "tiled" : "rows", x_bf16 ? "bf16" : "fp32", out_bf16 ? "bf16" : "fp32");
       hipLaunchKernelGGL((gemv_fp4_kernel<M, TILED, TX, NC, RT, W, TW>), grid, dim3(64 * W), 0, st, a);

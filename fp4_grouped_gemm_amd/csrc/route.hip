@@ -479,8 +479,22 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const TI* __restric
 
 const KernelInfo kInfoRoute = {"route_kernel", "fgg_moe_route", 0, 0, 0, 256, 0, 0, 0, 0,
                                (const void*)route_kernel<float, 64, 4, false>};
-const KernelInfo kInfoRouteBackward = {"route_backward_kernel", "fgg_moe_route_backward", 0, 0, 0, 256, 0, 0, 4096, 4096,
-                                       (const void*)route_backward_kernel<float, 64, 4>};
+// The gradient's forms, by lanes of a token and experts of a lane: four waves' rows of LDS over 32 experts.
+template <int GW, int EPL>
+static KernelInfo backward_form(const char* name) {
+  constexpr int kLds = GW == 64 ? 4 * 64 * EPL * 4 : 0;
+  return {name, "fgg_moe_route_backward", 0, 0, 0, 256, 0, 0, kLds, kLds,
+          (const void*)route_backward_kernel<float, GW, EPL>};
+}
+const KernelInfo kInfoRouteBackward[kRouteBackwardForms] = {
+    backward_form<16, 1>("route_backward_kernel<16 lanes>"),
+    backward_form<32, 1>("route_backward_kernel<32 lanes>"),
+    backward_form<64, 1>("route_backward_kernel<64 lanes>"),
+    backward_form<64, 2>("route_backward_kernel<64 lanes x 2>"),
+    backward_form<64, 4>("route_backward_kernel<64 lanes x 4>"),
+    backward_form<64, 8>("route_backward_kernel<64 lanes x 8>"),
+    backward_form<64, 16>("route_backward_kernel<64 lanes x 16>"),
+};
 
 // Calls f(group width, experts per lane) as compile-time constants: the smallest that hold E.
 template <class F>
@@ -526,10 +540,11 @@ hipError_t launch_route_backward(const void* logits, bool bf16, int64_t T, int32
                                  bool sigmoid, bool renorm, float scale, const int32_t* ids, const float* dw,
                                  void* dlogits, int64_t ldd, hipStream_t st) {
   const dim3 grid((unsigned)route_blocks(T, E));
-  trace_launch(kInfoRouteBackward, grid, "T=%lld E=%d k=%d %s %s%s", (long long)T, (int)E, (int)k,
-               bf16 ? "bf16" : "fp32", sigmoid ? "sigmoid" : "softmax", renorm ? " renorm" : "");
   with_shape(E, [&](auto gw, auto epl) {
     constexpr int GW = decltype(gw)::value, EPL = decltype(epl)::value;
+    constexpr int kForm = GW == 16 ? 0 : GW == 32 ? 1 : EPL == 1 ? 2 : EPL == 2 ? 3 : EPL == 4 ? 4 : EPL == 8 ? 5 : 6;
+    trace_launch(kInfoRouteBackward[kForm], grid, "T=%lld E=%d k=%d %s %s%s", (long long)T, (int)E, (int)k,
+                 bf16 ? "bf16" : "fp32", sigmoid ? "sigmoid" : "softmax", renorm ? " renorm" : "");
     if (bf16)
       hipLaunchKernelGGL((route_backward_kernel<uint16_t, GW, EPL>), grid, dim3(256), 0, st, (const uint16_t*)logits,
                          T, (int)E, ld, (int)k, sigmoid, renorm, scale, ids, dw, (uint16_t*)dlogits, ldd);
