@@ -402,7 +402,7 @@ template <int MODE, bool TILED, class TX, int NCMAX, int RT, int kWaves, int kTi
 __global__ void __launch_bounds__(kWaves == 16 ? 1024 : 512, 4) gemv_fp4_kernel(GemvArgs a) {
   constexpr int NT = MODE == kSilu ? 2 : RT;         // row tiles: gate and up, or RT one below the other
   __shared__ Items L;
-  __shared__ float part[kWaves][NT][16][16];         // [wave][tile][token][row]
+  __shared__ __attribute__((aligned(16))) float part[kWaves][NT][16][16];   // [wave][tile][token][row]
   constexpr bool kXs = stages_activations<TX, NCMAX>();
   constexpr int kScratch = kXs ? kXsBytes : 0;       // a wave's own
   __shared__ __attribute__((aligned(16))) uint8_t scratch[kScratch ? kWaves * kScratch : 16];
