@@ -1,4 +1,4 @@
-// Cross-lane helpers shared by the router and the row kernels (gfx950 only).
+// Cross-lane helpers shared by the router, the row kernels and the few-token products (gfx950 only).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -9,10 +9,6 @@ namespace fgg {
 struct OpMax {
   template <class T>
   __device__ T operator()(T a, T b) const { return a > b ? a : b; }
-};
-struct OpMin {
-  template <class T>
-  __device__ T operator()(T a, T b) const { return a < b ? a : b; }
 };
 struct OpFMax {   // fmaxf: a NaN operand is ignored
   __device__ float operator()(float a, float b) const { return fmaxf(a, b); }
