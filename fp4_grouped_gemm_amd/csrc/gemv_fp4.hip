@@ -17,7 +17,7 @@
 // as its columns: products are exact, sums in fp32.  One 16-byte load per lane (row lane % 16, 32
 // consecutive K at 32 * (lane / 16): one scale) feeds four of them; K runs through the instructions in
 // that order on both operands.  fp32 activations are split into three bf16 parts (8 + 8 + 8 bits,
-// exact) and take three instructions.
+// exact down to bf16's smallest step, 2^-133) and take three instructions.
 //
 // A workgroup owns a tile of weight rows; its four, eight or sixteen waves split the K blocks (of every
 // expert, in the summed form), or with little K own a tile for each one or two, and their partial sums
@@ -64,7 +64,9 @@ struct GemvArgs {
   int group;             // tokens of a workgroup, at most 16
 };
 
-// The eight codes of one 32-bit word, times 2^(byte - 127), as bf16.
+// The eight codes of one 32-bit word, times 2^(byte - 127), as bf16.  scale holds the byte as its exponent, which is
+// all that the instruction reads: byte 0 is 2^-127 and 255 a NaN, and results below 2^-126 keep their bits (bf16 has
+// them to 2^-133, and the matrix core takes them).
 __device__ inline bf16x8 dequant8(uint32_t codes, float scale) {
   const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0);
   const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1);

@@ -509,7 +509,7 @@ fgg_status fgg_moe_unpermute_rows_backward(const void* dout, fgg_dtype dtype, in
  * unquantized: the form of the experts' products for single tokens (no permute, no
  * workspace, one launch).
  *   y[t][j][n] = sum_K x[t(, j)][K] * code(b[e][n][K]) * 2^(b_scales[e][n][K/32] - 127),  e = topk_ids[t][j]
- * accumulated in fp32 (the products are exact), then, per output form:
+ * accumulated in fp32 (the products are exact, see the ends of the ranges below), then, per output form:
  *   topk_w NULL, FGG_ACT_NONE:     out[t·k + j][n] = y[t][j][n]
  *   topk_w NULL, FGG_ACT_SILU_MUL: b holds [gate | up] rows (2N of them):
  *                                  out[t·k + j][n] = g / (1 + e^-g) * u,  g = y[t][j][n], u = y[t][j][N + n]
@@ -521,9 +521,12 @@ fgg_status fgg_moe_unpermute_rows_backward(const void* dout, fgg_dtype dtype, in
  * x: fp32 or bf16, [T][ldx], or with x_per_slot != 0 [T·k][ldx] (row t·k + j for slot j);
  * ldx >= K, any alignment of the element.  bq: {E2M1X2,E8M0,1,32} (b [G][N][K/2], b_scales
  * [G][N][K/32], any N, K % 32 == 0) or {E2M1X2_TILED,E8M0,1,32} (from fgg_pack_fp4_weights:
- * N % 16 == 0, K % 128 == 0), b 16-byte aligned.  Scale bytes 2 to 252 are exact (6 times a
- * larger power of two is beyond the bf16 and fp32 range, half of a smaller one subnormal, which
- * the matrix core may take as zero).
+ * N % 16 == 0, K % 128 == 0), b 16-byte aligned.
+ * Scale bytes 0 to 252 are exact with every code, 253 and 254 with the codes whose value stays
+ * below 2^128; a weight of 2^128 and more, which fp32 does not have either, makes its outputs
+ * infinite or NaN, and byte 255 (E8M0's NaN) makes them NaN.  bf16 activations are exact
+ * whatever their size; of fp32 activations what lies below 2^-133 is dropped, the smallest step of
+ * the bf16 parts that they are split into (nothing of a number of 2^-110 and more).
  * Each expert that tokens 16i .. 16i + 15 name is read once for the 16 of them (for fewer of
  * them in the summed form with few columns), so the call is meant for up to 16 tokens; more
  * are taken 16 by 16.  No result depends on an order of

@@ -1,6 +1,6 @@
-"""The few-token FP4 products in the forms that their launch rules choose between:
-whatever the number of compute units they are told of, every output is written once
-and right.
+"""The few-token FP4 products in the forms that their launch rules choose between
+(whatever the number of compute units they are told of, every output is written once
+and right), and at the ends of the ranges of scales and activations.
 
 Tolerance: as in test_gpu_gemv_fp4.py's summed form, the chain of one wave counted
 as the whole of K (K/32 instructions), 5 levels inside an instruction, 16 waves
@@ -57,3 +57,56 @@ def test_sum_writes_every_column(cus, tiled):
             fgg.moe_gemv_fp4(cuda(x, torch.bfloat16), b, s, cuda(ids), cuda(w), b_qdesc=q, n=N, out=out)
             ref, mag = oracle.moe_gemv_fp4(x, W, ids, w=w)
             assert np.all(np.abs(to_np(out) - ref) <= _bound(mag, K, k) + 2.0 ** -24 * np.abs(ref)), (N, T)
+
+
+@pytest.mark.parametrize("tiled", [True, False])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_scale_bytes_at_the_ends(tiled, dtype):
+    """One-hot activations and a row per code and scale byte: exact for every weight below 2^128 (0 to
+    252 are all of the codes'), infinite or NaN from there on, NaN for byte 255, and each row by itself."""
+    K, ends = 256, [0, 1, 2, 3, 126, 127, 252, 253, 254, 255]
+    codes = np.repeat(np.tile(np.arange(16, dtype=np.uint8) * 17, len(ends))[:, None], K // 2, 1)[None]
+    sc = np.repeat(np.repeat(np.array(ends, np.uint8), 16)[:, None], K // 32, 1)[None]
+    N = codes.shape[1]
+    W = oracle.fp4_weights(codes, sc)[0]
+    b, s, q = cuda(codes), cuda(sc), fgg.Q_E2M1_E8M0_1x32
+    if tiled:
+        (b, s), q = fgg.pack_fp4_weights(b, s), fgg.Q_E2M1_E8M0_1x32_TILED
+    for T in (1, 7, 16):
+        for value in (1.0, -2.0 ** -20):
+            x = np.zeros((T, K), np.float32)
+            at = (np.arange(T) * 37 + 5) % K
+            x[np.arange(T), at] = value
+            got = to_np(fgg.moe_gemv_fp4(cuda(x, dtype), b, s, b_qdesc=q, n=N, out_dtype=torch.float32))
+            want = W[:, at].T * value
+            inside = np.abs(W[:, at].T) < 2.0 ** 128
+            assert inside[:, :16 * 7].all() and not inside[:, 16 * 9:].any()
+            np.testing.assert_array_equal(got[inside], want[inside].astype(np.float32))
+            assert not np.isfinite(got[~inside]).any() and np.isnan(got[:, 16 * 9:]).all()
+
+
+@pytest.mark.parametrize("byte", [127, 150, 220])
+def test_the_smallest_activations(byte):
+    """bf16 down to its smallest step is exact; of fp32 what lies below 2^-133 is dropped, nothing of a
+    number of 2^-110 and more."""
+    K, N = 96, 16
+    codes = np.full((1, N, K // 2), 0x22, np.uint8)          # code 2: the value 1
+    sc = np.full((1, N, K // 32), byte, np.uint8)
+    b, s = cuda(codes), cuda(sc)
+    scale = 2.0 ** (byte - 127)
+    g = synth.rng(byte)
+
+    def one_hot(v):
+        x = np.zeros((len(v), K), np.float32)
+        x[np.arange(len(v)), g.integers(0, K, len(v))] = v
+        return x
+
+    v = (np.arange(1, 128) * 2.0 ** -133).astype(np.float32) * np.where(np.arange(127) % 2, 1, -1).astype(np.float32)
+    x = torch.from_numpy(one_hot(v)).to(torch.bfloat16).cuda()
+    got = to_np(fgg.moe_gemv_fp4(x, b, s, out_dtype=torch.float32)).astype(np.float64)
+    np.testing.assert_array_equal(got, np.repeat(v.astype(np.float64)[:, None] * scale, N, 1))
+    e = np.arange(-149, -95)
+    v = np.ldexp(1 + g.integers(0, 1 << 23, e.size) / 2.0 ** 23, e).astype(np.float32)
+    got = to_np(fgg.moe_gemv_fp4(cuda(one_hot(v)), b, s, out_dtype=torch.float32)).astype(np.float64)
+    err = np.abs(got - v.astype(np.float64)[:, None] * scale)
+    assert np.all(err < 2.0 ** -133 * scale) and np.all(err[e >= -110] == 0)
