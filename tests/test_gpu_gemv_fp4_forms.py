@@ -110,3 +110,36 @@ def test_the_smallest_activations(byte):
     got = to_np(fgg.moe_gemv_fp4(cuda(one_hot(v)), b, s, out_dtype=torch.float32)).astype(np.float64)
     err = np.abs(got - v.astype(np.float64)[:, None] * scale)
     assert np.all(err < 2.0 ** -133 * scale) and np.all(err[e >= -110] == 0)
+
+
+@pytest.mark.parametrize("T,G,k,N,K", [(1, 1, 1, 64, 512), (16, 1, 1, 48, 512), (5, 1, 1, 32, 1024), (3, 2, 1, 9600, 256),
+                                       (16, 2, 1, 9600, 512), (8, 2, 1, 9600, 1024), (2, 1, 1, 16, 4096)])
+@pytest.mark.parametrize("tiled", [True, False])
+@pytest.mark.parametrize("silu", [True, False])
+def test_chain_of_a_waves_share(T, G, k, N, K, tiled, silu):
+    """Nonnegative weights and activations, so that every sum only grows and no rounding is hidden by
+    cancellation.  A wave takes spans of 512 of K, 16 instructions each, as many as its share of the
+    tile's waves: from one wave a tile (K to 512 with many tiles) to eight, a chain of at most K/32
+    instructions whatever the share, 5 levels inside one, 8 waves joined.  SiLU of g >= 0 has a slope of
+    at most 1.1 and 16 roundings of its own."""
+    g = synth.rng(N + K)
+    rows = 2 * N if silu else N
+    codes = (g.integers(0, 8, size=(G, rows, K // 2)) + 16 * g.integers(0, 8, size=(G, rows, K // 2))).astype(np.uint8)
+    sc = g.integers(116, 120, size=(G, rows, K // 32), dtype=np.uint8)
+    W = oracle.fp4_weights(codes, sc)
+    b, s, q = cuda(codes), cuda(sc), fgg.Q_E2M1_E8M0_1x32
+    if tiled:
+        (b, s), q = fgg.pack_fp4_weights(b, s), fgg.Q_E2M1_E8M0_1x32_TILED
+    ids = None if G == 1 else g.integers(0, G, size=(T, k)).astype(np.int32)
+    x = synth.to_bf16_values(g.random((T, K), dtype=np.float32))
+    got = to_np(fgg.moe_gemv_fp4(cuda(x, torch.bfloat16), b, s, None if ids is None else cuda(ids), b_qdesc=q, n=N,
+                                 silu_mul=silu, out_dtype=torch.float32))
+    levels = (K / 32 + 5 + 8) * 2.0 ** -23
+    if silu:
+        ref, mag, gate, up = oracle.moe_gemv_fp4(x, W, ids, silu_mul=True)
+        eg, eu = levels * mag[..., 0, :], levels * mag[..., 1, :]
+        tol = (up + eu) * 1.1 * eg + np.abs(gate) * eu + 17 * 2.0 ** -24 * np.abs(ref)
+    else:
+        ref, mag = oracle.moe_gemv_fp4(x, W, ids)
+        tol = levels * mag + 2.0 ** -24 * np.abs(ref)
+    assert np.all(np.abs(got.reshape(ref.shape) - ref) <= tol)

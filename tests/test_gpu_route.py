@@ -282,3 +282,43 @@ def test_gradient_of_a_nan_that_was_chosen(E, k, gate, renorm):
     clean[1] = 0
     rest = to_np(fgg.moe_route_backward(cuda(clean), cuda(ids), cuda(dw), gate, renorm))
     assert np.array_equal(got[[0, 2]], rest[[0, 2]])
+
+
+def _open_case(seed, T, E, k, dtype):
+    """Random logits, no row and few experts closed: nearly every slot holds an expert."""
+    g = synth.rng(seed)
+    x = (g.standard_normal((T, E)) * 2.0).astype(np.float32)
+    if dtype == torch.bfloat16:
+        x = synth.to_bf16_values(x).astype(np.float32)
+    if E > 2 * k:
+        x[g.random((T, E)) < 0.05] = -np.inf
+    return x
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 2), (1, 40, 4), (1, 64, 6), (1, 100, 8), (1, 256, 8), (1, 384, 8),
+                                   (1, 1024, 16),
+                                   (7, 65, 4), (33, 100, 6), (130, 128, 8), (5, 127, 60),
+                                   (9, 257, 8), (70, 300, 6), (65, 384, 8), (31, 500, 10), (6, 512, 64)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("gate", ["softmax", "sigmoid"])
+def test_expert_counts(T, E, k, dtype, gate):
+    """One token with real logits, and two and eight experts a lane (E 65 to 128, 257 to 512), forward with and
+    without a bias and backward, against the oracle."""
+    x = _open_case(7 * T + E, T, E, k, dtype)
+    bias = (synth.rng(E + 1).standard_normal(E) * 0.1).astype(np.float32)
+    d = cuda(x, dtype)
+    dw = synth.rng(T + 3).standard_normal((T, k)).astype(np.float32)
+    for renorm in (False, True):
+        for b in (None, bias):
+            ids, w = fgg.moe_route(d, k, gate, bias=None if b is None else cuda(b), renormalize=renorm, scale=1.5)
+            ref_ids, ref_w = oracle.moe_route(x, k, gate, b, renorm, 1.5)
+            assert (ref_ids >= 0).all()
+            assert np.array_equal(to_np(ids), ref_ids)
+            _check_weights(to_np(w), ref_w, x, (b is not None, renorm))
+        got = to_np(fgg.moe_route_backward(d, cuda(ref_ids), cuda(dw), gate, renorm, 1.5))
+        ref = oracle.moe_route_backward(x, ref_ids, dw, gate, renorm, 1.5)
+        tol = 2 * (64 + _spread(x)) * U * _gradient_scale(x, ref_ids, dw, gate, renorm, 1.5) + TINY
+        if dtype == torch.bfloat16:
+            tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref)
+        assert np.all(np.abs(got - ref) <= tol), (np.abs(got - ref) / tol).max()
+        assert E == 1 or k == E or renorm and k == 1 or np.count_nonzero(ref) >= k
