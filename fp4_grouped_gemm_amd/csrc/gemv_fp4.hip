@@ -622,7 +622,9 @@ static constexpr int gemv_index(int mode, int rt, int waves, int tile_waves, boo
 hipError_t launch_gemv_fp4(bool tiled, int32_t G, int64_t T, int32_t k, int64_t N, int64_t K, const void* x,
                            bool x_bf16, int64_t ldx, bool per_slot, const uint8_t* b, const uint8_t* s,
                            const int32_t* ids, const float* w, bool silu, void* out, bool out_bf16, int64_t ldo,
-                           int num_cus, hipStream_t st) {
+                           int cus, hipStream_t st) {
+  // (any count may be set: at most 65535 workgroups where a rule below fills the compute units, the grid's depth)
+  const int64_t num_cus = cus < 65535 ? cus : 65535;
   GemvArgs a = {G, T, k, N, K, x, ldx, per_slot, b, s, ids, w, out, out_bf16, ldo, 16};
   const int64_t pairs = (T < 16 ? T : 16) * k;
   const unsigned visits = ids && !w ? (unsigned)(pairs < G ? pairs : G) : 1;

@@ -59,6 +59,26 @@ def test_sum_writes_every_column(cus, tiled):
             assert np.all(np.abs(to_np(out) - ref) <= _bound(mag, K, k) + 2.0 ** -24 * np.abs(ref)), (N, T)
 
 
+@pytest.mark.parametrize("cus", [65535, 65536, 200000, 1 << 22, 1 << 29, 1 << 30, (1 << 31) - 1])
+@pytest.mark.parametrize("T", [3, 70001])
+def test_any_number_of_compute_units(cus, T):
+    """The launch rules hold for every count that fgg_set_num_cus takes: no overflow, no grid past the limits."""
+    G, N, K, k = 3, 16, 64, 1
+    W, b, s, q = _weights(T, G, N, K, False)
+    g = synth.rng(T)
+    ids = g.integers(0, G, size=(T, k)).astype(np.int32)
+    x = synth.to_bf16_values(g.standard_normal((T, K)).astype(np.float32))
+    w = g.random((T, k), dtype=np.float32)
+    fgg.set_num_cus(cus)
+    args = (cuda(x, torch.bfloat16), b, s, cuda(ids))
+    y = np.stack([x.astype(np.float64) @ W[e].T for e in range(G)])[ids[:, 0], np.arange(T)]
+    mag = np.stack([np.abs(x.astype(np.float64)) @ np.abs(W[e].T) for e in range(G)])[ids[:, 0], np.arange(T)]
+    got = to_np(fgg.moe_gemv_fp4(*args, out_dtype=torch.float32))[:, 0]
+    assert np.all(np.abs(got - y) <= _bound(mag, K, k) + 2.0 ** -24 * np.abs(y))
+    got = to_np(fgg.moe_gemv_fp4(*args, cuda(w), out_dtype=torch.float32))
+    assert np.all(np.abs(got - y * w) <= _bound(mag * w, K, k) + 2.0 ** -24 * np.abs(y * w))
+
+
 @pytest.mark.parametrize("tiled", [True, False])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_scale_bytes_at_the_ends(tiled, dtype):
