@@ -4,7 +4,8 @@ Argument marshalling only: torch supplies device memory and the current HIP
 stream; every step of the computation runs in the library's HIP kernels.  The
 names follow the C ABI in ``include/fgg.h``, which documents layouts, formats
 and error behaviour.  There is no fallback path: if the library is missing or
-the device is not gfx950, calls raise.
+the device is not gfx950, calls raise.  No call records an autograd node: results are
+detached whatever their inputs require, and the gradients are the ``_backward`` calls.
 """
 
 import ctypes

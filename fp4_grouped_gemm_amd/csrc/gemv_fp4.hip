@@ -11,7 +11,8 @@
 // of them chose it.  Measured: gate-up of one token's 8 experts (N 2048, K 7168, tiled, 125 MB) 22.8
 // us, 5.5 TB/s, of 32 experts 85.7 us, 5.8 TB/s; of 16 tokens 94.7 us, 5.2 TB/s; down of 16 tokens (N
 // 7168, K 2048, 248 MB) 49 us tiled, 62 us untiled (half lines); a 4096 x 7168 matrix and one token 6.0
-// us, of which a launch and two memory latencies are most.  An E2M1 code times a power of two is a bf16
+// us, of which a launch and two memory latencies are most.  fp32 activations cost two to four times that
+// (gate-up of one token 60 us, of 16 tokens 225; down of 16 tokens, tiled, 189): instruction issue.  An E2M1 code times a power of two is a bf16
 // number, so the weights go through v_cvt_scalef32_pk_bf16_fp4 (two codes and their scale per
 // instruction) into the bf16 matrix instruction 16x16x32 with 16 weight rows as its rows and the tokens
 // as its columns: products are exact, sums in fp32.  One 16-byte load per lane (row lane % 16, 32

@@ -13,8 +13,8 @@
 // All of it is bound by memory: a token row is read (or written) once however many slots
 // it has, a permuted row once.  Measured (a 4 GiB copy on the same card: 4.5 TB/s): permute of
 // 8192 x 7168 bf16 onto 32 of 256 experts, 224 MB in 49 us (4.6 TB/s); gradient of a permute,
-// 4096 x 2 x 4096 fp32, 201 MB in 34 us (5.9); gradients of an unpermute with its weights',
-// 8192 x 4 x 4096 bf16, 621 MB in 121 us (5.1).  The permuted rows are stored through the caches:
+// 4096 x 2 x 4096 fp32, 201 MB in 34 us (5.9; 40 where every call has an output of its own);
+// gradients of an unpermute with its weights', 8192 x 4 x 4096 bf16, 621 MB in 121 us (5.1).  The permuted rows are stored through the caches:
 // past them the first took 38 us, but with the reader that follows (a copy of the rows) 36 us instead
 // of 31 for 68 MB, 128 instead of 129 for 206 MB and 657 instead of 625 for 1 GB.  Rows are moved 16
 // bytes per lane; the loads and stores are declared with the element's alignment (this part's vector

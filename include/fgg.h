@@ -481,8 +481,9 @@ fgg_status fgg_moe_route_backward(const void* logits, fgg_dtype dtype, int64_t T
  * topk_w [T][k] fp32 may be NULL: every weight is 1 (a row is then the token's bits).  dtopk_w
  * may be NULL; when given, the forward's input (x, or rows) is read and dtopk_w [T][k] fp32 is
  * written whole, 0 for a pair without a row.  A pair whose r is outside [0, M) has no row.
- * Sums over slots run in increasing j in fp32 (with bf16 rows, the result of
- * fgg_moe_combine bit for bit) and are rounded once; dot products are fp32 sums in a fixed
+ * Sums over slots run in increasing j in fp32 (with bf16 rows and weights the result of
+ * fgg_moe_combine bit for bit, whose call takes N and strides in multiples of 8 only: 2 %
+ * faster for thousands of wide rows, slower for few tokens and for N to 1024) and are rounded once; dot products are fp32 sums in a fixed
  * order.  All results are the same from run to run.
  * Any N >= 1, row strides >= N and element-aligned pointers; each output must not overlap
  * an input.  row_to_src [M], offsets [E + 1], 1 <= k <= 64, 1 <= E <= 1024.  T == 0 is a
