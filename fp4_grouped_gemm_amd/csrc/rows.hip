@@ -14,15 +14,16 @@
 // it has, a permuted row once.  Measured (a 4 GiB copy on the same card: 4.5 TB/s): permute of
 // 8192 x 7168 bf16 onto 32 of 256 experts, 224 MB in 49 us (4.6 TB/s); gradient of a permute,
 // 4096 x 2 x 4096 fp32, 201 MB in 34 us (5.9; 40 where every call has an output of its own);
-// gradients of an unpermute with its weights', 8192 x 4 x 4096 bf16, 621 MB in 121 us (5.1).  The permuted rows are stored through the caches:
-// past them the first took 38 us, but with the reader that follows (a copy of the rows) 36 us instead
-// of 31 for 68 MB, 128 instead of 129 for 206 MB and 657 instead of 625 for 1 GB.  Rows are moved 16
-// bytes per lane; the loads and stores are declared with the element's alignment (this part's vector
-// memory takes any), so odd widths and strides run the same path; the last vector of a row ends with
-// it, overlapping the one before (its elements are written twice alike, and counted once in a dot
-// product).  A token has a wave to itself up to 128 vectors, four waves beyond.  (With element-wise
-// tails and four waves for every token, 8192 x 4 x 500 bf16: permute 16.4 us, its gradient 70.6,
-// unpermute 22.8, its gradient 64.4; now 10.7, 14.5, 9.3 and 18.9.)
+// gradients of an unpermute with its weights', 8192 x 4 x 4096 bf16, 621 MB in 121 us (5.1).  The
+// permuted rows are stored through the caches: past them the first took 38 us, but with the reader
+// that follows (a copy of the rows) 36 us instead of 31 for 68 MB, 128 instead of 129 for 206 MB and
+// 657 instead of 625 for 1 GB.  Rows are moved 16 bytes per lane; the loads and stores are declared
+// with the element's alignment (this part's vector memory takes any), so odd widths and strides run
+// the same path; the last vector of a row ends with it, overlapping the one before (its elements are
+// written twice alike, and counted once in a dot product).  A token has a wave to itself up to 128
+// vectors, four waves beyond.  (With element-wise tails and four waves for every token, 8192 x 4 x
+// 500 bf16: permute 16.4 us, its gradient 70.6, unpermute 22.8, its gradient 64.4; now 10.7, 14.5,
+// 9.3 and 18.9.)
 #include "fgg_device.hpp"
 #include "fgg_internal.hpp"
 #include "fgg_wave.hpp"
