@@ -20,7 +20,9 @@ __all__ = [
     "moe_permute_quantize_noalloc", "grouped_gemm_scaled", "grouped_gemm_silu_quantize", "pack_fp4_weights",
     "scaled_gemm", "moe_combine", "set_num_cus", "kernel_table", "kernel_compiled_lds",
     "moe_route", "moe_route_backward", "moe_permute_rows", "moe_permute_rows_backward", "moe_unpermute_rows",
-    "moe_unpermute_rows_backward", "moe_gemv_fp4",
+    "moe_unpermute_rows_backward", "moe_gemv_fp4", "grouped_linear", "grouped_linear_backward_input",
+    "grouped_linear_backward_weight", "grouped_linear_backward_weight_workspace_bytes", "grouped_gated",
+    "grouped_gated_backward",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -110,6 +112,12 @@ def load_library():
         "fgg_moe_unpermute_rows_backward": ([P, I32, I64, I32, I64, I64, P, I64, P, P, P, P, I32, I64, P, I64, P, P],
                                             I32),
         "fgg_moe_gemv_fp4": ([I32, I64, I32, I64, I64, P, I32, I64, I32, P, P, QDesc, P, P, I32, P, I32, I64, P], I32),
+        "fgg_grouped_linear": ([I32, I64, I64, I64, P, I64, P, P, P, P, I32, I64, P], I32),
+        "fgg_grouped_linear_backward_input": ([I32, I64, I64, I64, P, I64, P, P, P, P, I32, I64, P], I32),
+        "fgg_grouped_linear_backward_weight_workspace": ([I32, I64, I64, I64, ctypes.POINTER(SZ)], I32),
+        "fgg_grouped_linear_backward_weight": ([I32, I64, I64, I64, P, I64, P, I64, P, P, P, I32, I32, P, SZ, P], I32),
+        "fgg_grouped_gated": ([I32, I64, I64, I64, P, I64, P, P, P, P, I64, P, I64, P], I32),
+        "fgg_grouped_gated_backward": ([I32, I64, I64, I64, P, I64, P, P, I64, P, P, P, I64, P, I64, P], I32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -692,3 +700,121 @@ def moe_gemv_fp4(x, b, b_scales, topk_ids=None, topk_w=None, b_qdesc=Q_E2M1_E8M0
           b.data_ptr(), b_scales.data_ptr(), desc, _addr(topk_ids), _addr(topk_w),
           FGG_ACT_SILU_MUL if silu_mul else FGG_ACT_NONE, out.data_ptr(), _FLOAT[out.dtype], ldo)
     return out
+
+
+# ------------------------------------------ bf16 rows times their segment's weights
+
+def _segments(offsets, counts, G, dev):
+    _dense(offsets, "offsets", dev, torch.int32, (G + 1,))
+    _dense(counts, "counts", dev, torch.int32, (G,))
+    assert offsets is not None or G == 1, "offsets"
+
+
+def _bf16_out(out, shape, dtype, dev, name):
+    """The given output (checked) or a new one, and its row stride."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=dev), shape[1]
+    ld = _float_rows(out, name)
+    assert out.shape == shape and out.device == dev, name
+    return out, ld
+
+
+def grouped_linear(x, w, offsets=None, counts=None, out=None, out_dtype=torch.bfloat16):
+    """Rows times their segment's weights (fgg_grouped_linear): x bf16 [M, K] (rows may be strided), w bf16
+    [G, N, K], segment g the rows [offsets[g], offsets[g + 1]) (of which the first counts[g]); without
+    offsets one segment (G = 1).  Returns [M, N], bf16 or fp32; rows of no segment are left as ``out`` had them."""
+    ldx = _float_rows(x, "x", torch.bfloat16)
+    (M, K), dev = x.shape, x.device
+    G, N = w.shape[0], w.shape[1]
+    _dense(w, "w", dev, torch.bfloat16, (G, N, K))
+    _segments(offsets, counts, G, dev)
+    out, ldo = _bf16_out(out, (M, N), out_dtype, dev, "out")
+    _call("fgg_grouped_linear", dev, G, M, N, K, x.data_ptr(), ldx, w.data_ptr(), _addr(offsets), _addr(counts),
+          out.data_ptr(), _FLOAT[out.dtype], ldo)
+    return out
+
+
+def grouped_linear_backward_input(dy, w, offsets=None, counts=None, out=None, out_dtype=torch.bfloat16):
+    """Gradient of grouped_linear's rows (fgg_grouped_linear_backward_input): dy bf16 [M, N], w bf16 [G, N, K];
+    returns [M, K], bf16 or fp32, rows of no segment left as ``out`` had them."""
+    lddy = _float_rows(dy, "dy", torch.bfloat16)
+    (M, N), dev = dy.shape, dy.device
+    G, K = w.shape[0], w.shape[2]
+    _dense(w, "w", dev, torch.bfloat16, (G, N, K))
+    _segments(offsets, counts, G, dev)
+    out, ldo = _bf16_out(out, (M, K), out_dtype, dev, "out")
+    _call("fgg_grouped_linear_backward_input", dev, G, M, N, K, dy.data_ptr(), lddy, w.data_ptr(), _addr(offsets),
+          _addr(counts), out.data_ptr(), _FLOAT[out.dtype], ldo)
+    return out
+
+
+def grouped_linear_backward_weight_workspace_bytes(G: int, M: int, N: int, K: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("fgg_grouped_linear_backward_weight_workspace",
+           load_library().fgg_grouped_linear_backward_weight_workspace(G, M, N, K, ctypes.byref(n)))
+    return n.value
+
+
+def grouped_linear_backward_weight(dy, x, num_groups, offsets=None, counts=None, out=None, out_dtype=torch.float32,
+                                   accumulate=False, workspace=None):
+    """Gradient of grouped_linear's weights (fgg_grouped_linear_backward_weight): dy bf16 [M, N], x bf16 [M, K];
+    returns [G, N, K], fp32 or bf16 (0 for an empty segment); accumulate adds to ``out``."""
+    lddy, ldx = _float_rows(dy, "dy", torch.bfloat16), _float_rows(x, "x", torch.bfloat16)
+    (M, N), K, dev, G = dy.shape, x.shape[1], dy.device, int(num_groups)
+    assert x.shape[0] == M and x.device == dev, "x"
+    _segments(offsets, counts, G, dev)
+    if out is None:
+        assert not accumulate, "accumulate adds to out"
+        out = torch.empty((G, N, K), dtype=out_dtype, device=dev)
+    else:
+        assert out.dtype in _FLOAT, "out"
+        _dense(out, "out", dev, out.dtype, (G, N, K))
+    nbytes = grouped_linear_backward_weight_workspace_bytes(G, M, N, K)
+    if workspace is None and nbytes > 0:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _dense(workspace, "workspace", dev, torch.uint8)
+    _call("fgg_grouped_linear_backward_weight", dev, G, M, N, K, dy.data_ptr(), lddy, x.data_ptr(), ldx,
+          _addr(offsets), _addr(counts), out.data_ptr(), _FLOAT[out.dtype], 1 if accumulate else 0, _addr(workspace),
+          0 if workspace is None else workspace.numel())
+    return out
+
+
+def grouped_gated(x, w, offsets=None, counts=None, out=None, h=None):
+    """The gated block's first half (fgg_grouped_gated): x bf16 [M, K], w bf16 [G, 2I, K] ([gate | up] rows);
+    a = silu(gate) * up, bf16 [M, I].  h (bf16 [M, 2I], optional) receives the pre-activations that
+    the backward pass needs.  Returns (a, h); rows of no segment are left as they were."""
+    ldx = _float_rows(x, "x", torch.bfloat16)
+    (M, K), dev = x.shape, x.device
+    G, I = w.shape[0], w.shape[1] // 2
+    _dense(w, "w", dev, torch.bfloat16, (G, 2 * I, K))
+    _segments(offsets, counts, G, dev)
+    out, lda = _bf16_out(out, (M, I), torch.bfloat16, dev, "out")
+    assert out.dtype == torch.bfloat16, "out"
+    ldh = 0
+    if h is not None:
+        ldh = _float_rows(h, "h", torch.bfloat16)
+        assert h.shape == (M, 2 * I) and h.device == dev, "h"
+    _call("fgg_grouped_gated", dev, G, M, I, K, x.data_ptr(), ldx, w.data_ptr(), _addr(offsets), _addr(counts),
+          out.data_ptr(), lda, _addr(h), ldh)
+    return out, h
+
+
+def grouped_gated_backward(dy, w_down, h, offsets=None, counts=None, out=None, a=None):
+    """From the gradient of the block's output to that of its pre-activations (fgg_grouped_gated_backward):
+    dy bf16 [M, N], w_down bf16 [G, N, I], h bf16 [M, 2I] from grouped_gated; returns (dh bf16 [M, 2I], a).
+    a (bf16 [M, I], optional) receives the activation again, which w_down's gradient needs."""
+    lddy, ldh = _float_rows(dy, "dy", torch.bfloat16), _float_rows(h, "h", torch.bfloat16)
+    (M, N), dev = dy.shape, dy.device
+    G, I = w_down.shape[0], w_down.shape[2]
+    _dense(w_down, "w_down", dev, torch.bfloat16, (G, N, I))
+    assert h.shape == (M, 2 * I) and h.device == dev, "h"
+    _segments(offsets, counts, G, dev)
+    out, ldo = _bf16_out(out, (M, 2 * I), torch.bfloat16, dev, "out")
+    assert out.dtype == torch.bfloat16, "out"
+    lda = 0
+    if a is not None:
+        lda = _float_rows(a, "a", torch.bfloat16)
+        assert a.shape == (M, I) and a.device == dev, "a"
+    _call("fgg_grouped_gated_backward", dev, G, M, I, N, dy.data_ptr(), lddy, w_down.data_ptr(), h.data_ptr(), ldh,
+          _addr(offsets), _addr(counts), out.data_ptr(), ldo, _addr(a), lda)
+    return out, a

@@ -101,11 +101,12 @@ int kernel_table(const KernelInfo* const** out) {
   };
   constexpr int kSingle = (int)(sizeof single / sizeof single[0]);
   static const auto table = [] {
-    std::array<const KernelInfo*, kSingle + kRouteBackwardForms + kGemvForms> t{};
+    std::array<const KernelInfo*, kSingle + kRouteBackwardForms + kGemvForms + kGemmBf16Forms> t{};
     int n = 0;
     for (const KernelInfo* k : single) t[n++] = k;
     for (const KernelInfo& k : kInfoRouteBackward) t[n++] = &k;
     for (const KernelInfo& k : kInfoGemvFp4) t[n++] = &k;
+    for (const KernelInfo& k : kInfoGemmBf16) t[n++] = &k;
     return t;
   }();
   *out = table.data();
@@ -613,6 +614,115 @@ fgg_status fgg_moe_gemv_fp4(int32_t G, int64_t T, int32_t k, int64_t N, int64_t 
                                      (const uint8_t*)b, (const uint8_t*)b_scales, topk_ids, topk_w,
                                      act == FGG_ACT_SILU_MUL, out, out_dtype == FGG_BF16, ldo, num_cus,
                                      (hipStream_t)stream));
+}
+
+// Shapes of the bf16 products: segments of M rows, weights [G][N][K].
+static fgg_status segments_check(int32_t G, int64_t M, int64_t N, int64_t K, const int32_t* offsets,
+                                 const int32_t* counts) {
+  if (G < 1 || G > 1024 || M < 0 || N < 0 || K < 0) return FGG_ERR_INVALID_VALUE;
+  if ((!offsets && (G != 1 || counts)) || !aligned(offsets, 4) || !aligned(counts, 4)) return FGG_ERR_INVALID_VALUE;
+  // (16-byte pieces of a row, and 32-bit offsets of 256 rows)
+  if (N == 0 || K == 0 || N % 8 != 0 || K % 8 != 0 || N > fgg::kMaxBf16Width || K > fgg::kMaxBf16Width ||
+      M > (int64_t)INT32_MAX)
+    return FGG_ERR_UNSUPPORTED;
+  return FGG_OK;
+}
+
+// A matrix of `cols` columns and rows of 16-byte pieces; NULL only where `needed` is false.
+static fgg_status rows_operand(const void* p, int64_t ld, int64_t cols, int64_t el, bool needed) {
+  if (needed && !p) return FGG_ERR_INVALID_VALUE;
+  if (ld < cols || (ld * el) % 16 != 0 || !aligned(p, 16)) return FGG_ERR_INVALID_VALUE;
+  return ld > fgg::kMaxBf16Width ? FGG_ERR_UNSUPPORTED : FGG_OK;
+}
+
+#define FGG_TRY(call)                     \
+  do {                                    \
+    const fgg_status s_ = (call);         \
+    if (s_ != FGG_OK) return s_;          \
+  } while (0)
+
+fgg_status fgg_grouped_linear(int32_t G, int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx, const void* w,
+                              const int32_t* offsets, const int32_t* counts, void* y, fgg_dtype y_dtype, int64_t ldy,
+                              void* stream) {
+  FGG_TRY(segments_check(G, M, N, K, offsets, counts));
+  if (!float_type(y_dtype)) return FGG_ERR_UNSUPPORTED;
+  FGG_TRY(rows_operand(x, ldx, K, 2, M > 0));
+  FGG_TRY(rows_operand(w, K, K, 2, M > 0));
+  FGG_TRY(rows_operand(y, ldy, N, (int64_t)float_size(y_dtype), M > 0));
+  if (fgg::gemm_bf16_tiles(offsets, G, M, N, false) > fgg::kMaxBf16Tiles) return FGG_ERR_UNSUPPORTED;
+  if (M == 0) return FGG_OK;
+  FGG_TRY(device_check(nullptr));
+  return finish(fgg::launch_grouped_linear({offsets, counts, G, M}, N, K, (const uint16_t*)x, ldx, (const uint16_t*)w,
+                                           y, y_dtype == FGG_F32, ldy, (hipStream_t)stream));
+}
+
+fgg_status fgg_grouped_linear_backward_input(int32_t G, int64_t M, int64_t N, int64_t K, const void* dy, int64_t lddy,
+                                             const void* w, const int32_t* offsets, const int32_t* counts, void* dx,
+                                             fgg_dtype dx_dtype, int64_t lddx, void* stream) {
+  FGG_TRY(segments_check(G, M, N, K, offsets, counts));
+  if (!float_type(dx_dtype)) return FGG_ERR_UNSUPPORTED;
+  FGG_TRY(rows_operand(dy, lddy, N, 2, M > 0));
+  FGG_TRY(rows_operand(w, K, K, 2, M > 0));
+  FGG_TRY(rows_operand(dx, lddx, K, (int64_t)float_size(dx_dtype), M > 0));
+  if (fgg::gemm_bf16_tiles(offsets, G, M, K, false) > fgg::kMaxBf16Tiles) return FGG_ERR_UNSUPPORTED;
+  if (M == 0) return FGG_OK;
+  FGG_TRY(device_check(nullptr));
+  return finish(fgg::launch_grouped_dx({offsets, counts, G, M}, N, K, (const uint16_t*)dy, lddy, (const uint16_t*)w, dx,
+                                       dx_dtype == FGG_F32, lddx, (hipStream_t)stream));
+}
+
+fgg_status fgg_grouped_linear_backward_weight_workspace(int32_t G, int64_t M, int64_t N, int64_t K, size_t* bytes) {
+  if (!bytes || G < 1 || G > 1024 || M < 0 || N < 0 || K < 0) return FGG_ERR_INVALID_VALUE;
+  *bytes = 0;
+  return FGG_OK;
+}
+
+fgg_status fgg_grouped_linear_backward_weight(int32_t G, int64_t M, int64_t N, int64_t K, const void* dy, int64_t lddy,
+                                              const void* x, int64_t ldx, const int32_t* offsets,
+                                              const int32_t* counts, void* dw, fgg_dtype dw_dtype,
+                                              int32_t accumulate, void* workspace, size_t ws_bytes, void* stream) {
+  FGG_TRY(segments_check(G, M, N, K, offsets, counts));
+  if (!float_type(dw_dtype)) return FGG_ERR_UNSUPPORTED;
+  FGG_TRY(rows_operand(dy, lddy, N, 2, M > 0));
+  FGG_TRY(rows_operand(x, ldx, K, 2, M > 0));
+  FGG_TRY(rows_operand(dw, K, K, (int64_t)float_size(dw_dtype), true));
+  if (fgg::gemm_bf16_dw_tiles(G, N, K) > fgg::kMaxBf16Tiles) return FGG_ERR_UNSUPPORTED;
+  FGG_TRY(device_check(nullptr));
+  return finish(fgg::launch_grouped_dw({offsets, counts, G, M}, N, K, (const uint16_t*)dy, lddy, (const uint16_t*)x,
+                                       ldx, dw, dw_dtype == FGG_F32, accumulate != 0, (hipStream_t)stream));
+}
+
+fgg_status fgg_grouped_gated(int32_t G, int64_t M, int64_t I, int64_t K, const void* x, int64_t ldx, const void* w,
+                             const int32_t* offsets, const int32_t* counts, void* a, int64_t lda, void* h,
+                             int64_t ldh, void* stream) {
+  FGG_TRY(segments_check(G, M, I, K, offsets, counts));
+  FGG_TRY(rows_operand(x, ldx, K, 2, M > 0));
+  FGG_TRY(rows_operand(w, K, K, 2, M > 0));
+  FGG_TRY(rows_operand(a, lda, I, 2, M > 0));
+  if (h) FGG_TRY(rows_operand(h, ldh, 2 * I, 2, true));
+  if (fgg::gemm_bf16_tiles(offsets, G, M, I, true) > fgg::kMaxBf16Tiles) return FGG_ERR_UNSUPPORTED;
+  if (M == 0) return FGG_OK;
+  FGG_TRY(device_check(nullptr));
+  return finish(fgg::launch_grouped_gated({offsets, counts, G, M}, I, K, (const uint16_t*)x, ldx, (const uint16_t*)w,
+                                          (uint16_t*)a, lda, (uint16_t*)h, ldh, (hipStream_t)stream));
+}
+
+fgg_status fgg_grouped_gated_backward(int32_t G, int64_t M, int64_t I, int64_t N, const void* dy, int64_t lddy,
+                                      const void* w_down, const void* h, int64_t ldh, const int32_t* offsets,
+                                      const int32_t* counts, void* dh, int64_t lddh, void* a, int64_t lda,
+                                      void* stream) {
+  FGG_TRY(segments_check(G, M, I, N, offsets, counts));
+  FGG_TRY(rows_operand(dy, lddy, N, 2, M > 0));
+  FGG_TRY(rows_operand(w_down, I, I, 2, M > 0));
+  FGG_TRY(rows_operand(h, ldh, 2 * I, 2, M > 0));
+  FGG_TRY(rows_operand(dh, lddh, 2 * I, 2, M > 0));
+  if (a) FGG_TRY(rows_operand(a, lda, I, 2, true));
+  if (fgg::gemm_bf16_tiles(offsets, G, M, I, false) > fgg::kMaxBf16Tiles) return FGG_ERR_UNSUPPORTED;
+  if (M == 0) return FGG_OK;
+  FGG_TRY(device_check(nullptr));
+  return finish(fgg::launch_grouped_gated_backward({offsets, counts, G, M}, I, N, (const uint16_t*)dy, lddy,
+                                                   (const uint16_t*)w_down, (const uint16_t*)h, ldh, (uint16_t*)dh,
+                                                   lddh, (uint16_t*)a, lda, (hipStream_t)stream));
 }
 
 int32_t fgg_kernel_count(void) {

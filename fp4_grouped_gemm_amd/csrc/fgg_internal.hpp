@@ -41,8 +41,9 @@ extern const KernelInfo kInfoQuantE4m3_1x128, kInfoQuantE4m3_128x128, kInfoQuant
     kInfoW4a4Gemm, kInfoMxfp4Gemm, kInfoRoute, kInfoRowsScatter, kInfoRowsCollect, kInfoRowsScatterDot,
     kInfoRowsCollectDot;
 // (kernels with several forms: one entry for each that differs in its workgroup)
-constexpr int kRouteBackwardForms = 7, kGemvForms = 21;
-extern const KernelInfo kInfoRouteBackward[kRouteBackwardForms], kInfoGemvFp4[kGemvForms];
+constexpr int kRouteBackwardForms = 7, kGemvForms = 21, kGemmBf16Forms = 5;
+extern const KernelInfo kInfoRouteBackward[kRouteBackwardForms], kInfoGemvFp4[kGemvForms],
+    kInfoGemmBf16[kGemmBf16Forms];
 
 enum class QuantKind { E4M3_1x128, E4M3_128x128, E2M1_1x16, E2M1_E8M0_1x32 };
 
@@ -150,5 +151,32 @@ hipError_t launch_gemv_fp4(bool tiled, int32_t G, int64_t T, int32_t k, int64_t 
                            bool x_bf16, int64_t ldx, bool per_slot, const uint8_t* b, const uint8_t* s,
                            const int32_t* ids, const float* w, bool silu, void* out, bool out_bf16, int64_t ldo,
                            int num_cus, hipStream_t st);
+
+// Row segments of the bf16 products: rows [offsets[g], offsets[g + 1]) of M, the first counts[g] of them
+// (nullable); without offsets one segment of M rows.
+struct Segments {
+  const int32_t *offsets, *counts;
+  int32_t G;
+  int64_t M;
+};
+// Workgroups of a launch at most (the rows' forms; the weights' gradient).
+int64_t gemm_bf16_tiles(const int32_t* offsets, int32_t G, int64_t M, int64_t cols, bool gated);
+int64_t gemm_bf16_dw_tiles(int32_t G, int64_t N, int64_t K);
+constexpr int64_t kMaxBf16Tiles = 0xFFFFFFFFll / 512 - 256;
+// Row strides and widths at most: 256 rows of them stay below 2^31 bytes.
+constexpr int64_t kMaxBf16Width = (int64_t(1) << 22) - 8;
+
+hipError_t launch_grouped_linear(const Segments& s, int64_t N, int64_t K, const uint16_t* x, int64_t ldx,
+                                 const uint16_t* w, void* y, bool y_f32, int64_t ldy, hipStream_t st);
+hipError_t launch_grouped_dx(const Segments& s, int64_t N, int64_t K, const uint16_t* dy, int64_t lddy,
+                             const uint16_t* w, void* dx, bool dx_f32, int64_t lddx, hipStream_t st);
+hipError_t launch_grouped_dw(const Segments& s, int64_t N, int64_t K, const uint16_t* dy, int64_t lddy,
+                             const uint16_t* x, int64_t ldx, void* dw, bool dw_f32, bool accumulate, hipStream_t st);
+hipError_t launch_grouped_gated(const Segments& s, int64_t I, int64_t K, const uint16_t* x, int64_t ldx,
+                                const uint16_t* w, uint16_t* act, int64_t lda, uint16_t* h, int64_t ldh,
+                                hipStream_t st);
+hipError_t launch_grouped_gated_backward(const Segments& s, int64_t I, int64_t N, const uint16_t* dy, int64_t lddy,
+                                         const uint16_t* w_down, const uint16_t* h, int64_t ldh, uint16_t* dh,
+                                         int64_t lddh, uint16_t* act, int64_t lda, hipStream_t st);
 
 }  // namespace fgg

@@ -539,6 +539,59 @@ fgg_status fgg_moe_gemv_fp4(int32_t G, int64_t T, int32_t k, int64_t N, int64_t 
                             const int32_t* topk_ids, const float* topk_w, fgg_act act, void* out,
                             fgg_dtype out_dtype, int64_t ldo, void* stream);
 
+/*
+ * Products of unquantized (bf16) rows with their segment's weights: the linear layer of an
+ * expert layer, its gradients, and the gated block.  They stand between the calls above:
+ * fgg_moe_permute_rows makes the rows and fgg_moe_unpermute_rows takes them back.
+ *
+ * Segment g (one expert, or with offsets NULL and G = 1 all M rows) is rows [offsets[g],
+ * offsets[g + 1]), of which with counts the first counts[g]; offsets does not fall, segments
+ * may begin anywhere (no alignment) and be empty, and no row at or past M belongs to one, whatever
+ * offsets hold.  Rows of no segment (padding) are neither read nor written, so their contents
+ * (NaN too) reach no result, and outputs keep what they held there.
+ *   linear                      y[r][n]  = sum_k x[r][k] w[g][n][k]
+ *   linear_backward_input       dx[r][k] = sum_n dy[r][n] w[g][n][k]
+ *   linear_backward_weight      dw[g][n][k] (+)= sum over the segment's r of dy[r][n] x[r][k]
+ *                               (an empty segment's gradient is 0; accumulate != 0 adds to dw)
+ *   gated                       hg[r][i] = sum_k x[r][k] w[g][i][k],  hu[r][i] = sum_k x[r][k] w[g][I + i][k]
+ *                               a[r][i] = hg / (1 + e^-hg) * hu       (h, optional, receives [hg | hu])
+ *   gated_backward              da[r][i] = sum_n dy[r][n] w_down[g][n][i] (the gradient of a, through the
+ *                               linear layer w_down that follows; it stays in registers in fp32)
+ *                               s = 1 / (1 + e^-hg);  dh[r] = [da hu s (1 + hg (1 - s)) | da hg s]
+ *                               a[r][i] = hg s hu                     (optional: what w_down's gradient needs)
+ * With these, the block's backward pass is gated_backward, backward_weight(dy, a) for w_down,
+ * backward_input(dh) and backward_weight(dh, x) for w.
+ *
+ * x, dy, h, dh, a, w, w_down: bf16; y, dx, dw: FGG_BF16 or FGG_F32.  Sums run in fp32 (exact products)
+ * and results are rounded once (gated_backward reads h as the forward rounded it).  Weights are
+ * dense, w [G][N][K] (gated: [G][2I][K], w_down [G][N][I]); dw is dense [G][N][K].  Rows may be strided
+ * (ld >= the row's width).  Base pointers are 16-byte aligned and strides whole 16-byte pieces.
+ * N, K (and I) are multiples of 8 from 8 to 2^22 - 8, strides at most that, 1 <= G <= 1024,
+ * M < 2^31 (FGG_ERR_UNSUPPORTED beyond).  M == 0 is a no-op, except that backward_weight
+ * writes zeros.  Outputs must not overlap inputs.  Results do not depend on an order of arrival:
+ * the same call gives the same bits.
+ * workspace: fgg_grouped_linear_backward_weight_workspace bytes, 16-byte aligned (0: may be NULL);
+ * contents need not be kept or cleared, and calls that may overlap in time need one each.
+ */
+fgg_status fgg_grouped_linear(int32_t G, int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx, const void* w,
+                              const int32_t* offsets, const int32_t* counts, void* y, fgg_dtype y_dtype, int64_t ldy,
+                              void* stream);
+fgg_status fgg_grouped_linear_backward_input(int32_t G, int64_t M, int64_t N, int64_t K, const void* dy, int64_t lddy,
+                                             const void* w, const int32_t* offsets, const int32_t* counts, void* dx,
+                                             fgg_dtype dx_dtype, int64_t lddx, void* stream);
+fgg_status fgg_grouped_linear_backward_weight_workspace(int32_t G, int64_t M, int64_t N, int64_t K, size_t* bytes);
+fgg_status fgg_grouped_linear_backward_weight(int32_t G, int64_t M, int64_t N, int64_t K, const void* dy, int64_t lddy,
+                                              const void* x, int64_t ldx, const int32_t* offsets,
+                                              const int32_t* counts, void* dw, fgg_dtype dw_dtype,
+                                              int32_t accumulate, void* workspace, size_t ws_bytes, void* stream);
+fgg_status fgg_grouped_gated(int32_t G, int64_t M, int64_t I, int64_t K, const void* x, int64_t ldx, const void* w,
+                             const int32_t* offsets, const int32_t* counts, void* a, int64_t lda, void* h,
+                             int64_t ldh, void* stream);
+fgg_status fgg_grouped_gated_backward(int32_t G, int64_t M, int64_t I, int64_t N, const void* dy, int64_t lddy,
+                                      const void* w_down, const void* h, int64_t ldh, const int32_t* offsets,
+                                      const int32_t* counts, void* dh, int64_t lddh, void* a, int64_t lda,
+                                      void* stream);
+
 #ifdef __cplusplus
 }
 #endif
