@@ -22,7 +22,7 @@ __all__ = [
     "moe_route", "moe_route_backward", "moe_permute_rows", "moe_permute_rows_backward", "moe_unpermute_rows",
     "moe_unpermute_rows_backward", "moe_gemv_fp4", "grouped_linear", "grouped_linear_backward_input",
     "grouped_linear_backward_weight", "grouped_linear_backward_weight_workspace_bytes", "grouped_gated",
-    "grouped_gated_backward",
+    "grouped_gated_backward", "lora_add", "lora_workspace_bytes",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -118,6 +118,8 @@ def load_library():
         "fgg_grouped_linear_backward_weight": ([I32, I64, I64, I64, P, I64, P, I64, P, P, P, I32, I32, P, SZ, P], I32),
         "fgg_grouped_gated": ([I32, I64, I64, I64, P, I64, P, P, P, P, I64, P, I64, P], I32),
         "fgg_grouped_gated_backward": ([I32, I64, I64, I64, P, I64, P, P, I64, P, P, P, I64, P, I64, P], I32),
+        "fgg_lora_workspace": ([I64, I32, I32, I64, I64, ctypes.POINTER(SZ)], I32),
+        "fgg_lora_add": ([I64, I32, I32, I64, I64, P, I64, P, P, P, P, P, I64, P, I32, I64, P, SZ, P], I32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -818,3 +820,34 @@ def grouped_gated_backward(dy, w_down, h, offsets=None, counts=None, out=None, a
     _call("fgg_grouped_gated_backward", dev, G, M, I, N, dy.data_ptr(), lddy, w_down.data_ptr(), h.data_ptr(), ldh,
           _addr(offsets), _addr(counts), out.data_ptr(), ldo, _addr(a), lda)
     return out, a
+
+
+# ------------------------------------------------------------- low-rank adapters
+
+def lora_workspace_bytes(T: int, L: int, r: int, N: int, K: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("fgg_lora_workspace", load_library().fgg_lora_workspace(T, L, r, N, K, ctypes.byref(n)))
+    return n.value
+
+
+def lora_add(base, x, ids, a, b, scales=None, out=None, workspace=None):
+    """Low-rank adapters beside a shared projection (fgg_lora_add): out[t] = base[t] + scales[i] (x[t] a[i]^T) b[i]^T,
+    i = ids[t] (outside [0, L): base[t]).  base [T, N] fp32 or bf16, x bf16 [T, K], ids int32 [T], a bf16 [L, r, K],
+    b bf16 [L, N, r], scales fp32 [L].  ``out`` may be ``base`` itself; workspace: lora_workspace_bytes, uint8."""
+    ldb, ldx = _float_rows(base, "base"), _float_rows(x, "x", torch.bfloat16)
+    (T, K), N, dev = x.shape, base.shape[1], x.device
+    L, r = a.shape[0], a.shape[1]
+    assert base.shape[0] == T and base.device == dev, "base"
+    _dense(ids, "ids", dev, torch.int32, (T,))
+    _dense(a, "a", dev, torch.bfloat16, (L, r, K))
+    _dense(b, "b", dev, torch.bfloat16, (L, N, r))
+    _dense(scales, "scales", dev, torch.float32, (L,))
+    out, ldo = _rows_out(out, (T, N), base, "out")
+    if workspace is None:
+        workspace = torch.empty(lora_workspace_bytes(T, L, r, N, K), dtype=torch.uint8, device=dev)
+    else:
+        _dense(workspace, "workspace", dev, torch.uint8)
+    _call("fgg_lora_add", dev, T, L, r, N, K, x.data_ptr(), ldx, ids.data_ptr(), a.data_ptr(), b.data_ptr(),
+          _addr(scales), base.data_ptr(), ldb, out.data_ptr(), _FLOAT[base.dtype], ldo, workspace.data_ptr(),
+          workspace.numel())
+    return out

@@ -101,12 +101,13 @@ int kernel_table(const KernelInfo* const** out) {
   };
   constexpr int kSingle = (int)(sizeof single / sizeof single[0]);
   static const auto table = [] {
-    std::array<const KernelInfo*, kSingle + kRouteBackwardForms + kGemvForms + kGemmBf16Forms> t{};
+    std::array<const KernelInfo*, kSingle + kRouteBackwardForms + kGemvForms + kGemmBf16Forms + kLoraForms> t{};
     int n = 0;
     for (const KernelInfo* k : single) t[n++] = k;
     for (const KernelInfo& k : kInfoRouteBackward) t[n++] = &k;
     for (const KernelInfo& k : kInfoGemvFp4) t[n++] = &k;
     for (const KernelInfo& k : kInfoGemmBf16) t[n++] = &k;
+    for (const KernelInfo& k : kInfoLora) t[n++] = &k;
     return t;
   }();
   *out = table.data();
@@ -723,6 +724,44 @@ fgg_status fgg_grouped_gated_backward(int32_t G, int64_t M, int64_t I, int64_t N
   return finish(fgg::launch_grouped_gated_backward({offsets, counts, G, M}, I, N, (const uint16_t*)dy, lddy,
                                                    (const uint16_t*)w_down, (const uint16_t*)h, ldh, (uint16_t*)dh,
                                                    lddh, (uint16_t*)a, lda, (hipStream_t)stream));
+}
+
+static fgg_status lora_check(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K) {
+  if (T < 0 || L < 1 || r < 1 || N < 0 || K < 0) return FGG_ERR_INVALID_VALUE;
+  // (16-byte pieces of a row; 32-bit counts of items, and grids of 16 tokens by 32 columns)
+  if (N == 0 || K == 0 || N % 8 != 0 || K % 8 != 0 || r % 8 != 0 || r > 128 || N > (int64_t(1) << 20) ||
+      K > (int64_t(1) << 20) || T > (int64_t(1) << 26))
+    return FGG_ERR_UNSUPPORTED;
+  return FGG_OK;
+}
+
+fgg_status fgg_lora_workspace(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K, size_t* bytes) {
+  if (!bytes) return FGG_ERR_INVALID_VALUE;
+  FGG_TRY(lora_check(T, L, r, N, K));
+  *bytes = fgg::lora_workspace_bytes(T, L, r, K);
+  return FGG_OK;
+}
+
+fgg_status fgg_lora_add(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K, const void* x, int64_t ldx,
+                        const int32_t* ids, const void* a, const void* b, const float* scales, const void* base,
+                        int64_t ldb, void* out, fgg_dtype dtype, int64_t ldo, void* workspace, size_t ws_bytes,
+                        void* stream) {
+  FGG_TRY(lora_check(T, L, r, N, K));
+  if (!float_type(dtype)) return FGG_ERR_UNSUPPORTED;
+  const int64_t el = (int64_t)float_size(dtype);
+  if (ldx < K || ldx % 8 != 0 || ldb < N || ldo < N || ldb * el % 16 != 0 || ldo * el % 16 != 0)
+    return FGG_ERR_INVALID_VALUE;
+  if (T == 0) return FGG_OK;
+  if (base == out && ldb != ldo) return FGG_ERR_INVALID_VALUE;
+  if (!x || !ids || !a || !b || !base || !out || !workspace) return FGG_ERR_INVALID_VALUE;
+  if (!aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(base, 16) || !aligned(out, 16) ||
+      !aligned(ids, 4) || !aligned(scales, 4) || !aligned(workspace, 16) ||
+      ws_bytes < fgg::lora_workspace_bytes(T, L, r, K))
+    return FGG_ERR_INVALID_VALUE;
+  FGG_TRY(device_check(nullptr));
+  return finish(fgg::launch_lora(T, L, r, N, K, (const uint16_t*)x, ldx, ids, (const uint16_t*)a, (const uint16_t*)b,
+                                 scales, base, ldb, out, dtype == FGG_F32, ldo, (float*)workspace,
+                                 (hipStream_t)stream));
 }
 
 int32_t fgg_kernel_count(void) {

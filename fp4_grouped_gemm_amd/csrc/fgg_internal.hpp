@@ -41,9 +41,9 @@ extern const KernelInfo kInfoQuantE4m3_1x128, kInfoQuantE4m3_128x128, kInfoQuant
     kInfoW4a4Gemm, kInfoMxfp4Gemm, kInfoRoute, kInfoRowsScatter, kInfoRowsCollect, kInfoRowsScatterDot,
     kInfoRowsCollectDot;
 // (kernels with several forms: one entry for each that differs in its workgroup)
-constexpr int kRouteBackwardForms = 7, kGemvForms = 21, kGemmBf16Forms = 5;
+constexpr int kRouteBackwardForms = 7, kGemvForms = 21, kGemmBf16Forms = 5, kLoraForms = 14;
 extern const KernelInfo kInfoRouteBackward[kRouteBackwardForms], kInfoGemvFp4[kGemvForms],
-    kInfoGemmBf16[kGemmBf16Forms];
+    kInfoGemmBf16[kGemmBf16Forms], kInfoLora[kLoraForms];
 
 enum class QuantKind { E4M3_1x128, E4M3_128x128, E2M1_1x16, E2M1_E8M0_1x32 };
 
@@ -178,5 +178,11 @@ hipError_t launch_grouped_gated(const Segments& s, int64_t I, int64_t K, const u
 hipError_t launch_grouped_gated_backward(const Segments& s, int64_t I, int64_t N, const uint16_t* dy, int64_t lddy,
                                          const uint16_t* w_down, const uint16_t* h, int64_t ldh, uint16_t* dh,
                                          int64_t lddh, uint16_t* act, int64_t lda, hipStream_t st);
+
+// Low-rank adapters: the per-token low-rank sums (workspace: the chunks' fp32 sums), then the result on top of base.
+size_t lora_workspace_bytes(int64_t T, int32_t L, int32_t r, int64_t K);
+hipError_t launch_lora(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K, const uint16_t* x, int64_t ldx,
+                       const int32_t* ids, const uint16_t* a, const uint16_t* b, const float* scales, const void* base,
+                       int64_t ldb, void* out, bool f32, int64_t ldo, float* ws, hipStream_t st);
 
 }  // namespace fgg

@@ -592,6 +592,30 @@ fgg_status fgg_grouped_gated_backward(int32_t G, int64_t M, int64_t I, int64_t N
                                       const int32_t* counts, void* dh, int64_t lddh, void* a, int64_t lda,
                                       void* stream);
 
+/*
+ * fgg_lora_add — low-rank adapters of many requests beside a projection that all tokens share
+ * (the base: an output of fgg_grouped_linear, fgg_scaled_gemm, fgg_moe_gemv_fp4, ...):
+ *   out[t][n] = base[t][n] + scales[i] * sum_j (sum_k x[t][k] a[i][j][k]) b[i][n][j],   i = ids[t]
+ * and out[t] = base[t] for a token whose id is outside [0, L).  Where fgg_epilogue has one pair of
+ * factors for every row, here each token brings its own; tokens of one adapter need not be
+ * neighbours (they cost least when they are).  No token's result depends on another adapter's or
+ * token's contents.  Sums run in fp32, the inner sums enter the outer product to 2^-17 (out bf16)
+ * or 2^-24 (out fp32) of their value, and the result is rounded once.  The same call gives the
+ * same bits.
+ * x: bf16 [T][ldx], ids: [T] int32, a: bf16 [L][r][K], b: bf16 [L][N][r], scales: fp32 [L] or NULL (1);
+ * base, out: [T][ldb], [T][ldo] of dtype (FGG_BF16 or FGG_F32); out may be base itself (same pointer
+ * and stride), else it must not overlap an input.  Base pointers are 16-byte aligned and row strides
+ * whole 16-byte pieces; N, K and r are multiples of 8, r <= 128, N, K <= 2^20, T <= 2^26
+ * (FGG_ERR_UNSUPPORTED beyond).  workspace: fgg_lora_workspace bytes, 16-byte aligned, its
+ * contents need not be kept or cleared; calls that may overlap in time need one each.  T == 0 is a
+ * no-op.
+ */
+fgg_status fgg_lora_workspace(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K, size_t* bytes);
+fgg_status fgg_lora_add(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K, const void* x, int64_t ldx,
+                        const int32_t* ids, const void* a, const void* b, const float* scales, const void* base,
+                        int64_t ldb, void* out, fgg_dtype dtype, int64_t ldo, void* workspace, size_t ws_bytes,
+                        void* stream);
+
 #ifdef __cplusplus
 }
 #endif
