@@ -101,13 +101,15 @@ int kernel_table(const KernelInfo* const** out) {
   };
   constexpr int kSingle = (int)(sizeof single / sizeof single[0]);
   static const auto table = [] {
-    std::array<const KernelInfo*, kSingle + kRouteBackwardForms + kGemvForms + kGemmBf16Forms + kLoraForms> t{};
+    std::array<const KernelInfo*, kSingle + kRouteBackwardForms + kGemvForms + kGemmBf16Forms + kLoraForms + 6> t{};
     int n = 0;
     for (const KernelInfo* k : single) t[n++] = k;
     for (const KernelInfo& k : kInfoRouteBackward) t[n++] = &k;
     for (const KernelInfo& k : kInfoGemvFp4) t[n++] = &k;
     for (const KernelInfo& k : kInfoGemmBf16) t[n++] = &k;
     for (const KernelInfo& k : kInfoLora) t[n++] = &k;
+    for (const KernelInfo& k : kInfoRowsBf16) t[n++] = &k;
+    for (const KernelInfo& k : kInfoDwJoin) t[n++] = &k;
     return t;
   }();
   *out = table.data();
@@ -674,7 +676,7 @@ fgg_status fgg_grouped_linear_backward_input(int32_t G, int64_t M, int64_t N, in
 
 fgg_status fgg_grouped_linear_backward_weight_workspace(int32_t G, int64_t M, int64_t N, int64_t K, size_t* bytes) {
   if (!bytes || G < 1 || G > 1024 || M < 0 || N < 0 || K < 0) return FGG_ERR_INVALID_VALUE;
-  *bytes = 0;
+  *bytes = fgg::gemm_bf16_dw_workspace(G, M, N, K);
   return FGG_OK;
 }
 
@@ -688,9 +690,12 @@ fgg_status fgg_grouped_linear_backward_weight(int32_t G, int64_t M, int64_t N, i
   FGG_TRY(rows_operand(x, ldx, K, 2, M > 0));
   FGG_TRY(rows_operand(dw, K, K, (int64_t)float_size(dw_dtype), true));
   if (fgg::gemm_bf16_dw_tiles(G, N, K) > fgg::kMaxBf16Tiles) return FGG_ERR_UNSUPPORTED;
+  const size_t need = fgg::gemm_bf16_dw_workspace(G, M, N, K);
+  if (need > 0 && (!workspace || ws_bytes < need || !aligned(workspace, 16))) return FGG_ERR_INVALID_VALUE;
   FGG_TRY(device_check(nullptr));
   return finish(fgg::launch_grouped_dw({offsets, counts, G, M}, N, K, (const uint16_t*)dy, lddy, (const uint16_t*)x,
-                                       ldx, dw, dw_dtype == FGG_F32, accumulate != 0, (hipStream_t)stream));
+                                       ldx, dw, dw_dtype == FGG_F32, accumulate != 0, (float*)workspace,
+                                       (hipStream_t)stream));
 }
 
 fgg_status fgg_grouped_gated(int32_t G, int64_t M, int64_t I, int64_t K, const void* x, int64_t ldx, const void* w,

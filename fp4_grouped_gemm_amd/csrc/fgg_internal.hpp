@@ -41,9 +41,10 @@ extern const KernelInfo kInfoQuantE4m3_1x128, kInfoQuantE4m3_128x128, kInfoQuant
     kInfoW4a4Gemm, kInfoMxfp4Gemm, kInfoRoute, kInfoRowsScatter, kInfoRowsCollect, kInfoRowsScatterDot,
     kInfoRowsCollectDot;
 // (kernels with several forms: one entry for each that differs in its workgroup)
-constexpr int kRouteBackwardForms = 7, kGemvForms = 21, kGemmBf16Forms = 5, kLoraForms = 14;
+constexpr int kRouteBackwardForms = 7, kGemvForms = 21, kGemmBf16Forms = 15, kLoraForms = 14;
 extern const KernelInfo kInfoRouteBackward[kRouteBackwardForms], kInfoGemvFp4[kGemvForms],
-    kInfoGemmBf16[kGemmBf16Forms], kInfoLora[kLoraForms];
+    kInfoGemmBf16[kGemmBf16Forms], kInfoLora[kLoraForms], kInfoRowsBf16[2],
+    kInfoDwJoin[4];
 
 enum class QuantKind { E4M3_1x128, E4M3_128x128, E2M1_1x16, E2M1_E8M0_1x32 };
 
@@ -171,7 +172,10 @@ hipError_t launch_grouped_linear(const Segments& s, int64_t N, int64_t K, const 
 hipError_t launch_grouped_dx(const Segments& s, int64_t N, int64_t K, const uint16_t* dy, int64_t lddy,
                              const uint16_t* w, void* dx, bool dx_f32, int64_t lddx, hipStream_t st);
 hipError_t launch_grouped_dw(const Segments& s, int64_t N, int64_t K, const uint16_t* dy, int64_t lddy,
-                             const uint16_t* x, int64_t ldx, void* dw, bool dw_f32, bool accumulate, hipStream_t st);
+                             const uint16_t* x, int64_t ldx, void* dw, bool dw_f32, bool accumulate, float* ws,
+                             hipStream_t st);
+// Workspace of launch_grouped_dw: the fp32 results of the sum's parts (0 where it is taken in one).
+size_t gemm_bf16_dw_workspace(int32_t G, int64_t M, int64_t N, int64_t K);
 hipError_t launch_grouped_gated(const Segments& s, int64_t I, int64_t K, const uint16_t* x, int64_t ldx,
                                 const uint16_t* w, uint16_t* act, int64_t lda, uint16_t* h, int64_t ldh,
                                 hipStream_t st);
@@ -179,6 +183,10 @@ hipError_t launch_grouped_gated_backward(const Segments& s, int64_t I, int64_t N
                                          const uint16_t* w_down, const uint16_t* h, int64_t ldh, uint16_t* dh,
                                          int64_t lddh, uint16_t* act, int64_t lda, hipStream_t st);
 
+// The linear layer and the gated block for few rows per segment (gated: h nullable, out bf16).
+hipError_t launch_rows_bf16(const Segments& s, bool gated, int64_t N, int64_t K, const uint16_t* x, int64_t ldx,
+                            const uint16_t* w, void* out, bool out_f32, int64_t ldo, uint16_t* h, int64_t ldh,
+                            hipStream_t st);
 // Low-rank adapters: the per-token low-rank sums (workspace: the chunks' fp32 sums), then the result on top of base.
 size_t lora_workspace_bytes(int64_t T, int32_t L, int32_t r, int64_t K);
 hipError_t launch_lora(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K, const uint16_t* x, int64_t ldx,

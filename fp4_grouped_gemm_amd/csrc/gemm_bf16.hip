@@ -27,28 +27,43 @@
 //  * one workgroup per tile; a tile's segment is found by a scan over the segments' row counts
 //    in each wave's lanes (no table, no workspace).  Workgroups are dealt to the 8 XCDs in turn,
 //    and 32 consecutive tiles (8 high, 4 wide) go to one XCD, whose L2 then holds what they share.
-#include <type_traits>
 
 #include "fgg_device.hpp"
 #include "fgg_internal.hpp"
+#include "fgg_segments.hpp"
 
 namespace fgg {
 
 namespace {
 
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef short v8s __attribute__((ext_vector_type(8)));
 
-constexpr int BM = 256, BN = 256, BK = 64;
-constexpr int kWaves = 8, kThreads = 64 * kWaves;
-constexpr int kTileBytes = 256 * BK * 2;                 // one operand of one stage: 32 KB
-constexpr int kStageBytes = 2 * kTileBytes;
-constexpr int kQOff = 2 * kTileBytes;                    // LDS: P stage 0, 1, Q stage 0, 1
-constexpr int kLdsBytes = 2 * kStageBytes;
-constexpr int kDma = kTileBytes / 1024 / kWaves;         // 1 KB loads per wave, operand and stage
 constexpr int kXcds = 8, kSM = 8, kChunk = 32;           // tiles of one XCD at a time: 8 high, 4 wide
 constexpr uint32_t kOutside = 0x80000000u;               // offset that the range check rejects
+
+// A workgroup's shape: MxN outputs by WM x WN waves, STAGES buffers of K (32 or 64) deep.
+template <int M_, int N_, int WM_, int WN_, int K_, int STAGES_>
+struct Shape {
+  static constexpr int M = M_, N = N_, WM = WM_, WN = WN_, K = K_, kStages = STAGES_;
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  static constexpr int FI = M / WM / 16, FJ = N / WN / 16;     // a wave's 16 x 16 accumulators
+  static constexpr int kPBytes = M * K * 2, kQBytes = N * K * 2;
+  static constexpr int kQOff = kStages * kPBytes;              // LDS: P stages, then Q stages
+  static constexpr int kStageBytes = kPBytes + kQBytes, kLdsBytes = kStages * kStageBytes;
+  static constexpr int kPDma = kPBytes / 1024 / kWaves, kQDma = kQBytes / 1024 / kWaves;   // 1 KB loads per wave
+};
+using Large = Shape<256, 256, 2, 4, 64, 2>;
+using Medium = Shape<128, 128, 2, 2, 64, 2>;
+using Small = Shape<64, 64, 2, 2, 64, 4>;
+
+// "row" tiles: the 16-byte chunk c of row r lies at chunk c ^ row_key(r), such that the sixteen lanes that one
+// cycle of a ds_read_b128 serves (rows 0..3 and 12..15 of one chunk, 4..11 of the next) hit different chunks.
+template <int K>
+__device__ inline int row_key(int r) {
+  const int b = (r >> 2) & 3;
+  return K == 64 ? r & 7 : ((b ^ (b >> 1)) & 1) << 1 | b >> 1;
+}
 
 enum Form { kLinear, kGated, kDx, kGatedBwd, kDw };
 constexpr bool p_is_col(int f) { return f == kDw; }
@@ -70,37 +85,21 @@ __device__ inline void buf_dma16(const void* base, uint32_t voff, uint32_t lds) 
       : "memory");
 }
 
+// "col" tiles hold W outputs a row, in 32-byte units; the key that unit numbers of row c are mixed with, such
+// that the eight rows that 32 lanes read (0..3 and 8..11 from a multiple of 4) lie in different banks.
+template <int W>
+__device__ inline int col_key(int c) {
+  return W == 64 ? ((c >> 1) & 1) | ((c >> 3) & 1) << 1 : (c & 3) | ((c >> 3) & 1) << 2;
+}
+
 // Eight consecutive summed indices of one output from a "col" tile: two 4 x 16 blocks, 4 rows apart.
+template <int W>
 __device__ inline v8bf tr_read(const uint8_t* p) {
   typedef __attribute__((address_space(3))) v4s lds_v4s;
   const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p));
-  const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 4 * 512));
+  const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 4 * W * 2));
   const v8s v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   return __builtin_bit_cast(v8bf, v);
-}
-
-// 1 / (1 + e^-g) by the hardware's base-2 exponential and reciprocal: within |g| 2^-23 of the
-// value for g < 0 (the product's rounding), far inside the bf16 rounding that follows; an
-// overflowing e^-g gives 0, NaN stays NaN.
-__device__ inline float sigmoid(float g) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896341f));
-}
-
-struct Segment {
-  int64_t first;   // its first row
-  int rows;        // its rows (never past M)
-};
-
-// Segment g, from the caller's arrays, kept inside [0, M) whatever they hold.
-__device__ inline Segment segment_of(const int32_t* offsets, const int32_t* counts, int g, int64_t M) {
-  int64_t s = offsets[g], e = offsets[g + 1];
-  s = s < 0 ? 0 : s > M ? M : s;
-  if (counts) {
-    const int64_t c = counts[g];
-    if (c < e - s) e = s + c;
-  }
-  e = e > M ? M : e;
-  return {s, e > s ? (int)(e - s) : 0};
 }
 
 }  // namespace
@@ -121,15 +120,17 @@ struct BfArgs {
   int64_t ldh;
   int out_f32, accumulate;
   int chunk;                           // consecutive tiles of one XCD
+  int splits;                          // kDw: parts of the sum (gridDim.y), each with its own fp32 result
 };
 
-template <int F>
-__global__ void __launch_bounds__(kThreads, 1) gemm_bf16_kernel(const BfArgs A) {
-  __shared__ __align__(16) uint8_t smem[kLdsBytes];
+template <int F, class S>
+__global__ void __launch_bounds__(S::kThreads, 2) gemm_bf16_kernel(const BfArgs A) {
+  __shared__ __align__(16) uint8_t smem[S::kLdsBytes];
+  constexpr int BM = S::M, BN = S::N, BK = S::K, FI = S::FI, FJ = S::FJ;
   const uint32_t lds_base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave >> 2, wn = wave & 3;
+  const int wm = wave / S::WN, wn = wave % S::WN;
   const int l16 = lane & 15, q = lane >> 4;
 
   // the tile of this workgroup
@@ -181,175 +182,244 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_bf16_kernel(const BfArgs A) 
   // output rows and columns from here on, and the length of the sum
   const int m_here = F == kDw ? (int)A.m_cols - m0 : seg.rows - m0;
   const int n_here = (int)A.n_cols - n0;
-  const int sum = F == kDw ? seg.rows : (int)A.sum;
+  int sum = F == kDw ? seg.rows : (int)A.sum;
+  int first = 0;                       // kDw: this part's first row of the segment
+  if constexpr (F == kDw) {
+    if (A.splits > 1) {
+      const int per = ((sum + BK - 1) / BK + A.splits - 1) / A.splits * BK;
+      first = (int64_t)per * blockIdx.y < sum ? per * (int)blockIdx.y : sum;
+      sum = sum - first < per ? sum - first : per;
+    }
+  }
   const int nk = (sum + BK - 1) / BK;
 
-  const uint16_t* P = A.p + seg.first * A.ldp + (F == kDw ? (int64_t)m0 : (int64_t)m0 * A.ldp);
+  const uint16_t* P = A.p + (seg.first + first) * A.ldp + (F == kDw ? (int64_t)m0 : (int64_t)m0 * A.ldp);
   const uint16_t* Q;
-  if constexpr (F == kDw) Q = A.q + seg.first * A.ldq + n0;
+  if constexpr (F == kDw) Q = A.q + (seg.first + first) * A.ldq + n0;
   else if constexpr (q_is_col(F)) Q = A.q + (int64_t)g * A.q_group + n0;
   else Q = A.q + (int64_t)g * A.q_group + (int64_t)n0 * A.ldq;
 
   // what this wave loads: 1 KB pieces of both tiles; byte offsets from P and Q, kOutside past an edge
-  uint32_t voff_p[kDma], voff_q[kDma];
-  const int r_row = lane >> 3, r_chunk = (lane & 7) ^ r_row;                  // "row": 8 rows a piece
+  uint32_t voff_p[S::kPDma], voff_q[S::kQDma];
+  // "row": a piece is 1 KB of rows of BK elements; this lane's row in it and its chunk's place in memory
+  const int r_row = lane / (BK / 8), r_chunk = (lane % (BK / 8)) ^ row_key<BK>(r_row);
+  // "col": a piece is 1 KB of rows of W outputs; this lane's row in it and its first output
+  auto c_row = [&](int W, int piece) { return piece * (512 / W) + lane / (W / 8); };
+  auto c_col = [&](auto w_tag, int piece) {
+    constexpr int W = decltype(w_tag)::value;
+    const int in = lane % (W / 8);
+    return ((in >> 1) ^ col_key<W>(c_row(W, piece))) * 16 + (in & 1) * 8;
+  };
 #pragma unroll
-  for (int i = 0; i < kDma; ++i) {
-    const int piece = wave * kDma + i;
-    const int c_row = 2 * piece + (lane >> 5);                                // "col": 2 rows a piece
-    const int c_col = ((((lane & 31) >> 1) ^ ((c_row & 3) | ((c_row >> 3) & 1) << 2)) << 4) + (lane & 1) * 8;
+  for (int i = 0; i < S::kPDma; ++i) {
+    const int piece = wave * S::kPDma + i;
     if constexpr (p_is_col(F)) {
-      voff_p[i] = c_col < m_here ? (uint32_t)c_row * (uint32_t)(A.ldp * 2) + c_col * 2 : kOutside;
+      const int c = c_col(std::integral_constant<int, BM>{}, piece);
+      voff_p[i] = c < m_here ? (uint32_t)c_row(BM, piece) * (uint32_t)(A.ldp * 2) + c * 2 : kOutside;
     } else {
-      const int row = piece * 8 + r_row;
+      const int row = piece * (512 / BK) + r_row;
       voff_p[i] = row < m_here ? (uint32_t)row * (uint32_t)(A.ldp * 2) + r_chunk * 16 : kOutside;
     }
+  }
+#pragma unroll
+  for (int i = 0; i < S::kQDma; ++i) {
+    const int piece = wave * S::kQDma + i;
     if constexpr (q_is_col(F)) {
-      voff_q[i] = c_col < n_here ? (uint32_t)c_row * (uint32_t)(A.ldq * 2) + c_col * 2 : kOutside;
+      const int c = c_col(std::integral_constant<int, BN>{}, piece);
+      voff_q[i] = c < n_here ? (uint32_t)c_row(BN, piece) * (uint32_t)(A.ldq * 2) + c * 2 : kOutside;
     } else {
-      const int row = piece * 8 + r_row;
-      if constexpr (F == kGated) {     // tile rows 0..127: gate columns, 128..255: the up columns of the same index
-        voff_q[i] = (row & 127) < n_here ? (uint32_t)(row & 127) * (uint32_t)(A.ldq * 2) + r_chunk * 16 : kOutside;
-      } else {
-        voff_q[i] = row < n_here ? (uint32_t)row * (uint32_t)(A.ldq * 2) + r_chunk * 16 : kOutside;
-      }
+      int row = piece * (512 / BK) + r_row;
+      if (F == kGated) row &= BN / 2 - 1;  // tile rows: gate columns, then the up columns of the same index
+      voff_q[i] = row < n_here ? (uint32_t)row * (uint32_t)(A.ldq * 2) + r_chunk * 16 : kOutside;
     }
   }
-  // (gated: waves 4..7 load the up rows, n_cols rows further)
-  const uint16_t* Qw = F == kGated && wave >= 4 ? Q + A.n_cols * A.ldq : Q;
+  // (gated: the second half of the waves loads the up rows, n_cols rows further)
+  const uint16_t* Qw = F == kGated && wave >= S::kWaves / 2 ? Q + A.n_cols * A.ldq : Q;
   auto issue = [&](int kb, int stage) {
     const uint16_t* p = P + (p_is_col(F) ? (int64_t)kb * BK * A.ldp : (int64_t)kb * BK);
     const uint16_t* qq = Qw + (q_is_col(F) ? (int64_t)kb * BK * A.ldq : (int64_t)kb * BK);
     const int rest = sum - kb * BK;
-    const uint32_t lds = lds_base + stage * kTileBytes + wave * kDma * 1024;
 #pragma unroll
-    for (int i = 0; i < kDma; ++i) {
-      const int c_row = 2 * (wave * kDma + i) + (lane >> 5);
-      uint32_t vp = voff_p[i], vq = voff_q[i];
-      if (rest < BK) {                 // the end of the sum: zeros
-        if ((p_is_col(F) ? c_row : r_chunk * 8) >= rest) vp = kOutside;
-        if ((q_is_col(F) ? c_row : r_chunk * 8) >= rest) vq = kOutside;
-      }
-      buf_dma16(p, vp, lds + i * 1024);
-      buf_dma16(qq, vq, lds + kQOff + i * 1024);
+    for (int i = 0; i < S::kPDma; ++i) {
+      const int piece = wave * S::kPDma + i;
+      uint32_t v = voff_p[i];
+      if (rest < BK && (p_is_col(F) ? c_row(BM, piece) : r_chunk * 8) >= rest) v = kOutside;   // the sum's end: zeros
+      buf_dma16(p, v, lds_base + stage * S::kPBytes + piece * 1024);
+    }
+#pragma unroll
+    for (int i = 0; i < S::kQDma; ++i) {
+      const int piece = wave * S::kQDma + i;
+      uint32_t v = voff_q[i];
+      if (rest < BK && (q_is_col(F) ? c_row(BN, piece) : r_chunk * 8) >= rest) v = kOutside;
+      buf_dma16(qq, v, lds_base + S::kQOff + stage * S::kQBytes + piece * 1024);
     }
   };
 
   // this lane's operand reads: "row": chunk 4 s + q of row l16 (+ 16 per fragment); "col": rows
   // 8 q + (l16 >> 2) (+ 4 for the second half), the fragment's 32-byte unit
-  const int c_key = ((l16 >> 2) & 3) | (q & 1) << 2;
-  const uint32_t c_lane = (8 * q + (l16 >> 2)) * 512 + (l16 & 3) * 8;
+  const int c_line = 8 * q + (l16 >> 2);
   auto read_p = [&](int stage, int s, int i) -> v8bf {
-    const uint8_t* base = smem + stage * kTileBytes;
+    const uint8_t* base = smem + stage * S::kPBytes;
     if constexpr (p_is_col(F)) {
-      return tr_read(base + (c_lane + wm * 256 + ((i ^ c_key) << 5)) + s * 32 * 512);
+      const uint32_t at = c_line * (BM * 2) + (l16 & 3) * 8 + (((S::WM * i + wm) ^ col_key<BM>(c_line)) << 5);
+      return tr_read<BM>(base + at + s * 32 * BM * 2);
     } else {
-      const int row = wm * 128 + l16;
-      return *reinterpret_cast<const v8bf*>(base + (row * 128 + (((4 * s + q) ^ (row & 7)) << 4)) + i * 2048);
+      // (fragments go to the waves in turn, so that a part-filled tile is spread over them)
+      return *reinterpret_cast<const v8bf*>(base + ((16 * wm + l16) * (BK * 2) + (((4 * s + q) ^ row_key<BK>(l16)) << 4)) +
+                                            i * (S::WM * 16 * BK * 2));
     }
   };
   auto read_q = [&](int stage, int s, int n) -> v8bf {
-    const uint8_t* base = smem + kQOff + stage * kTileBytes;
+    const uint8_t* base = smem + S::kQOff + stage * S::kQBytes;
     if constexpr (q_is_col(F)) {
-      return tr_read(base + (c_lane + (((4 * wn + n) ^ c_key) << 5)) + s * 32 * 512);
+      const uint32_t at = c_line * (BN * 2) + (l16 & 3) * 8 + (((FJ * wn + n) ^ col_key<BN>(c_line)) << 5);
+      return tr_read<BN>(base + at + s * 32 * BN * 2);
     } else {
-      const int row = (F == kGated ? 32 : 64) * wn + l16;
-      const int further = F == kGated ? (n & 1) * 16 + (n >> 1) * 128 : 16 * n;
-      return *reinterpret_cast<const v8bf*>(base + (row * 128 + (((4 * s + q) ^ (row & 7)) << 4)) + further * 128);
+      constexpr int kHalf = FJ / 2;
+      const int row = (F == kGated ? 16 * kHalf : 16 * FJ) * wn + l16;
+      const int further = F == kGated ? n % kHalf * 16 + n / kHalf * (BN / 2) : 16 * n;
+      return *reinterpret_cast<const v8bf*>(base + (row * (BK * 2) + (((4 * s + q) ^ row_key<BK>(l16)) << 4)) +
+                                            further * (BK * 2));
     }
   };
 
-  v4f acc[8][4];
+  v4f acc[FI][FJ];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < FI; ++i)
 #pragma unroll
-    for (int n = 0; n < 4; ++n) acc[i][n] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int n = 0; n < FJ; ++n) acc[i][n] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  // One stage: 16 groups (two halves of the depth, 8 row fragments) of 4 MFMAs.  A group's row
-  // fragment is read two groups ahead, the column fragments of the second half during the first.
-  // At group 14 every fragment of the stage has been read: there the next stage's loads are
-  // awaited, the waves meet, the stage after next goes into this stage's buffers, and the last
-  // two groups read the next stage's first fragments, so that the matrix cores have work while
-  // those reads run.  The order is pinned.
-  v8bf fp[3], fq[2][4];
-  auto step = [&](auto st_tag, auto off_tag, int kb) {
-    constexpr int ST = decltype(st_tag)::value;
-    constexpr int R = decltype(off_tag)::value;          // place of the stage's first row fragment in fp
+  if constexpr (FJ == 4) {
+    // One stage: NG groups (32-deep steps x row fragments) of 4 MFMAs.  A group's row fragment is read
+    // two groups ahead, the column fragments of a stage's second step during its first.  Two groups
+    // before the end every fragment of the stage has been read: there the next stage's loads are
+    // awaited, the waves meet, the stage kStages further goes into this stage's buffers, and the last two
+    // groups read the next stage's first fragments, so that the matrix cores have work while those
+    // reads run.  The order is pinned.  NI: row fragments of each wave that hold rows (a tile that is
+    // at most half full does half the work).
+    constexpr int KS = BK / 32, kAhead = S::kStages - 1;
+    v8bf fp[3], fq[2][4];
+    auto step = [&](auto ni_tag, auto no_tag, int kb) {
+      constexpr int NI = decltype(ni_tag)::value, NG = KS * NI;
+      constexpr int NO = decltype(no_tag)::value;        // kb mod 6
+      constexpr int ST = NO % S::kStages, NEXT = (NO + 1) % S::kStages;
+      constexpr int R = NO * NG % 3;                     // place of the stage's first row fragment in fp
 #pragma unroll
-    for (int gi = 0; gi < 16; ++gi) {
-      const int s = gi >> 3, i = gi & 7;
-      if (gi == 14) {
-        __builtin_amdgcn_s_waitcnt(kLgkmZero);
-        wait_vmcnt<0>();
-        block_barrier();
-        if (kb + 2 < nk) issue(kb + 2, ST);
-      }
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[s][n], fp[(R + gi) % 3], acc[i][n], 0, 0, 0);
-        __builtin_amdgcn_sched_barrier(0);
-        if (n == 0) {
-          const int ahead = gi + 2;                       // (of the next stage from group 14 on)
-          fp[(R + ahead) % 3] = ahead < 16 ? read_p(ST, ahead >> 3, ahead & 7) : read_p(ST ^ 1, 0, ahead - 16);
+      for (int gi = 0; gi < NG; ++gi) {
+        const int s = gi / NI, i = gi % NI, now = (KS * NO + s) & 1;
+        if (gi == NG - 2) {
+          __builtin_amdgcn_s_waitcnt(kLgkmZero);
+          if (kb + kAhead < nk) wait_vmcnt<(kAhead - 1) * (S::kPDma + S::kQDma)>();
+          else wait_vmcnt<0>();
+          block_barrier();
+          if (kb + S::kStages < nk) issue(kb + S::kStages, ST);
         }
-        if (n == 2 && gi >= 3 && gi < 7) fq[1][gi - 3] = read_q(ST, 1, gi - 3);
-        if ((n == 1 || n == 3) && gi >= 14) fq[0][2 * (gi - 14) + (n >> 1)] = read_q(ST ^ 1, 0, 2 * (gi - 14) + (n >> 1));
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
-  };
-  if (nk > 0) {
-    issue(0, 0);
-    wait_vmcnt<0>();
-    block_barrier();
-    if (nk > 1) issue(1, 1);
 #pragma unroll
-    for (int n = 0; n < 4; ++n) fq[0][n] = read_q(0, 0, n);
-    fp[0] = read_p(0, 0, 0), fp[1] = read_p(0, 0, 1);
-    // (16 fragments a stage and three places: the first one's place moves on by one)
-    using I0 = std::integral_constant<int, 0>;
-    using I1 = std::integral_constant<int, 1>;
-    using I2 = std::integral_constant<int, 2>;
-    for (int kb = 0; kb < nk; kb += 6) {
-      step(I0{}, I0{}, kb);
-      if (kb + 1 < nk) step(I1{}, I1{}, kb + 1);
-      if (kb + 2 < nk) step(I0{}, I2{}, kb + 2);
-      if (kb + 3 < nk) step(I1{}, I0{}, kb + 3);
-      if (kb + 4 < nk) step(I0{}, I1{}, kb + 4);
-      if (kb + 5 < nk) step(I1{}, I2{}, kb + 5);
+        for (int n = 0; n < 4; ++n) {
+          acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[now][n], fp[(R + gi) % 3], acc[i][n], 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
+          const int ahead = gi + 2;                       // (of the next stage in the last two groups)
+          if (n == 0) fp[(R + ahead) % 3] = ahead < NG ? read_p(ST, ahead / NI, ahead % NI) : read_p(NEXT, 0, ahead - NG);
+          if (KS == 2 && n == 2 && s == 0) {
+            if (NI == 8 ? gi >= 3 && gi < 7 : true) fq[now ^ 1][NI == 8 ? gi - 3 : gi] = read_q(ST, 1, NI == 8 ? gi - 3 : gi);
+          }
+          if ((n == 1 || n == 3) && gi >= NG - 2) {
+            const int k = 2 * (gi - NG + 2) + (n >> 1);
+            fq[now ^ 1][k] = read_q(NEXT, 0, k);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    };
+    auto run = [&](auto ni_tag) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) fq[0][n] = read_q(0, 0, n);
+      fp[0] = read_p(0, 0, 0), fp[1] = read_p(0, 0, 1);
+      for (int kb = 0; kb < nk; kb += 6) {
+        step(ni_tag, std::integral_constant<int, 0>{}, kb);
+        if (kb + 1 < nk) step(ni_tag, std::integral_constant<int, 1>{}, kb + 1);
+        if (kb + 2 < nk) step(ni_tag, std::integral_constant<int, 2>{}, kb + 2);
+        if (kb + 3 < nk) step(ni_tag, std::integral_constant<int, 3>{}, kb + 3);
+        if (kb + 4 < nk) step(ni_tag, std::integral_constant<int, 4>{}, kb + 4);
+        if (kb + 5 < nk) step(ni_tag, std::integral_constant<int, 5>{}, kb + 5);
+      }
+    };
+    if (nk > 0) {
+#pragma unroll
+      for (int i = 0; i < S::kStages; ++i)
+        if (i < nk) issue(i, i);
+      if (nk >= S::kStages) wait_vmcnt<kAhead * (S::kPDma + S::kQDma)>();
+      else wait_vmcnt<0>();
+      block_barrier();
+      if (FI == 8 && m_here <= BM / 2) run(std::integral_constant<int, 4>{});
+      else run(std::integral_constant<int, FI>{});
+    }
+  } else {
+    // The smaller shapes: kStages - 1 stages in flight, several workgroups on a compute unit cover each
+    // other's waits.
+    constexpr int kAhead = S::kStages - 1;
+    auto compute = [&](int stage) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        v8bf fq[FJ], fp[FI];
+#pragma unroll
+        for (int n = 0; n < FJ; ++n) fq[n] = read_q(stage, s, n);
+#pragma unroll
+        for (int i = 0; i < FI; ++i) fp[i] = read_p(stage, s, i);
+#pragma unroll
+        for (int i = 0; i < FI; ++i)
+#pragma unroll
+          for (int n = 0; n < FJ; ++n)
+            acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[n], fp[i], acc[i][n], 0, 0, 0);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (i < nk) issue(i, i);
+    for (int kb = 0; kb < nk; kb += S::kStages) {
+#pragma unroll
+      for (int st = 0; st < S::kStages; ++st) {
+        if (kb + st >= nk) break;
+        // this stage has landed for every wave, and every wave has read the one before
+        if (kb + st + kAhead <= nk) wait_vmcnt<(kAhead - 1) * (S::kPDma + S::kQDma)>();
+        else wait_vmcnt<0>();
+        block_barrier();
+        if (kb + st + kAhead < nk) issue(kb + st + kAhead, (st + kAhead) % S::kStages);
+        compute(st);
+      }
     }
   }
 
   // outputs: lane holds columns 4 q + (0..3) of each fragment for row l16
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = wm * 128 + 16 * i + l16;
+  for (int i = 0; i < FI; ++i) {
+    const int r = 16 * (S::WM * i + wm) + l16;
     if (r >= m_here) continue;
-    const int64_t row = (F == kDw ? (int64_t)g * A.m_cols : seg.first) + m0 + r;
+    const int64_t row = (F == kDw ? ((int64_t)blockIdx.y * A.G + g) * A.m_cols : seg.first) + m0 + r;
     if constexpr (F == kGated) {
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const int c = 32 * wn + 16 * n + 4 * q;
+      for (int n = 0; n < FJ / 2; ++n) {
+        const int c = 16 * (FJ / 2) * wn + 16 * n + 4 * q;
         if (c >= n_here) continue;
         float a[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float gate = acc[i][n][e];
-          a[e] = gate * sigmoid(gate) * acc[i][n + 2][e];
+          a[e] = gate * sigmoid(gate) * acc[i][n + FJ / 2][e];
         }
         *reinterpret_cast<uint2*>((uint16_t*)A.out + row * A.ldo + n0 + c) =
             make_uint2(bf16x2_rne(a[0], a[1]), bf16x2_rne(a[2], a[3]));
         if (A.out2) {
           uint16_t* hrow = A.out2 + row * A.ldo2 + n0 + c;
-          const v4f u = acc[i][n], v = acc[i][n + 2];
+          const v4f u = acc[i][n], v = acc[i][n + FJ / 2];
           *reinterpret_cast<uint2*>(hrow) = make_uint2(bf16x2_rne(u[0], u[1]), bf16x2_rne(u[2], u[3]));
           *reinterpret_cast<uint2*>(hrow + A.n_cols) = make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
         }
       }
     } else {
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const int c = wn * 64 + 16 * n + 4 * q;
+      for (int n = 0; n < FJ; ++n) {
+        const int c = 16 * FJ * wn + 16 * n + 4 * q;
         if (c >= n_here) continue;
         v4f v = acc[i][n];
         if constexpr (F == kGatedBwd) {
@@ -395,96 +465,248 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_bf16_kernel(const BfArgs A) 
   }
 }
 
-#define FGG_BF16_INFO(name, entry, form) \
-  {"gemm_bf16_kernel<" name ">", entry, BM, BN, BK, kThreads, 2, kStageBytes, 0, kLdsBytes, \
-   (const void*)gemm_bf16_kernel<form>}
+#define FGG_BF16_INFO(name, entry, form, S) \
+  {"gemm_bf16_kernel<" name "," #S ">", entry, S::M, S::N, S::K, S::kThreads, S::kStages, S::kStageBytes, 0, \
+   S::kLdsBytes, (const void*)gemm_bf16_kernel<form, S>}
+#define FGG_BF16_SHAPES(name, entry, form) \
+  FGG_BF16_INFO(name, entry, form, Large), FGG_BF16_INFO(name, entry, form, Medium), \
+      FGG_BF16_INFO(name, entry, form, Small)
 const KernelInfo kInfoGemmBf16[kGemmBf16Forms] = {
-    FGG_BF16_INFO("linear", "fgg_grouped_linear", kLinear),
-    FGG_BF16_INFO("gated", "fgg_grouped_gated", kGated),
-    FGG_BF16_INFO("dx", "fgg_grouped_linear_backward_input", kDx),
-    FGG_BF16_INFO("gated_backward", "fgg_grouped_gated_backward", kGatedBwd),
-    FGG_BF16_INFO("dw", "fgg_grouped_linear_backward_weight", kDw),
+    FGG_BF16_SHAPES("linear", "fgg_grouped_linear", kLinear),
+    FGG_BF16_SHAPES("gated", "fgg_grouped_gated", kGated),
+    FGG_BF16_SHAPES("dx", "fgg_grouped_linear_backward_input", kDx),
+    FGG_BF16_SHAPES("gated_backward", "fgg_grouped_gated_backward", kGatedBwd),
+    FGG_BF16_SHAPES("dw", "fgg_grouped_linear_backward_weight", kDw),
 };
+#undef FGG_BF16_SHAPES
 #undef FGG_BF16_INFO
 
 namespace {
 
+int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
 // Tiles that can exist: with offsets a segment may begin and end anywhere, so each may have a partial tile.
-int64_t row_tiles(const int32_t* offsets, int32_t G, int64_t M) {
-  const int64_t whole = (M + BM - 1) / BM;
-  return offsets ? whole + (G < M ? G : M) : whole;
+int64_t row_tiles(const int32_t* offsets, int32_t G, int64_t M, int height) {
+  return up(M, height) + (offsets ? (G < M ? G : M) : 0);
 }
 
-template <int F>
-hipError_t launch(BfArgs a, int64_t m_tiles, int64_t tiles, hipStream_t st) {
-  if (tiles == 0) return hipSuccess;
-  a.m_tiles = (int)m_tiles;
-  a.n_tiles = (int)((a.n_cols + (F == kGated ? BN / 2 : BN) - 1) / (F == kGated ? BN / 2 : BN));
+template <int F, class S>
+int64_t tiles_of(const BfArgs& a) {
+  const int64_t across = up(a.n_cols, F == kGated ? S::N / 2 : S::N);
+  return across * (F == kDw ? a.G * up(a.m_cols, S::M) : row_tiles(a.offsets, a.G, a.M, S::M));
+}
+
+template <int F, class S>
+hipError_t launch_shape(BfArgs a, int index, hipStream_t st) {
+  a.n_tiles = (int)up(a.n_cols, F == kGated ? S::N / 2 : S::N);
+  a.m_tiles = F == kDw ? (int)up(a.m_cols, S::M) : 0;
+  const int64_t tiles = tiles_of<F, S>(a);
   // tiles of one XCD side by side; with few tiles, an eighth of them
-  a.chunk = tiles >= kXcds * kChunk ? kChunk : (int)((tiles + kXcds - 1) / kXcds);
+  a.chunk = tiles >= kXcds * kChunk ? kChunk : (int)up(tiles, kXcds);
   const int64_t round = (int64_t)kXcds * a.chunk;
-  const dim3 grid((unsigned)((tiles + round - 1) / round * round));
-  trace_launch(kInfoGemmBf16[F], grid, "G=%d M=%lld columns=%lld sum=%lld%s", a.G, (long long)a.M,
+  const dim3 grid((unsigned)(up(tiles, round) * round), (unsigned)a.splits);
+  trace_launch(kInfoGemmBf16[3 * F + index], grid, "G=%d M=%lld columns=%lld sum=%lld%s", a.G, (long long)a.M,
                (long long)a.n_cols, (long long)(F == kDw ? a.M : a.sum), a.counts ? " counts" : "");
-  hipLaunchKernelGGL(gemm_bf16_kernel<F>, grid, dim3(kThreads), 0, st, a);
+  hipLaunchKernelGGL((gemm_bf16_kernel<F, S>), grid, dim3(S::kThreads), 0, st, a);
   return hipGetLastError();
 }
 
-int64_t col_tiles(int64_t cols, int width) { return (cols + width - 1) / width; }
+// The shape whose estimated time is least.  A tile takes its stages (64 deep) one after the other; measured, in
+// microseconds a stage: 1.16 / 0.58 / 0.27 (Large / Medium / Small) where a compute unit has one workgroup, and
+// 1.57 / 0.92 / 0.37 for what it holds (1 / 2 / 2 workgroups) when the chip is full; plus 10 / 5 / 3 to begin and
+// end.  E.g. linear, one segment: 2048^3 50 / 26 / 33 us, 4096 x 2048 x 2048 53 / 36 / 55, 8192^3 803 / 943 /
+// 1520, 256 x 4096 x 4096 87 / 41 / 20.
+struct Plan {
+  int shape, splits;   // 0 Large, 1 Medium, 2 Small; parts of the sum
+};
+
+double shape_us(int shape, double tiles, double stages) {
+  constexpr double kCus = 256.0;
+  constexpr double one[3] = {1.16, 0.58, 0.27}, full[3] = {1.57, 0.92, 0.37}, ends[3] = {10.0, 5.0, 3.0};
+  const double slots = shape == 0 ? kCus : 2 * kCus;
+  const double rounds = tiles <= kCus && shape != 0 ? one[shape]
+                        : tiles <= kCus             ? one[0] + (full[0] - one[0]) * tiles / kCus
+                                                    : full[shape] * (double)(int64_t)((tiles + slots - 1) / slots);
+  return stages * rounds + ends[shape];
+}
+
+// Rows' forms: segments are taken to be alike, with half a tile of each lost at its end.
+Plan plan_rows(const Segments& s, int64_t cols, int64_t sum, bool gated) {
+  constexpr int kSide[3] = {256, 128, 64};
+  Plan best = {2, 1};
+  double least = 1e30;
+  for (int i = 0; i < 3; ++i) {
+    double down = (double)up(s.M, kSide[i]);
+    if (s.G > 1) {
+      const double live = (double)(s.G < s.M ? s.G : s.M);
+      down = (double)s.M / kSide[i] + 0.5 * live;
+      if (down < live) down = live;
+    }
+    const double us = shape_us(i, down * (double)up(cols, gated ? kSide[i] / 2 : kSide[i]), (double)up(sum, 64));
+    if (us < least) least = us, best.shape = i;
+  }
+  return best;
+}
+
+// Weights' gradient: few results with a long sum are cut into parts, whose fp32 results (written and read at
+// about 4 bytes a picosecond) a second kernel adds: 30000 rows onto 1024 x 1160, 588 us in one part.
+Plan plan_dw(int32_t G, int64_t M, int64_t N, int64_t K) {
+  constexpr int kSide[3] = {256, 128, 64};
+  Plan best = {2, 1};
+  double least = 1e30;
+  const double each = (double)up(up(M, G), 64);
+  for (int i = 0; i < 3; ++i) {
+    const double tiles = (double)G * (double)up(N, kSide[i]) * (double)up(K, kSide[i]);
+    for (int z = 1; z <= 32; ++z) {
+      const double stages = (double)(int64_t)((each + z - 1) / z);
+      if (z > 1 && (stages < 4 || tiles * z > 1024)) break;
+      const double us = shape_us(i, tiles * z, stages) + (z > 1 ? 4.0 + (double)z * G * N * K * 8 / 4e6 : 0.0);
+      if (us < least) least = us, best = {i, z};
+    }
+  }
+  return best;
+}
+
+template <int F>
+hipError_t launch(const BfArgs& a, int shape, hipStream_t st) {
+  if (shape == 0) return launch_shape<F, Large>(a, 0, st);
+  if (shape == 1) return launch_shape<F, Medium>(a, 1, st);
+  return launch_shape<F, Small>(a, 2, st);
+}
+
+// out (+)= the parts' sums, in their order; four elements a thread.
+template <bool F32, bool ADD>
+__global__ void __launch_bounds__(256) dw_join_kernel(const float4* __restrict__ part, int splits, int64_t quads,
+                                                      void* __restrict__ out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= quads) return;
+  float4 s = part[i];
+  for (int z = 1; z < splits; ++z) {
+    const float4 p = part[z * quads + i];
+    s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
+  }
+  if constexpr (F32) {
+    float4* o = (float4*)out + i;
+    if constexpr (ADD) {
+      const float4 old = *o;
+      s.x += old.x, s.y += old.y, s.z += old.z, s.w += old.w;
+    }
+    *o = s;
+  } else {
+    uint2* o = (uint2*)out + i;
+    if constexpr (ADD) {
+      const uint2 old = *o;
+      s.x += __uint_as_float(old.x << 16), s.y += __uint_as_float(old.x & 0xFFFF0000u);
+      s.z += __uint_as_float(old.y << 16), s.w += __uint_as_float(old.y & 0xFFFF0000u);
+    }
+    *o = make_uint2(bf16x2_rne(s.x, s.y), bf16x2_rne(s.z, s.w));
+  }
+}
+
+// Few rows take the few-row kernel where the smallest tiles would leave half the chip without one: they then wait
+// out one tile's whole sum (K 7168: 30 us; the few-row kernel shares it between eight waves: 12 us for one row
+// onto 4096 columns, 16 for 16 rows; onto 16384 columns, 256 tiles, 34 against 21 us).
+bool few_rows(const Segments& s, int64_t cols, bool gated) {
+  const int64_t live = s.G < s.M ? s.G : s.M;
+  return s.M <= 32 * live && live * up(cols, gated ? Small::N / 2 : Small::N) <= 128;
+}
 
 }  // namespace
 
+const KernelInfo kInfoDwJoin[4] = {
+    {"dw_join_kernel<bf16>", "fgg_grouped_linear_backward_weight", 0, 0, 0, 256, 0, 0, 0, 0,
+     (const void*)dw_join_kernel<false, false>},
+    {"dw_join_kernel<bf16,add>", "fgg_grouped_linear_backward_weight", 0, 0, 0, 256, 0, 0, 0, 0,
+     (const void*)dw_join_kernel<false, true>},
+    {"dw_join_kernel<f32>", "fgg_grouped_linear_backward_weight", 0, 0, 0, 256, 0, 0, 0, 0,
+     (const void*)dw_join_kernel<true, false>},
+    {"dw_join_kernel<f32,add>", "fgg_grouped_linear_backward_weight", 0, 0, 0, 256, 0, 0, 0, 0,
+     (const void*)dw_join_kernel<true, true>},
+};
+
 int64_t gemm_bf16_tiles(const int32_t* offsets, int32_t G, int64_t M, int64_t cols, bool gated) {
-  return row_tiles(offsets, G, M) * col_tiles(cols, gated ? BN / 2 : BN);
+  return row_tiles(offsets, G, M, Small::M) * up(cols, gated ? Small::N / 2 : Small::N);
 }
 
-int64_t gemm_bf16_dw_tiles(int32_t G, int64_t N, int64_t K) { return (int64_t)G * col_tiles(N, BM) * col_tiles(K, BN); }
+int64_t gemm_bf16_dw_tiles(int32_t G, int64_t N, int64_t K) { return (int64_t)G * up(N, Small::M) * up(K, Small::N); }
+
+size_t gemm_bf16_dw_workspace(int32_t G, int64_t M, int64_t N, int64_t K) {
+  if (M == 0 || N == 0 || K == 0) return 0;
+  const int splits = plan_dw(G, M, N, K).splits;
+  return splits > 1 ? (size_t)splits * (size_t)G * (size_t)N * (size_t)K * 4 : 0;
+}
 
 hipError_t launch_grouped_linear(const Segments& s, int64_t N, int64_t K, const uint16_t* x, int64_t ldx,
                                  const uint16_t* w, void* y, bool y_f32, int64_t ldy, hipStream_t st) {
   BfArgs a{};
+  a.splits = 1;
   a.p = x, a.ldp = ldx, a.q = w, a.ldq = K, a.q_group = N * K;
   a.offsets = s.offsets, a.counts = s.counts, a.G = s.G, a.M = s.M;
   a.n_cols = N, a.sum = K, a.out = y, a.ldo = ldy, a.out_f32 = y_f32;
-  return launch<kLinear>(a, 0, gemm_bf16_tiles(s.offsets, s.G, s.M, N, false), st);
+  if (few_rows(s, N, false))
+    return launch_rows_bf16(s, false, N, K, x, ldx, w, y, y_f32, ldy, nullptr, 0, st);
+  return launch<kLinear>(a, plan_rows(s, N, K, false).shape, st);
 }
 
 hipError_t launch_grouped_gated(const Segments& s, int64_t I, int64_t K, const uint16_t* x, int64_t ldx,
                                 const uint16_t* w, uint16_t* act, int64_t lda, uint16_t* h, int64_t ldh,
                                 hipStream_t st) {
   BfArgs a{};
+  a.splits = 1;
   a.p = x, a.ldp = ldx, a.q = w, a.ldq = K, a.q_group = 2 * I * K;
   a.offsets = s.offsets, a.counts = s.counts, a.G = s.G, a.M = s.M;
   a.n_cols = I, a.sum = K, a.out = act, a.ldo = lda, a.out2 = h, a.ldo2 = ldh;
-  return launch<kGated>(a, 0, gemm_bf16_tiles(s.offsets, s.G, s.M, I, true), st);
+  if (few_rows(s, I, true))
+    return launch_rows_bf16(s, true, I, K, x, ldx, w, act, false, lda, h, ldh, st);
+  return launch<kGated>(a, plan_rows(s, I, K, true).shape, st);
 }
 
 hipError_t launch_grouped_dx(const Segments& s, int64_t N, int64_t K, const uint16_t* dy, int64_t lddy,
                              const uint16_t* w, void* dx, bool dx_f32, int64_t lddx, hipStream_t st) {
   BfArgs a{};
+  a.splits = 1;
   a.p = dy, a.ldp = lddy, a.q = w, a.ldq = K, a.q_group = N * K;
   a.offsets = s.offsets, a.counts = s.counts, a.G = s.G, a.M = s.M;
   a.n_cols = K, a.sum = N, a.out = dx, a.ldo = lddx, a.out_f32 = dx_f32;
-  return launch<kDx>(a, 0, gemm_bf16_tiles(s.offsets, s.G, s.M, K, false), st);
+  return launch<kDx>(a, plan_rows(s, K, N, false).shape, st);
 }
 
 hipError_t launch_grouped_gated_backward(const Segments& s, int64_t I, int64_t N, const uint16_t* dy, int64_t lddy,
                                          const uint16_t* w_down, const uint16_t* h, int64_t ldh, uint16_t* dh,
                                          int64_t lddh, uint16_t* act, int64_t lda, hipStream_t st) {
   BfArgs a{};
+  a.splits = 1;
   a.p = dy, a.ldp = lddy, a.q = w_down, a.ldq = I, a.q_group = N * I;
   a.offsets = s.offsets, a.counts = s.counts, a.G = s.G, a.M = s.M;
   a.n_cols = I, a.sum = N, a.out = dh, a.ldo = lddh, a.out2 = act, a.ldo2 = lda, a.h = h, a.ldh = ldh;
-  return launch<kGatedBwd>(a, 0, gemm_bf16_tiles(s.offsets, s.G, s.M, I, false), st);
+  return launch<kGatedBwd>(a, plan_rows(s, I, N, false).shape, st);
 }
 
 hipError_t launch_grouped_dw(const Segments& s, int64_t N, int64_t K, const uint16_t* dy, int64_t lddy,
-                             const uint16_t* x, int64_t ldx, void* dw, bool dw_f32, bool accumulate, hipStream_t st) {
+                             const uint16_t* x, int64_t ldx, void* dw, bool dw_f32, bool accumulate, float* ws,
+                             hipStream_t st) {
+  const Plan p = s.M == 0 ? Plan{2, 1} : plan_dw(s.G, s.M, N, K);
   BfArgs a{};
   a.p = dy, a.ldp = lddy, a.q = x, a.ldq = ldx;
   a.offsets = s.offsets, a.counts = s.counts, a.G = s.G, a.M = s.M;
-  a.m_cols = N, a.n_cols = K, a.out = dw, a.ldo = K, a.out_f32 = dw_f32, a.accumulate = accumulate;
-  return launch<kDw>(a, col_tiles(N, BM), gemm_bf16_dw_tiles(s.G, N, K), st);
+  a.m_cols = N, a.n_cols = K, a.ldo = K, a.splits = p.splits;
+  if (p.splits == 1) {
+    a.out = dw, a.out_f32 = dw_f32, a.accumulate = accumulate;
+    return launch<kDw>(a, p.shape, st);
+  }
+  a.out = ws, a.out_f32 = 1;
+  const hipError_t e = launch<kDw>(a, p.shape, st);
+  if (e != hipSuccess) return e;
+  const int64_t quads = (int64_t)s.G * N * K / 4;
+  const dim3 grid((unsigned)up(quads, 256));
+  trace_launch(kInfoDwJoin[(dw_f32 ? 2 : 0) + (accumulate ? 1 : 0)], grid, "G=%d N=%lld K=%lld parts=%d", s.G,
+               (long long)N, (long long)K, p.splits);
+  auto join = [&](auto* kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, (const float4*)ws, p.splits, quads, dw);
+  };
+  if (dw_f32) accumulate ? join(dw_join_kernel<true, true>) : join(dw_join_kernel<true, false>);
+  else accumulate ? join(dw_join_kernel<false, true>) : join(dw_join_kernel<false, false>);
+  return hipGetLastError();
 }
 
 }  // namespace fgg
