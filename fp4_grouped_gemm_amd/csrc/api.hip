@@ -654,8 +654,9 @@ fgg_status fgg_grouped_linear(int32_t G, int64_t M, int64_t N, int64_t K, const 
   FGG_TRY(rows_operand(y, ldy, N, (int64_t)float_size(y_dtype), M > 0));
   if (fgg::gemm_bf16_tiles(offsets, G, M, N, false) > fgg::kMaxBf16Tiles) return FGG_ERR_UNSUPPORTED;
   if (M == 0) return FGG_OK;
-  FGG_TRY(device_check(nullptr));
-  return finish(fgg::launch_grouped_linear({offsets, counts, G, M}, N, K, (const uint16_t*)x, ldx, (const uint16_t*)w,
+  int num_cus = 0;
+  FGG_TRY(device_check(&num_cus));
+  return finish(fgg::launch_grouped_linear({offsets, counts, G, M, num_cus}, N, K, (const uint16_t*)x, ldx, (const uint16_t*)w,
                                            y, y_dtype == FGG_F32, ldy, (hipStream_t)stream));
 }
 
@@ -669,8 +670,9 @@ fgg_status fgg_grouped_linear_backward_input(int32_t G, int64_t M, int64_t N, in
   FGG_TRY(rows_operand(dx, lddx, K, (int64_t)float_size(dx_dtype), M > 0));
   if (fgg::gemm_bf16_tiles(offsets, G, M, K, false) > fgg::kMaxBf16Tiles) return FGG_ERR_UNSUPPORTED;
   if (M == 0) return FGG_OK;
-  FGG_TRY(device_check(nullptr));
-  return finish(fgg::launch_grouped_dx({offsets, counts, G, M}, N, K, (const uint16_t*)dy, lddy, (const uint16_t*)w, dx,
+  int num_cus = 0;
+  FGG_TRY(device_check(&num_cus));
+  return finish(fgg::launch_grouped_dx({offsets, counts, G, M, num_cus}, N, K, (const uint16_t*)dy, lddy, (const uint16_t*)w, dx,
                                        dx_dtype == FGG_F32, lddx, (hipStream_t)stream));
 }
 
@@ -692,8 +694,9 @@ fgg_status fgg_grouped_linear_backward_weight(int32_t G, int64_t M, int64_t N, i
   if (fgg::gemm_bf16_dw_tiles(G, N, K) > fgg::kMaxBf16Tiles) return FGG_ERR_UNSUPPORTED;
   const size_t need = fgg::gemm_bf16_dw_workspace(G, M, N, K);
   if (need > 0 && (!workspace || ws_bytes < need || !aligned(workspace, 16))) return FGG_ERR_INVALID_VALUE;
-  FGG_TRY(device_check(nullptr));
-  return finish(fgg::launch_grouped_dw({offsets, counts, G, M}, N, K, (const uint16_t*)dy, lddy, (const uint16_t*)x,
+  int num_cus = 0;
+  FGG_TRY(device_check(&num_cus));
+  return finish(fgg::launch_grouped_dw({offsets, counts, G, M, num_cus}, N, K, (const uint16_t*)dy, lddy, (const uint16_t*)x,
                                        ldx, dw, dw_dtype == FGG_F32, accumulate != 0, (float*)workspace,
                                        (hipStream_t)stream));
 }
@@ -708,8 +711,9 @@ fgg_status fgg_grouped_gated(int32_t G, int64_t M, int64_t I, int64_t K, const v
   if (h) FGG_TRY(rows_operand(h, ldh, 2 * I, 2, true));
   if (fgg::gemm_bf16_tiles(offsets, G, M, I, true) > fgg::kMaxBf16Tiles) return FGG_ERR_UNSUPPORTED;
   if (M == 0) return FGG_OK;
-  FGG_TRY(device_check(nullptr));
-  return finish(fgg::launch_grouped_gated({offsets, counts, G, M}, I, K, (const uint16_t*)x, ldx, (const uint16_t*)w,
+  int num_cus = 0;
+  FGG_TRY(device_check(&num_cus));
+  return finish(fgg::launch_grouped_gated({offsets, counts, G, M, num_cus}, I, K, (const uint16_t*)x, ldx, (const uint16_t*)w,
                                           (uint16_t*)a, lda, (uint16_t*)h, ldh, (hipStream_t)stream));
 }
 
@@ -725,8 +729,9 @@ fgg_status fgg_grouped_gated_backward(int32_t G, int64_t M, int64_t I, int64_t N
   if (a) FGG_TRY(rows_operand(a, lda, I, 2, true));
   if (fgg::gemm_bf16_tiles(offsets, G, M, I, false) > fgg::kMaxBf16Tiles) return FGG_ERR_UNSUPPORTED;
   if (M == 0) return FGG_OK;
-  FGG_TRY(device_check(nullptr));
-  return finish(fgg::launch_grouped_gated_backward({offsets, counts, G, M}, I, N, (const uint16_t*)dy, lddy,
+  int num_cus = 0;
+  FGG_TRY(device_check(&num_cus));
+  return finish(fgg::launch_grouped_gated_backward({offsets, counts, G, M, num_cus}, I, N, (const uint16_t*)dy, lddy,
                                                    (const uint16_t*)w_down, (const uint16_t*)h, ldh, (uint16_t*)dh,
                                                    lddh, (uint16_t*)a, lda, (hipStream_t)stream));
 }

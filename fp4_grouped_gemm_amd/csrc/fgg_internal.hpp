@@ -159,6 +159,7 @@ struct Segments {
   const int32_t *offsets, *counts;
   int32_t G;
   int64_t M;
+  int num_cus;
 };
 // Workgroups of a launch at most (the rows' forms; the weights' gradient).
 int64_t gemm_bf16_tiles(const int32_t* offsets, int32_t G, int64_t M, int64_t cols, bool gated);

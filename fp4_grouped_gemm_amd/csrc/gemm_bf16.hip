@@ -47,6 +47,7 @@ template <int M_, int N_, int WM_, int WN_, int K_, int STAGES_>
 struct Shape {
   static constexpr int M = M_, N = N_, WM = WM_, WN = WN_, K = K_, kStages = STAGES_;
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  static constexpr bool kPersistent = kWaves == 8;
   static constexpr int FI = M / WM / 16, FJ = N / WN / 16;     // a wave's 16 x 16 accumulators
   static constexpr int kPBytes = M * K * 2, kQBytes = N * K * 2;
   static constexpr int kQOff = kStages * kPBytes;              // LDS: P stages, then Q stages
@@ -69,6 +70,13 @@ enum Form { kLinear, kGated, kDx, kGatedBwd, kDw };
 constexpr bool p_is_col(int f) { return f == kDw; }
 constexpr bool q_is_col(int f) { return f == kDx || f == kGatedBwd || f == kDw; }
 
+// The value of x, hidden from the optimizer: what is derived from it in a tile's beginning or end is computed
+// there instead of being held (or spilled) across the K loop.
+__device__ inline int opaque(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // 16 bytes per lane from base + voff into LDS at lds + 16 * lane; zeros where voff is kOutside.
 __device__ inline void buf_dma16(const void* base, uint32_t voff, uint32_t lds) {
   const uint64_t b = (uint64_t)(uintptr_t)base;
@@ -81,7 +89,7 @@ __device__ inline void buf_dma16(const void* base, uint32_t voff, uint32_t lds) 
       "buffer_load_dwordx4 %1, %2, 0 offen lds\n\t"
       "s_mov_b32 m0, %0"
       : "=&s"(save)
-      : "v"(voff), "s"(rs), "s"(lds)
+      : "v"(voff), "s"(rs), "s"(__builtin_amdgcn_readfirstlane(lds))
       : "memory");
 }
 
@@ -107,7 +115,7 @@ __device__ inline v8bf tr_read(const uint8_t* p) {
 // (see launch_* below for what each form passes)
 struct BfArgs {
   const uint16_t *p, *q;
-  int64_t ldp, ldq, q_group;           // row strides; elements of one segment's weights
+  int64_t ldp, ldq, q_rows;            // row strides; rows of one segment's weights
   const int32_t *offsets, *counts;
   int G;
   int64_t M, m_cols, n_cols, sum;      // rows; output rows (kDw) and columns; length of the sum (not kDw)
@@ -120,7 +128,8 @@ struct BfArgs {
   int64_t ldh;
   int out_f32, accumulate;
   int chunk;                           // consecutive tiles of one XCD
-  int splits;                          // kDw: parts of the sum (gridDim.y), each with its own fp32 result
+  int num_cus;
+  int splits;                          // kDw: parts of the sum, each with its own fp32 result
 };
 
 template <int F, class S>
@@ -132,112 +141,132 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_bf16_kernel(const BfArgs 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / S::WN, wn = wave % S::WN;
   const int l16 = lane & 15, q = lane >> 4;
+  const auto same = [](int v) { return __builtin_amdgcn_readfirstlane(v); };   // (equal in every lane: kept in a scalar)
+  const auto same64 = [&](int64_t v) { return (int64_t)same((int)(v >> 32)) << 32 | (uint32_t)same((int)v); };
 
-  // the tile of this workgroup
-  const int b = blockIdx.x;
-  const int turn = b / kXcds;
-  const int t = (turn / A.chunk * kXcds + b % kXcds) * A.chunk + turn % A.chunk;
-  int g = 0, j = t, mtg = A.m_tiles;
-  Segment seg;
-  if constexpr (F == kDw) {
-    g = t / (A.m_tiles * A.n_tiles);
-    if (g >= A.G) return;
-    j = t - g * (A.m_tiles * A.n_tiles);
-    seg = A.offsets ? segment_of(A.offsets, A.counts, g, A.M) : Segment{0, (int)A.M};
-  } else if (A.offsets == nullptr) {
-    seg = {0, (int)A.M};
-    mtg = (int)((A.M + BM - 1) / BM);
-    if (t >= mtg * A.n_tiles) return;
-  } else {
-    int before = 0;
-    bool found = false;
-    for (int g0 = 0; g0 < A.G; g0 += 64) {
-      Segment mine = {0, 0};
-      if (g0 + lane < A.G) mine = segment_of(A.offsets, A.counts, g0 + lane, A.M);
-      const int tiles = (mine.rows + BM - 1) / BM * A.n_tiles;
-      int upto = tiles;
-      for (int d = 1; d < 64; d <<= 1) {
-        const int v = __shfl_up(upto, d);
-        if (lane >= d) upto += v;
-      }
-      const uint64_t hit = __ballot(before + upto > t);
-      if (hit) {
-        const int at = __builtin_ctzll(hit);
-        g = g0 + at;
-        j = t - (before + __builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(tiles, at));
-        seg.first = __builtin_amdgcn_readlane((int)mine.first, at);
-        seg.rows = __builtin_amdgcn_readlane(mine.rows, at);
-        found = true;
-        break;
-      }
-      before += __builtin_amdgcn_readlane(upto, 63);
-    }
-    if (!found) return;
-    mtg = (seg.rows + BM - 1) / BM;
-  }
-  const int mb = j / (kSM * A.n_tiles), k_in = j - mb * kSM * A.n_tiles;
-  const int high = mtg - mb * kSM < kSM ? mtg - mb * kSM : kSM;
-  const int m0 = (mb * kSM + k_in % high) * BM, nt = k_in / high;
-  const int n0 = nt * (F == kGated ? BN / 2 : BN);
-  // output rows and columns from here on, and the length of the sum
-  const int m_here = F == kDw ? (int)A.m_cols - m0 : seg.rows - m0;
-  const int n_here = (int)A.n_cols - n0;
-  int sum = F == kDw ? seg.rows : (int)A.sum;
-  int first = 0;                       // kDw: this part's first row of the segment
-  if constexpr (F == kDw) {
-    if (A.splits > 1) {
-      const int per = ((sum + BK - 1) / BK + A.splits - 1) / A.splits * BK;
-      first = (int64_t)per * blockIdx.y < sum ? per * (int)blockIdx.y : sum;
-      sum = sum - first < per ? sum - first : per;
-    }
-  }
-  const int nk = (sum + BK - 1) / BK;
-
-  const uint16_t* P = A.p + (seg.first + first) * A.ldp + (F == kDw ? (int64_t)m0 : (int64_t)m0 * A.ldp);
-  const uint16_t* Q;
-  if constexpr (F == kDw) Q = A.q + (seg.first + first) * A.ldq + n0;
-  else if constexpr (q_is_col(F)) Q = A.q + (int64_t)g * A.q_group + n0;
-  else Q = A.q + (int64_t)g * A.q_group + (int64_t)n0 * A.ldq;
-
-  // what this wave loads: 1 KB pieces of both tiles; byte offsets from P and Q, kOutside past an edge
-  uint32_t voff_p[S::kPDma], voff_q[S::kQDma];
-  // "row": a piece is 1 KB of rows of BK elements; this lane's row in it and its chunk's place in memory
-  const int r_row = lane / (BK / 8), r_chunk = (lane % (BK / 8)) ^ row_key<BK>(r_row);
-  // "col": a piece is 1 KB of rows of W outputs; this lane's row in it and its first output
-  auto c_row = [&](int W, int piece) { return piece * (512 / W) + lane / (W / 8); };
-  auto c_col = [&](auto w_tag, int piece) {
-    constexpr int W = decltype(w_tag)::value;
-    const int in = lane % (W / 8);
-    return ((in >> 1) ^ col_key<W>(c_row(W, piece))) * 16 + (in & 1) * 8;
+  // Tile t of the launch (in the order of kChunk-blocks, see launch_shape): where it lies, and how long its sum is.
+  struct Tile {
+    int64_t p_row, q_row, out_row;     // first row of P and Q (of the sum, for "col" operands), of the output
+    int m0, n0, m_here, n_here, sum;   // first output row and column in the segment's result; what is left from there
   };
-#pragma unroll
-  for (int i = 0; i < S::kPDma; ++i) {
-    const int piece = wave * S::kPDma + i;
-    if constexpr (p_is_col(F)) {
-      const int c = c_col(std::integral_constant<int, BM>{}, piece);
-      voff_p[i] = c < m_here ? (uint32_t)c_row(BM, piece) * (uint32_t)(A.ldp * 2) + c * 2 : kOutside;
+  auto find = [&](int t, Tile& tile) -> bool {
+    const int lane = opaque(threadIdx.x & 63);
+    int g = 0, j = t, z = 0, mtg = A.m_tiles;
+    Segment seg;
+    if constexpr (F == kDw) {
+      const int each = A.m_tiles * A.n_tiles;
+      z = t / (A.G * each);
+      if (z >= A.splits) return false;
+      j = t - z * (A.G * each);
+      g = j / each;
+      j -= g * each;
+      seg = A.offsets ? segment_of(A.offsets, A.counts, g, A.M) : Segment{0, (int)A.M};
+    } else if (A.offsets == nullptr) {
+      seg = {0, (int)A.M};
+      mtg = (int)((A.M + BM - 1) / BM);
+      if (t >= mtg * A.n_tiles) return false;
     } else {
-      const int row = piece * (512 / BK) + r_row;
-      voff_p[i] = row < m_here ? (uint32_t)row * (uint32_t)(A.ldp * 2) + r_chunk * 16 : kOutside;
+      int before = 0;
+      bool found = false;
+      for (int g0 = 0; g0 < A.G; g0 += 64) {
+        Segment mine = {0, 0};
+        if (g0 + lane < A.G) mine = segment_of(A.offsets, A.counts, g0 + lane, A.M);
+        const int tiles = (mine.rows + BM - 1) / BM * A.n_tiles;
+        int upto = tiles;
+        for (int d = 1; d < 64; d <<= 1) {
+          const int v = __shfl_up(upto, d);
+          if (lane >= d) upto += v;
+        }
+        const uint64_t hit = __ballot(before + upto > t);
+        if (hit) {
+          const int at = __builtin_ctzll(hit);
+          g = g0 + at;
+          j = t - (before + __builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(tiles, at));
+          seg.first = __builtin_amdgcn_readlane((int)mine.first, at);
+          seg.rows = __builtin_amdgcn_readlane(mine.rows, at);
+          found = true;
+          break;
+        }
+        before += __builtin_amdgcn_readlane(upto, 63);
+      }
+      if (!found) return false;
+      mtg = (seg.rows + BM - 1) / BM;
     }
-  }
-#pragma unroll
-  for (int i = 0; i < S::kQDma; ++i) {
-    const int piece = wave * S::kQDma + i;
-    if constexpr (q_is_col(F)) {
-      const int c = c_col(std::integral_constant<int, BN>{}, piece);
-      voff_q[i] = c < n_here ? (uint32_t)c_row(BN, piece) * (uint32_t)(A.ldq * 2) + c * 2 : kOutside;
+    const int mb = j / (kSM * A.n_tiles), k_in = j - mb * kSM * A.n_tiles;
+    const int high = mtg - mb * kSM < kSM ? mtg - mb * kSM : kSM;
+    const int nt = k_in / high;
+    tile.m0 = (mb * kSM + k_in - nt * high) * BM;
+    tile.n0 = nt * (F == kGated ? BN / 2 : BN);
+    tile.n_here = (int)A.n_cols - tile.n0;
+    if constexpr (F == kDw) {
+      // part z of the sum over the segment's rows
+      const int per = ((seg.rows + BK - 1) / BK + A.splits - 1) / A.splits * BK;
+      const int first = (int64_t)per * z < seg.rows ? per * z : seg.rows;
+      tile.sum = seg.rows - first < per ? seg.rows - first : per;
+      tile.m_here = (int)A.m_cols - tile.m0;
+      tile.p_row = tile.q_row = seg.first + first;
+      tile.out_row = ((int64_t)z * A.G + g) * A.m_cols + tile.m0;
     } else {
-      int row = piece * (512 / BK) + r_row;
-      if (F == kGated) row &= BN / 2 - 1;  // tile rows: gate columns, then the up columns of the same index
-      voff_q[i] = row < n_here ? (uint32_t)row * (uint32_t)(A.ldq * 2) + r_chunk * 16 : kOutside;
+      tile.sum = (int)A.sum;
+      tile.m_here = seg.rows - tile.m0;
+      tile.p_row = tile.out_row = seg.first + tile.m0;
+      tile.q_row = (int64_t)g * A.q_rows + (q_is_col(F) ? 0 : tile.n0);
     }
-  }
-  // (gated: the second half of the waves loads the up rows, n_cols rows further)
-  const uint16_t* Qw = F == kGated && wave >= S::kWaves / 2 ? Q + A.n_cols * A.ldq : Q;
+    tile = {same64(tile.p_row), same64(tile.q_row), same64(tile.out_row), same(tile.m0),
+            same(tile.n0),      same(tile.m_here),  same(tile.n_here),    same(tile.sum)};
+    return true;
+  };
+
+  // What this wave loads: 1 KB pieces of both tiles; byte offsets from P and Q, kOutside past an edge.
+  // "row": a piece is 1 KB of rows of BK elements; this lane's row in it and its chunk's place in memory
+  const int r_chunk = (lane % (BK / 8)) ^ row_key<BK>(lane / (BK / 8));
+  // "col": a piece is 1 KB of rows of W outputs; this lane's row in it (and, in begin, its first output)
+  auto c_row = [&](int W, int piece) { return piece * (512 / W) + lane / (W / 8); };
+  uint32_t voff_p[S::kPDma], voff_q[S::kQDma];
+  const uint16_t *P, *Q;
+  int sum, nk;
+  auto begin = [&](const Tile& t) {
+    const int lane = opaque(threadIdx.x & 63);
+    const int r_row = lane / (BK / 8), r_chunk = (lane % (BK / 8)) ^ row_key<BK>(r_row);
+    auto c_row = [&](int W, int piece) { return piece * (512 / W) + lane / (W / 8); };
+    auto c_col = [&](auto w_tag, int piece) {
+      constexpr int W = decltype(w_tag)::value;
+      const int in = lane % (W / 8);
+      return ((in >> 1) ^ col_key<W>(c_row(W, piece))) * 16 + (in & 1) * 8;
+    };
+    sum = t.sum;
+    nk = (sum + BK - 1) / BK;
+    P = A.p + t.p_row * A.ldp + (p_is_col(F) ? t.m0 : 0);
+    Q = A.q + t.q_row * A.ldq + (q_is_col(F) ? t.n0 : 0);
+    // (gated: the second half of the waves loads the up rows, n_cols rows further)
+    if (F == kGated && wave >= S::kWaves / 2) Q += A.n_cols * A.ldq;
+#pragma unroll
+    for (int i = 0; i < S::kPDma; ++i) {
+      const int piece = wave * S::kPDma + i;
+      if constexpr (p_is_col(F)) {
+        const int c = c_col(std::integral_constant<int, BM>{}, piece);
+        voff_p[i] = c < t.m_here ? (uint32_t)c_row(BM, piece) * (uint32_t)(A.ldp * 2) + c * 2 : kOutside;
+      } else {
+        const int row = piece * (512 / BK) + r_row;
+        voff_p[i] = row < t.m_here ? (uint32_t)row * (uint32_t)(A.ldp * 2) + r_chunk * 16 : kOutside;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < S::kQDma; ++i) {
+      const int piece = wave * S::kQDma + i;
+      if constexpr (q_is_col(F)) {
+        const int c = c_col(std::integral_constant<int, BN>{}, piece);
+        voff_q[i] = c < t.n_here ? (uint32_t)c_row(BN, piece) * (uint32_t)(A.ldq * 2) + c * 2 : kOutside;
+      } else {
+        int row = piece * (512 / BK) + r_row;
+        if (F == kGated) row &= BN / 2 - 1;  // tile rows: gate columns, then the up columns of the same index
+        voff_q[i] = row < t.n_here ? (uint32_t)row * (uint32_t)(A.ldq * 2) + r_chunk * 16 : kOutside;
+      }
+    }
+  };
   auto issue = [&](int kb, int stage) {
     const uint16_t* p = P + (p_is_col(F) ? (int64_t)kb * BK * A.ldp : (int64_t)kb * BK);
-    const uint16_t* qq = Qw + (q_is_col(F) ? (int64_t)kb * BK * A.ldq : (int64_t)kb * BK);
+    const uint16_t* qq = Q + (q_is_col(F) ? (int64_t)kb * BK * A.ldq : (int64_t)kb * BK);
     const int rest = sum - kb * BK;
 #pragma unroll
     for (int i = 0; i < S::kPDma; ++i) {
@@ -254,6 +283,24 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_bf16_kernel(const BfArgs 
       buf_dma16(qq, v, lds_base + S::kQOff + stage * S::kQBytes + piece * 1024);
     }
   };
+  constexpr int kFirst = FJ == 4 ? S::kStages : S::kStages - 1;   // stages under way when a tile begins
+  auto start = [&]() {
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i)
+      if (i < nk) issue(i, i);
+  };
+
+  // The tiles of this workgroup.  Large: one workgroup per compute unit takes tile after tile, and the next
+  // tile's first stages are loaded while the epilogue of the last one writes.  The others: one tile each.
+  const int b = blockIdx.x;
+  auto tile_at = [&](int round) {
+    const int turn = b / kXcds + round * (int)(gridDim.x / kXcds);
+    return (turn / A.chunk * kXcds + b % kXcds) * A.chunk + turn % A.chunk;
+  };
+  Tile cur;
+  if (!find(tile_at(0), cur)) return;
+  begin(cur);
+  start();
 
   // this lane's operand reads: "row": chunk 4 s + q of row l16 (+ 16 per fragment); "col": rows
   // 8 q + (l16 >> 2) (+ 4 for the second half), the fragment's 32-byte unit
@@ -283,6 +330,9 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_bf16_kernel(const BfArgs 
     }
   };
 
+  for (int round = 1;; ++round) {
+  Tile next;
+  const bool more = S::kPersistent && same((int)find(tile_at(round), next)) != 0;
   v4f acc[FI][FJ];
 #pragma unroll
   for (int i = 0; i < FI; ++i)
@@ -345,13 +395,11 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_bf16_kernel(const BfArgs 
       }
     };
     if (nk > 0) {
-#pragma unroll
-      for (int i = 0; i < S::kStages; ++i)
-        if (i < nk) issue(i, i);
-      if (nk >= S::kStages) wait_vmcnt<kAhead * (S::kPDma + S::kQDma)>();
+      // (after the first tile the last one's stores are under way too, in no order with the loads)
+      if (nk >= S::kStages && round == 1) wait_vmcnt<kAhead * (S::kPDma + S::kQDma)>();
       else wait_vmcnt<0>();
       block_barrier();
-      if (FI == 8 && m_here <= BM / 2) run(std::integral_constant<int, 4>{});
+      if (FI == 8 && cur.m_here <= BM / 2) run(std::integral_constant<int, 4>{});
       else run(std::integral_constant<int, FI>{});
     }
   } else {
@@ -373,9 +421,6 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_bf16_kernel(const BfArgs 
             acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[n], fp[i], acc[i][n], 0, 0, 0);
       }
     };
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (i < nk) issue(i, i);
     for (int kb = 0; kb < nk; kb += S::kStages) {
 #pragma unroll
       for (int st = 0; st < S::kStages; ++st) {
@@ -390,78 +435,107 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_bf16_kernel(const BfArgs 
     }
   }
 
-  // outputs: lane holds columns 4 q + (0..3) of each fragment for row l16
+  // (the last stage's barrier has passed: every buffer is free)
+  if (more) {
+    begin(next);
+    start();
+  }
+
+  // Outputs.  A lane holds columns 4 q + (0..3) of each fragment for row l16; two neighbouring fragments are
+  // exchanged between lanes 16 apart, so that it holds eight consecutive ones (V) of one of them.
+  constexpr int kAcross = F == kGated ? FJ / 2 : FJ, V = kAcross % 2 == 0 ? 8 : 4;
+  const int lane_e = opaque(lane), l16_e = lane_e & 15, q_e = lane_e >> 4;
+  const int c_lane = V == 8 ? 16 * (q_e & 1) + 8 * (q_e >> 1) : 4 * q_e;
+  auto gather = [&](int i, int n, float* v) {
 #pragma unroll
-  for (int i = 0; i < FI; ++i) {
-    const int r = 16 * (S::WM * i + wm) + l16;
-    if (r >= m_here) continue;
-    const int64_t row = (F == kDw ? ((int64_t)blockIdx.y * A.G + g) * A.m_cols : seg.first) + m0 + r;
-    if constexpr (F == kGated) {
-#pragma unroll
-      for (int n = 0; n < FJ / 2; ++n) {
-        const int c = 16 * (FJ / 2) * wn + 16 * n + 4 * q;
-        if (c >= n_here) continue;
-        float a[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float gate = acc[i][n][e];
-          a[e] = gate * sigmoid(gate) * acc[i][n + FJ / 2][e];
-        }
-        *reinterpret_cast<uint2*>((uint16_t*)A.out + row * A.ldo + n0 + c) =
-            make_uint2(bf16x2_rne(a[0], a[1]), bf16x2_rne(a[2], a[3]));
-        if (A.out2) {
-          uint16_t* hrow = A.out2 + row * A.ldo2 + n0 + c;
-          const v4f u = acc[i][n], v = acc[i][n + FJ / 2];
-          *reinterpret_cast<uint2*>(hrow) = make_uint2(bf16x2_rne(u[0], u[1]), bf16x2_rne(u[2], u[3]));
-          *reinterpret_cast<uint2*>(hrow + A.n_cols) = make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
-        }
-      }
-    } else {
-#pragma unroll
-      for (int n = 0; n < FJ; ++n) {
-        const int c = 16 * FJ * wn + 16 * n + 4 * q;
-        if (c >= n_here) continue;
-        v4f v = acc[i][n];
-        if constexpr (F == kGatedBwd) {
-          const uint16_t* hrow = A.h + row * A.ldh + n0 + c;
-          const uint2 gw = *reinterpret_cast<const uint2*>(hrow);
-          const uint2 uw = *reinterpret_cast<const uint2*>(hrow + A.n_cols);
-          const uint32_t gs[2] = {gw.x, gw.y}, us[2] = {uw.x, uw.y};
-          float dg[4], du[4], a[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float gate = __uint_as_float((e & 1) ? gs[e >> 1] & 0xFFFF0000u : gs[e >> 1] << 16);
-            const float up = __uint_as_float((e & 1) ? us[e >> 1] & 0xFFFF0000u : us[e >> 1] << 16);
-            const float s = sigmoid(gate);
-            const float silu = gate * s;
-            dg[e] = v[e] * up * fmaf(silu, 1.0f - s, s);
-            du[e] = v[e] * silu;
-            a[e] = silu * up;
-          }
-          uint16_t* drow = (uint16_t*)A.out + row * A.ldo + n0 + c;
-          *reinterpret_cast<uint2*>(drow) = make_uint2(bf16x2_rne(dg[0], dg[1]), bf16x2_rne(dg[2], dg[3]));
-          *reinterpret_cast<uint2*>(drow + A.n_cols) = make_uint2(bf16x2_rne(du[0], du[1]), bf16x2_rne(du[2], du[3]));
-          if (A.out2)
-            *reinterpret_cast<uint2*>(A.out2 + row * A.ldo2 + n0 + c) =
-                make_uint2(bf16x2_rne(a[0], a[1]), bf16x2_rne(a[2], a[3]));
-        } else if (A.out_f32) {
-          float4* o = reinterpret_cast<float4*>((float*)A.out + row * A.ldo + n0 + c);
-          if (F == kDw && A.accumulate) {
-            const float4 old = *o;
-            v[0] += old.x, v[1] += old.y, v[2] += old.z, v[3] += old.w;
-          }
-          *o = make_float4(v[0], v[1], v[2], v[3]);
-        } else {
-          uint2* o = reinterpret_cast<uint2*>((uint16_t*)A.out + row * A.ldo + n0 + c);
-          if (F == kDw && A.accumulate) {
-            const uint2 old = *o;
-            v[0] += __uint_as_float(old.x << 16), v[1] += __uint_as_float(old.x & 0xFFFF0000u);
-            v[2] += __uint_as_float(old.y << 16), v[3] += __uint_as_float(old.y & 0xFFFF0000u);
-          }
-          *o = make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
-        }
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (V == 8) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i][n][e]), __float_as_uint(acc[i][n + 1][e]),
+                                                        false, false);
+        v[e] = __uint_as_float(r[0]), v[4 + e] = __uint_as_float(r[1]);
+      } else {
+        v[e] = acc[i][n][e];
       }
     }
+  };
+  auto put = [&](void* base, int64_t at, const float* v) {      // V values in bf16
+    uint32_t w[V / 2];
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) w[e] = bf16x2_rne(v[2 * e], v[2 * e + 1]);
+    __builtin_memcpy(__builtin_assume_aligned((uint16_t*)base + at, 2 * V), w, 2 * V);
+  };
+  auto get = [&](const void* base, int64_t at, float* v) {
+    uint32_t w[V / 2];
+    __builtin_memcpy(w, __builtin_assume_aligned((const uint16_t*)base + at, 2 * V), 2 * V);
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
+  };
+#pragma unroll
+  for (int i = 0; i < FI; ++i) {
+    const int r = 16 * (S::WM * i + wm) + l16_e;
+    const int64_t row = cur.out_row + r;
+#pragma unroll
+    for (int n = 0; n < kAcross; n += V / 4) {
+      if (F != kGated && F != kGatedBwd && A.out_f32) {
+        // four fp32 values are a lane's 16 bytes already
+#pragma unroll
+        for (int k = 0; k < V / 4; ++k) {
+          const int c = 16 * (kAcross * wn + n + k) + 4 * q_e;
+          if (r >= cur.m_here || c >= cur.n_here) continue;
+          float4* o = reinterpret_cast<float4*>((float*)A.out + row * A.ldo + cur.n0 + c);
+          const v4f a = acc[i][n + k];
+          float4 w = make_float4(a[0], a[1], a[2], a[3]);
+          if (F == kDw && A.accumulate) {
+            const float4 old = *o;
+            w.x += old.x, w.y += old.y, w.z += old.z, w.w += old.w;
+          }
+          *o = w;
+        }
+        continue;
+      }
+      const int c = 16 * (kAcross * wn + n) + c_lane;
+      float v[V];
+      gather(i, n, v);                 // (every lane takes part)
+      float u[V];
+      if constexpr (F == kGated) gather(i, n + FJ / 2, u);
+      if (r >= cur.m_here || c >= cur.n_here) continue;
+      const int64_t at = row * A.ldo + cur.n0 + c;
+      if constexpr (F == kGated) {
+        if (A.out2) {
+          put(A.out2, row * A.ldo2 + cur.n0 + c, v);
+          put(A.out2, row * A.ldo2 + cur.n0 + c + A.n_cols, u);
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = v[e] * sigmoid(v[e]) * u[e];
+        put(A.out, at, v);
+      } else if constexpr (F == kGatedBwd) {
+        float gate[V], up[V], dg[V];
+        get(A.h, row * A.ldh + cur.n0 + c, gate);
+        get(A.h, row * A.ldh + cur.n0 + c + A.n_cols, up);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float s = sigmoid(gate[e]), silu = gate[e] * s;
+          dg[e] = v[e] * up[e] * fmaf(silu, 1.0f - s, s);
+          v[e] *= silu;
+          up[e] *= silu;
+        }
+        put(A.out, at, dg);
+        put(A.out, at + A.n_cols, v);
+        if (A.out2) put(A.out2, row * A.ldo2 + cur.n0 + c, up);
+      } else {
+        if (F == kDw && A.accumulate) {
+          float old[V];
+          get(A.out, at, old);
+#pragma unroll
+          for (int e = 0; e < V; ++e) v[e] += old[e];
+        }
+        put(A.out, at, v);
+      }
+    }
+  }
+
+  if (!more) break;
+  cur = next;
   }
 }
 
@@ -500,11 +574,12 @@ template <int F, class S>
 hipError_t launch_shape(BfArgs a, int index, hipStream_t st) {
   a.n_tiles = (int)up(a.n_cols, F == kGated ? S::N / 2 : S::N);
   a.m_tiles = F == kDw ? (int)up(a.m_cols, S::M) : 0;
-  const int64_t tiles = tiles_of<F, S>(a);
-  // tiles of one XCD side by side; with few tiles, an eighth of them
-  a.chunk = tiles >= kXcds * kChunk ? kChunk : (int)up(tiles, kXcds);
+  const int64_t tiles = tiles_of<F, S>(a) * a.splits;
+  // tiles of one XCD side by side; with few tiles, an eighth of them.  Large: a workgroup per compute unit.
+  const int64_t most = S::kPersistent && a.num_cus / kXcds < kChunk ? (a.num_cus < kXcds ? 1 : a.num_cus / kXcds) : kChunk;
+  a.chunk = (int)(tiles >= kXcds * most ? most : up(tiles, kXcds));
   const int64_t round = (int64_t)kXcds * a.chunk;
-  const dim3 grid((unsigned)(up(tiles, round) * round), (unsigned)a.splits);
+  const dim3 grid((unsigned)(S::kPersistent ? round : up(tiles, round) * round));
   trace_launch(kInfoGemmBf16[3 * F + index], grid, "G=%d M=%lld columns=%lld sum=%lld%s", a.G, (long long)a.M,
                (long long)a.n_cols, (long long)(F == kDw ? a.M : a.sum), a.counts ? " counts" : "");
   hipLaunchKernelGGL((gemm_bf16_kernel<F, S>), grid, dim3(S::kThreads), 0, st, a);
@@ -520,14 +595,17 @@ struct Plan {
   int shape, splits;   // 0 Large, 1 Medium, 2 Small; parts of the sum
 };
 
-double shape_us(int shape, double tiles, double stages) {
+double shape_us(int shape, double tiles, double stages, bool alike) {
   constexpr double kCus = 256.0;
-  constexpr double one[3] = {1.16, 0.58, 0.27}, full[3] = {1.57, 0.92, 0.37}, ends[3] = {10.0, 5.0, 3.0};
+  constexpr double one[3] = {1.16, 0.58, 0.27}, full[3] = {1.5, 0.95, 0.36}, ends[3] = {10.0, 4.0, 2.0};
+  constexpr double ragged[3] = {0.5, 0.9, 0.9};        // of a round, lost to uneven segments
   const double slots = shape == 0 ? kCus : 2 * kCus;
-  const double rounds = tiles <= kCus && shape != 0 ? one[shape]
-                        : tiles <= kCus             ? one[0] + (full[0] - one[0]) * tiles / kCus
-                                                    : full[shape] * (double)(int64_t)((tiles + slots - 1) / slots);
-  return stages * rounds + ends[shape];
+  if (tiles <= kCus)
+    return stages * (one[shape] + (shape == 0 ? (full[0] - one[0]) * tiles / kCus : 0.0)) + ends[shape] + 1.0;
+  double rounds = tiles / slots;
+  rounds = alike ? (double)(int64_t)(rounds + 0.999) : rounds + ragged[shape];
+  if (rounds < 1.0) rounds = 1.0;
+  return rounds * (stages * full[shape] + ends[shape]);
 }
 
 // Rows' forms: segments are taken to be alike, with half a tile of each lost at its end.
@@ -542,7 +620,8 @@ Plan plan_rows(const Segments& s, int64_t cols, int64_t sum, bool gated) {
       down = (double)s.M / kSide[i] + 0.5 * live;
       if (down < live) down = live;
     }
-    const double us = shape_us(i, down * (double)up(cols, gated ? kSide[i] / 2 : kSide[i]), (double)up(sum, 64));
+    const double us = shape_us(i, down * (double)up(cols, gated ? kSide[i] / 2 : kSide[i]), (double)up(sum, 64),
+                               s.G == 1);
     if (us < least) least = us, best.shape = i;
   }
   return best;
@@ -560,7 +639,7 @@ Plan plan_dw(int32_t G, int64_t M, int64_t N, int64_t K) {
     for (int z = 1; z <= 32; ++z) {
       const double stages = (double)(int64_t)((each + z - 1) / z);
       if (z > 1 && (stages < 4 || tiles * z > 1024)) break;
-      const double us = shape_us(i, tiles * z, stages) + (z > 1 ? 4.0 + (double)z * G * N * K * 8 / 4e6 : 0.0);
+      const double us = shape_us(i, tiles * z, stages, true) + (z > 1 ? 4.0 + (double)z * G * N * K * 8 / 4e6 : 0.0);
       if (us < least) least = us, best = {i, z};
     }
   }
@@ -640,8 +719,8 @@ hipError_t launch_grouped_linear(const Segments& s, int64_t N, int64_t K, const 
                                  const uint16_t* w, void* y, bool y_f32, int64_t ldy, hipStream_t st) {
   BfArgs a{};
   a.splits = 1;
-  a.p = x, a.ldp = ldx, a.q = w, a.ldq = K, a.q_group = N * K;
-  a.offsets = s.offsets, a.counts = s.counts, a.G = s.G, a.M = s.M;
+  a.p = x, a.ldp = ldx, a.q = w, a.ldq = K, a.q_rows = N;
+  a.offsets = s.offsets, a.counts = s.counts, a.G = s.G, a.M = s.M, a.num_cus = s.num_cus;
   a.n_cols = N, a.sum = K, a.out = y, a.ldo = ldy, a.out_f32 = y_f32;
   if (few_rows(s, N, false))
     return launch_rows_bf16(s, false, N, K, x, ldx, w, y, y_f32, ldy, nullptr, 0, st);
@@ -653,8 +732,8 @@ hipError_t launch_grouped_gated(const Segments& s, int64_t I, int64_t K, const u
                                 hipStream_t st) {
   BfArgs a{};
   a.splits = 1;
-  a.p = x, a.ldp = ldx, a.q = w, a.ldq = K, a.q_group = 2 * I * K;
-  a.offsets = s.offsets, a.counts = s.counts, a.G = s.G, a.M = s.M;
+  a.p = x, a.ldp = ldx, a.q = w, a.ldq = K, a.q_rows = 2 * I;
+  a.offsets = s.offsets, a.counts = s.counts, a.G = s.G, a.M = s.M, a.num_cus = s.num_cus;
   a.n_cols = I, a.sum = K, a.out = act, a.ldo = lda, a.out2 = h, a.ldo2 = ldh;
   if (few_rows(s, I, true))
     return launch_rows_bf16(s, true, I, K, x, ldx, w, act, false, lda, h, ldh, st);
@@ -665,8 +744,8 @@ hipError_t launch_grouped_dx(const Segments& s, int64_t N, int64_t K, const uint
                              const uint16_t* w, void* dx, bool dx_f32, int64_t lddx, hipStream_t st) {
   BfArgs a{};
   a.splits = 1;
-  a.p = dy, a.ldp = lddy, a.q = w, a.ldq = K, a.q_group = N * K;
-  a.offsets = s.offsets, a.counts = s.counts, a.G = s.G, a.M = s.M;
+  a.p = dy, a.ldp = lddy, a.q = w, a.ldq = K, a.q_rows = N;
+  a.offsets = s.offsets, a.counts = s.counts, a.G = s.G, a.M = s.M, a.num_cus = s.num_cus;
   a.n_cols = K, a.sum = N, a.out = dx, a.ldo = lddx, a.out_f32 = dx_f32;
   return launch<kDx>(a, plan_rows(s, K, N, false).shape, st);
 }
@@ -676,8 +755,8 @@ hipError_t launch_grouped_gated_backward(const Segments& s, int64_t I, int64_t N
                                          int64_t lddh, uint16_t* act, int64_t lda, hipStream_t st) {
   BfArgs a{};
   a.splits = 1;
-  a.p = dy, a.ldp = lddy, a.q = w_down, a.ldq = I, a.q_group = N * I;
-  a.offsets = s.offsets, a.counts = s.counts, a.G = s.G, a.M = s.M;
+  a.p = dy, a.ldp = lddy, a.q = w_down, a.ldq = I, a.q_rows = N;
+  a.offsets = s.offsets, a.counts = s.counts, a.G = s.G, a.M = s.M, a.num_cus = s.num_cus;
   a.n_cols = I, a.sum = N, a.out = dh, a.ldo = lddh, a.out2 = act, a.ldo2 = lda, a.h = h, a.ldh = ldh;
   return launch<kGatedBwd>(a, plan_rows(s, I, N, false).shape, st);
 }
@@ -688,7 +767,7 @@ hipError_t launch_grouped_dw(const Segments& s, int64_t N, int64_t K, const uint
   const Plan p = s.M == 0 ? Plan{2, 1} : plan_dw(s.G, s.M, N, K);
   BfArgs a{};
   a.p = dy, a.ldp = lddy, a.q = x, a.ldq = ldx;
-  a.offsets = s.offsets, a.counts = s.counts, a.G = s.G, a.M = s.M;
+  a.offsets = s.offsets, a.counts = s.counts, a.G = s.G, a.M = s.M, a.num_cus = s.num_cus;
   a.m_cols = N, a.n_cols = K, a.ldo = K, a.splits = p.splits;
   if (p.splits == 1) {
     a.out = dw, a.out_f32 = dw_f32, a.accumulate = accumulate;
