@@ -748,7 +748,7 @@ static fgg_status lora_check(int64_t T, int32_t L, int32_t r, int64_t N, int64_t
 fgg_status fgg_lora_workspace(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K, size_t* bytes) {
   if (!bytes) return FGG_ERR_INVALID_VALUE;
   FGG_TRY(lora_check(T, L, r, N, K));
-  *bytes = fgg::lora_workspace_bytes(T, L, r, K);
+  *bytes = fgg::lora_workspace_bytes(T, L, r, N, K);
   return FGG_OK;
 }
 
@@ -766,7 +766,7 @@ fgg_status fgg_lora_add(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K, c
   if (!x || !ids || !a || !b || !base || !out || !workspace) return FGG_ERR_INVALID_VALUE;
   if (!aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(base, 16) || !aligned(out, 16) ||
       !aligned(ids, 4) || !aligned(scales, 4) || !aligned(workspace, 16) ||
-      ws_bytes < fgg::lora_workspace_bytes(T, L, r, K))
+      ws_bytes < fgg::lora_workspace_bytes(T, L, r, N, K))
     return FGG_ERR_INVALID_VALUE;
   FGG_TRY(device_check(nullptr));
   return finish(fgg::launch_lora(T, L, r, N, K, (const uint16_t*)x, ldx, ids, (const uint16_t*)a, (const uint16_t*)b,

@@ -41,7 +41,7 @@ extern const KernelInfo kInfoQuantE4m3_1x128, kInfoQuantE4m3_128x128, kInfoQuant
     kInfoW4a4Gemm, kInfoMxfp4Gemm, kInfoRoute, kInfoRowsScatter, kInfoRowsCollect, kInfoRowsScatterDot,
     kInfoRowsCollectDot;
 // (kernels with several forms: one entry for each that differs in its workgroup)
-constexpr int kRouteBackwardForms = 7, kGemvForms = 21, kGemmBf16Forms = 15, kLoraForms = 14;
+constexpr int kRouteBackwardForms = 7, kGemvForms = 21, kGemmBf16Forms = 15, kLoraForms = 20;
 extern const KernelInfo kInfoRouteBackward[kRouteBackwardForms], kInfoGemvFp4[kGemvForms],
     kInfoGemmBf16[kGemmBf16Forms], kInfoLora[kLoraForms], kInfoRowsBf16[2],
     kInfoDwJoin[4];
@@ -189,7 +189,7 @@ hipError_t launch_rows_bf16(const Segments& s, bool gated, int64_t N, int64_t K,
                             const uint16_t* w, void* out, bool out_f32, int64_t ldo, uint16_t* h, int64_t ldh,
                             hipStream_t st);
 // Low-rank adapters: the per-token low-rank sums (workspace: the chunks' fp32 sums), then the result on top of base.
-size_t lora_workspace_bytes(int64_t T, int32_t L, int32_t r, int64_t K);
+size_t lora_workspace_bytes(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K);
 hipError_t launch_lora(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K, const uint16_t* x, int64_t ldx,
                        const int32_t* ids, const uint16_t* a, const uint16_t* b, const float* scales, const void* base,
                        int64_t ldb, void* out, bool f32, int64_t ldo, float* ws, hipStream_t st);

@@ -28,8 +28,6 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
 constexpr int kSpan = 128;               // of the sum over K per item
 constexpr int kCols = 32;                // columns per item of the second product
-constexpr int kMaxRank = 128;
-constexpr int kVRow = kMaxRank + 8;      // a token's row in LDS, in bf16 elements (16 bytes past a multiple of the banks)
 
 __device__ inline v8bf load_or_zero(const uint16_t* p, bool on) {
   uint4 u = make_uint4(0, 0, 0, 0);
@@ -46,12 +44,46 @@ __device__ inline int lane_adapter(const int32_t* ids, int64_t t0, int tokens, i
 
 }  // namespace
 
+// This wave's items of a tile: each adapter of the tile with each step of [from, to), dealt to the workgroup's waves
+// in turn.
+struct Items {
+  uint64_t left;         // tokens whose adapter is still to come
+  uint64_t match;        // the current adapter's tokens
+  int cur;               // the current adapter
+  int64_t at, from, to;  // current place
+  int step, item, wave;
+
+  // The next item of this wave; false when there is none.
+  __device__ bool next(int id) {
+    while (true) {
+      if (at >= to) {
+        if (!left) return false;
+        cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+        match = __ballot(id == cur);
+        left &= ~match;
+        at = from - step;
+      }
+      // (the steps up to the wave's own are passed over at once)
+      const int skip = (wave - item) & (kWaves - 1);
+      const int64_t rest = (to - at - 1) / step;      // steps left after `at`
+      if (skip + 1 > rest) {
+        item = (int)((item + rest) & (kWaves - 1));
+        at = to;
+        continue;
+      }
+      at += (int64_t)(skip + 1) * step;
+      item = (item + skip + 1) & (kWaves - 1);
+      return true;
+    }
+  }
+};
+
 // part[chunk][t][j] = sum over the chunk's k of x[t][k] A[ids[t]][j][k];  TT tiles of 16 tokens, RT of 16 ranks.
 template <int TT, int RT>
-__global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const uint16_t* __restrict__ x, int64_t ldx,
-                                                               const int32_t* __restrict__ ids,
-                                                               const uint16_t* __restrict__ a, int64_t T, int L, int r,
-                                                               int64_t K, int chunk, float* __restrict__ part) {
+__global__ void __launch_bounds__(kThreads, TT + RT <= 2 ? 4 : 2)
+lora_shrink_kernel(const uint16_t* __restrict__ x, int64_t ldx, const int32_t* __restrict__ ids,
+                   const uint16_t* __restrict__ a, int64_t T, int L, int r, int64_t K, int chunk,
+                   float* __restrict__ part) {
   __shared__ float red[kWaves][16 * TT][16 + 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, q = lane >> 4;
@@ -65,58 +97,72 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const uint16_t* _
 #pragma unroll
     for (int f = 0; f < TT; ++f) sum[i][f] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  int item = 0;
-  for (uint64_t left = __ballot(id >= 0); left;) {
-    const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-    const uint64_t match = __ballot(id == cur);
-    left &= ~match;
-    const uint16_t* mine = a + (int64_t)cur * r * K;
-    for (int64_t k = k0; k < k1; k += kSpan) {
-      if ((item++ & (kWaves - 1)) != wave) continue;
-      v8bf xf[TT][kSpan / 32];
+  constexpr int kSteps = kSpan / 32;
+  struct Operands {
+    v8bf x[TT][kSteps], a[RT][kSteps];
+    uint64_t match;
+  };
+  auto load = [&](const Items& it, Operands& o) {
+    o.match = it.match;
 #pragma unroll
-      for (int f = 0; f < TT; ++f)
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
-        for (int s = 0; s < kSpan / 32; ++s) {
-          const int64_t at = k + 32 * s + 8 * q;
-          const bool on = (match >> (16 * f + l16) & 1) && at < k1;
-          xf[f][s] = load_or_zero(x + (t0 + 16 * f + l16) * ldx + at, on);
-        }
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        v8bf af[kSpan / 32];
-#pragma unroll
-        for (int s = 0; s < kSpan / 32; ++s) {
-          const int64_t at = k + 32 * s + 8 * q;
-          const int row = 16 * i + l16;
-          af[s] = load_or_zero(mine + (int64_t)row * K + at, row < r && at < k1);
-        }
-#pragma unroll
-        for (int f = 0; f < TT; ++f) {
-          v4f d = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int s = 0; s < kSpan / 32; ++s) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[s], xf[f][s], d, 0, 0, 0);
-          const bool on = match >> (16 * f + l16) & 1;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sum[i][f][e] += on ? d[e] : 0.0f;
-        }
-      }
-    }
-  }
-
-  // the eight waves' sums, in their order
-  for (int i = 0; i < RT && 16 * i < r; ++i) {
-    v4f s[TT];
-#pragma unroll
-    for (int j = 0; j < RT; ++j)
-      if (j == i) {
-#pragma unroll
-        for (int f = 0; f < TT; ++f) s[f] = sum[j][f];
+      for (int s = 0; s < kSteps; ++s) {
+        const int64_t k = it.at + 32 * s + 8 * q;
+        const int row = 16 * i + l16;
+        o.a[i][s] = load_or_zero(a + ((int64_t)it.cur * r + row) * K + k, row < r && k < k1);
       }
 #pragma unroll
     for (int f = 0; f < TT; ++f)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) red[wave][16 * f + l16][4 * q + e] = s[f][e];
+      for (int s = 0; s < kSteps; ++s) {
+        const int64_t k = it.at + 32 * s + 8 * q;
+        o.x[f][s] = load_or_zero(x + (t0 + 16 * f + l16) * ldx + k, (it.match >> (16 * f + l16) & 1) && k < k1);
+      }
+  };
+  auto use = [&](const Operands& o) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int f = 0; f < TT; ++f) {
+        v4f d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(o.a[i][s], o.x[f][s], d, 0, 0, 0);
+        const bool on = o.match >> (16 * f + l16) & 1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[i][f][e] += on ? d[e] : 0.0f;
+      }
+  };
+  Items it = {__ballot(id >= 0), 0, -1, k1, k0, k1, kSpan, kWaves - 1, wave};
+  if constexpr (TT + RT <= 4) {          // the next item's operands are loaded before this one's are waited for
+    Operands o[2];
+    bool more = it.next(id);
+    if (more) load(it, o[0]);
+    while (more) {
+      more = it.next(id);
+      if (more) load(it, o[1]);
+      use(o[0]);
+      if (!more) break;
+      more = it.next(id);
+      if (more) load(it, o[0]);
+      use(o[1]);
+    }
+  } else {
+    Operands o;
+    while (it.next(id)) {
+      load(it, o);
+      use(o);
+    }
+  }
+
+  // the eight waves' sums, in their order
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    if (16 * i >= r) break;
+#pragma unroll
+    for (int f = 0; f < TT; ++f)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) red[wave][16 * f + l16][4 * q + e] = sum[i][f][e];
     __syncthreads();
     for (int v = threadIdx.x; v < 256 * TT; v += kThreads) {
       const int t = v >> 4, j = v & 15;
@@ -130,196 +176,283 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const uint16_t* _
 }
 
 // out[t][n] = base[t][n] + sum_j v[t][j] B[ids[t]][n][j],  v = scales[ids[t]] times the chunks' sums.
-template <int TT, bool F32>
-__global__ void __launch_bounds__(kThreads) lora_expand_kernel(const float* __restrict__ part, int chunks,
-                                                               const int32_t* __restrict__ ids,
-                                                               const uint16_t* __restrict__ b,
-                                                               const float* __restrict__ scales, const void* base,
-                                                               int64_t ldb, void* out, int64_t ldo, int64_t T, int L,
-                                                               int r, int64_t N, int cols) {
-  constexpr int kParts = F32 ? 3 : 2;
+// TT tiles of 16 tokens, rank up to 32 RS.
+template <int TT, int RS, bool F32>
+__global__ void __launch_bounds__(kThreads, TT == 4 && (RS == 4 || F32) ? 2 : 4)
+lora_expand_kernel(const float* __restrict__ part, int chunks, const int32_t* __restrict__ ids,
+                   const uint16_t* __restrict__ b, const float* __restrict__ scales, const void* base, int64_t ldb,
+                   void* out, int64_t ldo, int64_t T, int L, int r, int64_t N, int cols) {
+  constexpr int kParts = F32 ? 3 : 2, kVRow = 32 * RS + 8, kElem = F32 ? 4 : 2;
   __shared__ __align__(16) uint16_t vs[kParts][16 * TT][kVRow];
+  __shared__ float4 red[kThreads];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, q = lane >> 4;
   const int64_t t0 = (int64_t)blockIdx.x * (16 * TT);
   const int64_t n_from = (int64_t)blockIdx.y * cols, n_to = n_from + cols < N ? n_from + cols : N;
   const int id = lane_adapter(ids, t0, 16 * TT, T, L, lane);
 
-  // a token's low-rank sums in bf16 parts, zeros past the rank
-  const int wide = (r + 31) & ~31;
-  for (int v = threadIdx.x; v < 16 * TT * wide; v += kThreads) {
-    const int t = v / wide, j = v - t * wide;
-    float s = 0.0f;
-    if (t0 + t < T && j < r) {
-      const int i = ids[t0 + t];
-      if (i >= 0 && i < L) {
-        for (int c = 0; c < chunks; ++c) s += part[((int64_t)c * T + t0 + t) * r + j];
-        if (scales) s *= scales[i];
-      }
-    }
+  // an item's operands: rows of two fragments are dealt so that a lane's results are eight consecutive columns
+  struct Operands {
+    v8bf b[2][RS];
+    uint4 y[TT][kElem / 2];
+    uint64_t match;
+    int64_t at;
+  };
+  auto load = [&](const Items& it, Operands& o) {
+    o.match = it.match;
+    o.at = it.at;
 #pragma unroll
-    for (int p = 0; p < kParts; ++p) {
-      const uint16_t bits = (uint16_t)bf16x2_rne(s, 0.0f);
-      vs[p][t][j] = bits;
-      // (an infinite or NaN part carries the whole)
-      const float v0 = bf16_to_f32(bits);
-      s = fabsf(v0) < INFINITY ? s - v0 : 0.0f;
-    }
-  }
-  __syncthreads();
-
-  int item = 0;
-  auto columns = [&](int cur, uint64_t match) {
-    for (int64_t n0 = n_from; n0 < n_to; n0 += kCols) {
-      if ((item++ & (kWaves - 1)) != wave) continue;
-      // rows of two fragments are dealt so that a lane's results are eight consecutive columns
-      v8bf bf[2][kMaxRank / 32];
-      if (cur >= 0) {
+    for (int f = 0; f < 2; ++f)
 #pragma unroll
-        for (int f = 0; f < 2; ++f)
-#pragma unroll
-          for (int s = 0; s < kMaxRank / 32; ++s) {
-            if (32 * s >= r) break;
-            const int64_t n = n0 + 8 * (l16 >> 2) + 4 * f + (l16 & 3);
-            const int j = 32 * s + 8 * q;
-            bf[f][s] = load_or_zero(b + ((int64_t)cur * N + n) * r + j, n < n_to && j < r);
-          }
+      for (int s = 0; s < RS; ++s) {
+        const int64_t n = it.at + 8 * (l16 >> 2) + 4 * f + (l16 & 3);
+        const int j = 32 * s + 8 * q;
+        o.b[f][s] = load_or_zero(b + ((int64_t)it.cur * N + n) * r + j, n < n_to && j < r);
       }
 #pragma unroll
-      for (int f = 0; f < TT; ++f) {
-        if ((match >> (16 * f) & 0xFFFF) == 0) continue;
-        const int64_t t = t0 + 16 * f + l16, n = n0 + 8 * q;
-        const bool on = (match >> (16 * f + l16) & 1) && n < n_to;
-        float y[8];
-        if (on) load8<!F32>(base, t * ldb + n, y);
-        if (cur >= 0) {
-          v4f d[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    for (int f = 0; f < TT; ++f) {
+      const int64_t t = t0 + 16 * f + l16, n = it.at + 8 * q;
+      if ((it.match >> (16 * f + l16) & 1) && n < n_to) {
+        const uint4* p = reinterpret_cast<const uint4*>((const char*)base + (t * ldb + n) * kElem);
 #pragma unroll
-          for (int s = 0; s < kMaxRank / 32; ++s) {
-            if (32 * s >= r) break;
-#pragma unroll
-            for (int p = kParts - 1; p >= 0; --p) {
-              const v8bf v = *reinterpret_cast<const v8bf*>(&vs[p][16 * f + l16][32 * s + 8 * q]);
-              d[0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[0][s], v, d[0], 0, 0, 0);
-              d[1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[1][s], v, d[1], 0, 0, 0);
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] += d[e >> 2][e & 3];
-        }
-        if (on) {
-          if constexpr (F32) {
-            float4* o = reinterpret_cast<float4*>((float*)out + t * ldo + n);
-            o[0] = make_float4(y[0], y[1], y[2], y[3]);
-            o[1] = make_float4(y[4], y[5], y[6], y[7]);
-          } else {
-            *reinterpret_cast<uint4*>((uint16_t*)out + t * ldo + n) =
-                make_uint4(bf16x2_rne(y[0], y[1]), bf16x2_rne(y[2], y[3]), bf16x2_rne(y[4], y[5]),
-                           bf16x2_rne(y[6], y[7]));
-          }
-        }
+        for (int k = 0; k < kElem / 2; ++k) o.y[f][k] = p[k];
       }
     }
   };
-  for (uint64_t left = __ballot(id >= 0); left;) {
-    const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-    const uint64_t match = __ballot(id == cur);
-    left &= ~match;
-    columns(cur, match);
+  auto store = [&](int64_t t, int64_t n, const float* y) {
+    if constexpr (F32) {
+      float4* o = reinterpret_cast<float4*>((float*)out + t * ldo + n);
+      o[0] = make_float4(y[0], y[1], y[2], y[3]);
+      o[1] = make_float4(y[4], y[5], y[6], y[7]);
+    } else {
+      *reinterpret_cast<uint4*>((uint16_t*)out + t * ldo + n) =
+          make_uint4(bf16x2_rne(y[0], y[1]), bf16x2_rne(y[2], y[3]), bf16x2_rne(y[4], y[5]), bf16x2_rne(y[6], y[7]));
+    }
+  };
+  auto use = [&](const Operands& o) {
+#pragma unroll
+    for (int f = 0; f < TT; ++f) {
+      if ((o.match >> (16 * f) & 0xFFFF) == 0) continue;
+      v4f d[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int s = 0; s < RS; ++s)
+#pragma unroll
+        for (int p = kParts - 1; p >= 0; --p) {
+          const v8bf v = *reinterpret_cast<const v8bf*>(&vs[p][16 * f + l16][32 * s + 8 * q]);
+          d[0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(o.b[0][s], v, d[0], 0, 0, 0);
+          d[1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(o.b[1][s], v, d[1], 0, 0, 0);
+        }
+      const int64_t n = o.at + 8 * q;
+      if ((o.match >> (16 * f + l16) & 1) && n < n_to) {
+        float y[8];
+        if constexpr (F32) {
+          __builtin_memcpy(y, o.y[f], 32);
+        } else {
+          const uint32_t w[4] = {o.y[f][0].x, o.y[f][0].y, o.y[f][0].z, o.y[f][0].w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] += d[e >> 2][e & 3];
+        store(t0 + 16 * f + l16, n, y);
+      }
+    }
+  };
+
+  Items it = {__ballot(id >= 0), 0, -1, n_to, n_from, n_to, kCols, kWaves - 1, wave};
+  Operands o[2];
+  bool more = it.next(id);
+  if (more) load(it, o[0]);
+
+  // The tokens' low-rank sums in bf16 parts, zeros past the rank, four at a time.  With many chunks several threads
+  // share them, each a run of chunks in order, and the runs are added in order.
+  constexpr int kQuads = 16 * TT * 8 * RS;
+  auto sum_of = [&](int quad, int c0, int c1) {
+    const int t = quad / (8 * RS), j = quad % (8 * RS) * 4;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (t0 + t < T && j < r) {
+      const float4* p = reinterpret_cast<const float4*>(part + (t0 + t) * r + j);
+      const int64_t stride = T * r / 4;
+      for (int c = c0; c < c1; c += 4) {
+        float4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = c + k < c1 ? p[(c + k) * stride] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s.x += v[k].x, s.y += v[k].y, s.z += v[k].z, s.w += v[k].w;
+      }
+    }
+    return s;
+  };
+  auto keep = [&](int quad, float4 s) {
+    const int t = quad / (8 * RS), j = quad % (8 * RS) * 4;
+    const int i = t0 + t < T ? ids[t0 + t] : -1;
+    const bool on = i >= 0 && i < L;
+    const float scale = on && scales ? scales[i] : 1.0f;
+    float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = on ? v[e] * scale : 0.0f;
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
+      uint32_t w[2] = {bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
+      *reinterpret_cast<uint2*>(&vs[p][t][j]) = make_uint2(w[0], w[1]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {      // (an infinite or NaN part carries the whole)
+        const float v0 = __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
+        v[e] = fabsf(v0) < INFINITY ? v[e] - v0 : 0.0f;
+      }
+    }
+  };
+  if constexpr (kQuads < kThreads) {
+    constexpr int kRuns = kThreads / kQuads;
+    const int quad = threadIdx.x % kQuads, run = threadIdx.x / kQuads, each = (chunks + kRuns - 1) / kRuns;
+    const int c0 = run * each, c1 = c0 + each < chunks ? c0 + each : chunks;
+    red[threadIdx.x] = sum_of(quad, c0, c1);
+    __syncthreads();
+    if (threadIdx.x < kQuads) {
+      float4 s = red[threadIdx.x];
+#pragma unroll
+      for (int k = 1; k < kRuns; ++k) {
+        const float4 v = red[k * kQuads + threadIdx.x];
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+      }
+      keep(threadIdx.x, s);
+    }
+  } else {
+    for (int quad = threadIdx.x; quad < kQuads; quad += kThreads) keep(quad, sum_of(quad, 0, chunks));
   }
-  if (out != base) {
+  __syncthreads();
+
+  while (more) {
+    more = it.next(id);
+    if (more) load(it, o[1]);
+    use(o[0]);
+    if (!more) break;
+    more = it.next(id);
+    if (more) load(it, o[0]);
+    use(o[1]);
+  }
+
+  if (out != base) {                     // tokens without an adapter: copied
     const uint64_t none = __ballot(id < 0 && lane < 16 * TT && t0 + lane < T);
-    if (none) columns(-1, none);
+    for (int64_t n0 = n_from + wave * kCols; none && n0 < n_to; n0 += kWaves * kCols) {
+#pragma unroll
+      for (int f = 0; f < TT; ++f) {
+        const int64_t t = t0 + 16 * f + l16, n = n0 + 8 * q;
+        if ((none >> (16 * f + l16) & 1) && n < n_to) {
+          const uint4* p = reinterpret_cast<const uint4*>((const char*)base + (t * ldb + n) * kElem);
+          uint4* to = reinterpret_cast<uint4*>((char*)out + (t * ldo + n) * kElem);
+#pragma unroll
+          for (int k = 0; k < kElem / 2; ++k) to[k] = p[k];
+        }
+      }
+    }
   }
 }
 
 namespace {
 
-// A launch's shape.  Tiles of 64 tokens read each factor a quarter as often where tokens share them (32 over rank
-// 64, whose sums would not fit the registers).  The sum over K is cut so that few tokens still give every
-// compute unit loads to wait for.
+// A launch's shape.  Many tokens: tiles of 32 (64 over B) read each factor less often where tokens share them, and the
+// sum over K is taken whole as soon as the tiles fill the chip.  Few tokens: it is cut so that a wave has about
+// two items, as long as a token's chunks stay few enough to add.
 struct LoraPlan {
-  int tile, chunk, chunks;
+  int tile, chunk, chunks;     // of the first product
+  int tile2, cols;             // of the second
 };
 
-LoraPlan plan(int64_t T, int32_t L, int32_t r, int64_t K) {
+LoraPlan plan(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K) {
   LoraPlan p;
-  p.tile = T < 512 ? 16 : r <= 64 ? 64 : 32;
-  const int64_t tiles = (T + p.tile - 1) / p.tile;
-  const int64_t spans = (K + kSpan - 1) / kSpan;
-  const int64_t adapters = T < L ? (T < p.tile ? T : p.tile) : (L < p.tile ? L : p.tile);
-  // two items a wave, as long as there are fewer workgroups than 512
-  int64_t per = (2 * kWaves + adapters - 1) / adapters;
+  p.tile = T < 512 ? 16 : 32;
+  p.tile2 = T < 512 ? 16 : 64;
+  auto distinct = [&](int64_t tile) {
+    const int64_t n = T < tile ? T : tile;
+    return n < L ? n : (int64_t)L;
+  };
+  const int64_t tiles = (T + p.tile - 1) / p.tile, spans = (K + kSpan - 1) / kSpan;
+  int64_t per = (2 * kWaves + distinct(p.tile) - 1) / distinct(p.tile);
   const int64_t fill = (spans * tiles + 511) / 512;
   if (per < fill) per = fill;
+  if (per < (spans + 31) / 32) per = (spans + 31) / 32;
   if (per > spans) per = spans;
-  while ((spans + per - 1) / per > 32) ++per;
   p.chunk = (int)per * kSpan;
   p.chunks = (int)((spans + per - 1) / per);
+
+  const int64_t tiles2 = (T + p.tile2 - 1) / p.tile2, steps = (N + kCols - 1) / kCols;
+  int64_t cols = (steps * tiles2 + 511) / 512;
+  const int64_t least = (2 * kWaves + distinct(p.tile2) - 1) / distinct(p.tile2);
+  if (T >= 512 && cols < least) cols = least;
+  if (cols > steps) cols = steps;
+  p.cols = (int)cols * kCols;
   return p;
 }
 
 #define FGG_LORA_SHRINK(tt, rt) \
   {"lora_shrink_kernel<" #tt "," #rt ">", "fgg_lora_add", 16 * tt, 16 * rt, kSpan, kThreads, 0, 0, \
    kWaves * 16 * tt * 17 * 4, kWaves * 16 * tt * 17 * 4, (const void*)lora_shrink_kernel<tt, rt>}
-#define FGG_LORA_EXPAND(tt, f32, name) \
-  {"lora_expand_kernel<" #tt "," name ">", "fgg_lora_add", 16 * tt, kCols, kMaxRank, kThreads, 0, 0, \
-   (f32 ? 3 : 2) * 16 * tt * kVRow * 2, (f32 ? 3 : 2) * 16 * tt * kVRow * 2, (const void*)lora_expand_kernel<tt, f32>}
+#define FGG_LORA_EXPAND(tt, rs, f32, name) \
+  {"lora_expand_kernel<" #tt "," #rs "," name ">", "fgg_lora_add", 16 * tt, kCols, 32 * rs, kThreads, 0, 0, \
+   (f32 ? 3 : 2) * 16 * tt * (32 * rs + 8) * 2 + kRed(tt, rs), \
+   (f32 ? 3 : 2) * 16 * tt * (32 * rs + 8) * 2 + kRed(tt, rs), (const void*)lora_expand_kernel<tt, rs, f32>}
+// (the runs' sums: only where a tile has fewer quads than threads)
+constexpr int kRed(int tt, int rs) { return 16 * tt * 8 * rs < kThreads ? kThreads * 16 : 0; }
 
 }  // namespace
 
 const KernelInfo kInfoLora[kLoraForms] = {
     FGG_LORA_SHRINK(1, 1), FGG_LORA_SHRINK(1, 2), FGG_LORA_SHRINK(1, 4), FGG_LORA_SHRINK(1, 8),
-    FGG_LORA_SHRINK(4, 1), FGG_LORA_SHRINK(4, 2), FGG_LORA_SHRINK(4, 4), FGG_LORA_SHRINK(2, 8),
-    FGG_LORA_EXPAND(1, false, "bf16"), FGG_LORA_EXPAND(1, true, "f32"), FGG_LORA_EXPAND(2, false, "bf16"),
-    FGG_LORA_EXPAND(2, true, "f32"), FGG_LORA_EXPAND(4, false, "bf16"), FGG_LORA_EXPAND(4, true, "f32"),
+    FGG_LORA_SHRINK(2, 1), FGG_LORA_SHRINK(2, 2), FGG_LORA_SHRINK(2, 4), FGG_LORA_SHRINK(2, 8),
+    FGG_LORA_EXPAND(1, 1, false, "bf16"), FGG_LORA_EXPAND(1, 2, false, "bf16"), FGG_LORA_EXPAND(1, 4, false, "bf16"),
+    FGG_LORA_EXPAND(1, 1, true, "f32"), FGG_LORA_EXPAND(1, 2, true, "f32"), FGG_LORA_EXPAND(1, 4, true, "f32"),
+    FGG_LORA_EXPAND(4, 1, false, "bf16"), FGG_LORA_EXPAND(4, 2, false, "bf16"), FGG_LORA_EXPAND(4, 4, false, "bf16"),
+    FGG_LORA_EXPAND(4, 1, true, "f32"), FGG_LORA_EXPAND(4, 2, true, "f32"), FGG_LORA_EXPAND(4, 4, true, "f32"),
 };
 
-size_t lora_workspace_bytes(int64_t T, int32_t L, int32_t r, int64_t K) {
-  return T == 0 ? 0 : (size_t)plan(T, L, r, K).chunks * (size_t)T * (size_t)r * 4;
+size_t lora_workspace_bytes(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K) {
+  return T == 0 ? 0 : (size_t)plan(T, L, r, N, K).chunks * (size_t)T * (size_t)r * 4;
 }
 
 hipError_t launch_lora(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K, const uint16_t* x, int64_t ldx,
                        const int32_t* ids, const uint16_t* a, const uint16_t* b, const float* scales, const void* base,
                        int64_t ldb, void* out, bool f32, int64_t ldo, float* ws, hipStream_t st) {
-  const LoraPlan p = plan(T, L, r, K);
-  const unsigned tiles = (unsigned)((T + p.tile - 1) / p.tile);
-  const bool wide = p.tile > 16;
-  const int ranks = r <= 16 ? 0 : r <= 32 ? 1 : r <= 64 ? 2 : 3;
-  const dim3 g1(tiles, (unsigned)p.chunks);
-  trace_launch(kInfoLora[(wide ? 4 : 0) + ranks], g1, "T=%lld L=%d r=%d K=%lld", (long long)T, L, r, (long long)K);
+  const LoraPlan p = plan(T, L, r, N, K);
+  const dim3 g1((unsigned)((T + p.tile - 1) / p.tile), (unsigned)p.chunks);
+  const int first = (p.tile == 16 ? 0 : 4) + (r <= 16 ? 0 : r <= 32 ? 1 : r <= 64 ? 2 : 3);
+  trace_launch(kInfoLora[first], g1, "T=%lld L=%d r=%d K=%lld", (long long)T, L, r, (long long)K);
   auto shrink = [&](auto* kernel) {
     hipLaunchKernelGGL(kernel, g1, dim3(kThreads), 0, st, x, ldx, ids, a, T, L, r, K, p.chunk, ws);
   };
-  switch ((wide ? 4 : 0) + ranks) {
+  switch (first) {
     case 0: shrink(lora_shrink_kernel<1, 1>); break;
     case 1: shrink(lora_shrink_kernel<1, 2>); break;
     case 2: shrink(lora_shrink_kernel<1, 4>); break;
     case 3: shrink(lora_shrink_kernel<1, 8>); break;
-    case 4: shrink(lora_shrink_kernel<4, 1>); break;
-    case 5: shrink(lora_shrink_kernel<4, 2>); break;
-    case 6: shrink(lora_shrink_kernel<4, 4>); break;
+    case 4: shrink(lora_shrink_kernel<2, 1>); break;
+    case 5: shrink(lora_shrink_kernel<2, 2>); break;
+    case 6: shrink(lora_shrink_kernel<2, 4>); break;
     default: shrink(lora_shrink_kernel<2, 8>); break;
   }
-  hipError_t e = hipGetLastError();
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // columns of a workgroup: about 1024 workgroups, at least one item a wave where one adapter takes the tile
-  int64_t steps = (N + kCols - 1) / kCols;
-  int64_t per = (steps * tiles + 1023) / 1024;
-  const int64_t adapters = T < L ? (T < p.tile ? T : p.tile) : (L < p.tile ? L : p.tile);
-  const int64_t least = (kWaves + adapters - 1) / adapters;
-  if (per < least) per = least;
-  if (per > steps) per = steps;
-  const dim3 g2(tiles, (unsigned)((steps + per - 1) / per));
-  trace_launch(kInfoLora[8 + (p.tile >> 5) * 2 + (f32 ? 1 : 0)], g2, "T=%lld L=%d r=%d N=%lld", (long long)T, L, r,
-               (long long)N);
+  const dim3 g2((unsigned)((T + p.tile2 - 1) / p.tile2), (unsigned)((N + p.cols - 1) / p.cols));
+  const int second = (p.tile2 == 16 ? 0 : 6) + (f32 ? 3 : 0) + (r <= 32 ? 0 : r <= 64 ? 1 : 2);
+  trace_launch(kInfoLora[8 + second], g2, "T=%lld L=%d r=%d N=%lld", (long long)T, L, r, (long long)N);
   auto expand = [&](auto* kernel) {
     hipLaunchKernelGGL(kernel, g2, dim3(kThreads), 0, st, ws, p.chunks, ids, b, scales, base, ldb, out, ldo, T, L, r,
-                       N, (int)per * kCols);
+                       N, p.cols);
   };
-  if (p.tile == 64) f32 ? expand(lora_expand_kernel<4, true>) : expand(lora_expand_kernel<4, false>);
-  else if (p.tile == 32) f32 ? expand(lora_expand_kernel<2, true>) : expand(lora_expand_kernel<2, false>);
-  else f32 ? expand(lora_expand_kernel<1, true>) : expand(lora_expand_kernel<1, false>);
+  switch (second) {
+    case 0: expand(lora_expand_kernel<1, 1, false>); break;
+    case 1: expand(lora_expand_kernel<1, 2, false>); break;
+    case 2: expand(lora_expand_kernel<1, 4, false>); break;
+    case 3: expand(lora_expand_kernel<1, 1, true>); break;
+    case 4: expand(lora_expand_kernel<1, 2, true>); break;
+    case 5: expand(lora_expand_kernel<1, 4, true>); break;
+    case 6: expand(lora_expand_kernel<4, 1, false>); break;
+    case 7: expand(lora_expand_kernel<4, 2, false>); break;
+    case 8: expand(lora_expand_kernel<4, 4, false>); break;
+    case 9: expand(lora_expand_kernel<4, 1, true>); break;
+    case 10: expand(lora_expand_kernel<4, 2, true>); break;
+    default: expand(lora_expand_kernel<4, 4, true>); break;
+  }
   return hipGetLastError();
 }
 
