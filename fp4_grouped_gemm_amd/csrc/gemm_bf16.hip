@@ -57,6 +57,8 @@ struct Shape {
 using Large = Shape<256, 256, 2, 4, 64, 2>;
 using Medium = Shape<128, 128, 2, 2, 64, 2>;
 using Small = Shape<64, 64, 2, 2, 64, 4>;
+using Quarter = Shape<128, 128, 2, 4, 64, 4>;            // of a Large tile, by its eight waves
+static_assert(Quarter::kThreads == Large::kThreads && Quarter::kLdsBytes <= Large::kLdsBytes, "one workgroup");
 
 // "row" tiles: the 16-byte chunk c of row r lies at chunk c ^ row_key(r), such that the sixteen lanes that one
 // cycle of a ds_read_b128 serves (rows 0..3 and 12..15 of one chunk, 4..11 of the next) hit different chunks.
@@ -132,90 +134,128 @@ struct BfArgs {
   int splits;                          // kDw: parts of the sum, each with its own fp32 result
 };
 
+namespace {
+
+// (equal in every lane: kept in a scalar register)
+__device__ inline int same(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ inline int64_t same(int64_t v) {
+  return (int64_t)((uint64_t)(uint32_t)same((int)(v >> 32)) << 32 | (uint32_t)same((int)v));
+}
+
+// A tile: where it lies, and how long its sum is.
+struct Tile {
+  int64_t p_row, q_row, out_row;     // first row of P and Q (of the sum, for "col" operands), of the output
+  int m0, n0, m_here, n_here, sum;   // first output row and column in the segment's result; what is left from there
+};
+
+// Tiles of the whole launch.
 template <int F, class S>
-__global__ void __launch_bounds__(S::kThreads, 2) gemm_bf16_kernel(const BfArgs A) {
-  __shared__ __align__(16) uint8_t smem[S::kLdsBytes];
+__device__ inline int count_tiles(const BfArgs& A) {
+  if (F == kDw) return A.splits * A.G * A.m_tiles * A.n_tiles;
+  if (A.offsets == nullptr) return (int)((A.M + S::M - 1) / S::M) * A.n_tiles;
+  const int lane = threadIdx.x & 63;
+  int n = 0;
+  for (int g = lane; g < A.G; g += 64) n += (segment_of(A.offsets, A.counts, g, A.M).rows + S::M - 1) / S::M;
+  for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d);
+  return same(n) * A.n_tiles;
+}
+
+// Tile t of the launch, segment by segment, in blocks 8 high; false past the last one.
+template <int F, class S>
+__device__ inline bool find_tile(const BfArgs& A, int t, Tile& tile) {
+  constexpr int BM = S::M, BN = S::N, BK = S::K;
+  const int lane = opaque(threadIdx.x & 63);
+  int g = 0, j = t, z = 0, mtg = A.m_tiles;
+  Segment seg;
+  if constexpr (F == kDw) {
+    const int each = A.m_tiles * A.n_tiles;
+    z = t / (A.G * each);
+    if (z >= A.splits) return false;
+    j = t - z * (A.G * each);
+    g = j / each;
+    j -= g * each;
+    seg = A.offsets ? segment_of(A.offsets, A.counts, g, A.M) : Segment{0, (int)A.M};
+  } else if (A.offsets == nullptr) {
+    seg = {0, (int)A.M};
+    mtg = (int)((A.M + BM - 1) / BM);
+    if (t >= mtg * A.n_tiles) return false;
+  } else {
+    int before = 0;
+    bool found = false;
+    for (int g0 = 0; g0 < A.G; g0 += 64) {
+      Segment mine = {0, 0};
+      if (g0 + lane < A.G) mine = segment_of(A.offsets, A.counts, g0 + lane, A.M);
+      const int tiles = (mine.rows + BM - 1) / BM * A.n_tiles;
+      int upto = tiles;
+      for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(upto, d);
+        if (lane >= d) upto += v;
+      }
+      const uint64_t hit = __ballot(before + upto > t);
+      if (hit) {
+        const int at = __builtin_ctzll(hit);
+        g = g0 + at;
+        j = t - (before + __builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(tiles, at));
+        seg.first = __builtin_amdgcn_readlane((int)mine.first, at);
+        seg.rows = __builtin_amdgcn_readlane(mine.rows, at);
+        found = true;
+        break;
+      }
+      before += __builtin_amdgcn_readlane(upto, 63);
+    }
+    if (!found) return false;
+    mtg = (seg.rows + BM - 1) / BM;
+  }
+  const int mb = j / (kSM * A.n_tiles), k_in = j - mb * kSM * A.n_tiles;
+  const int high = mtg - mb * kSM < kSM ? mtg - mb * kSM : kSM;
+  const int nt = k_in / high;
+  tile.m0 = (mb * kSM + k_in - nt * high) * BM;
+  tile.n0 = nt * (F == kGated ? BN / 2 : BN);
+  tile.n_here = (int)A.n_cols - tile.n0;
+  if constexpr (F == kDw) {
+    // part z of the sum over the segment's rows
+    const int per = ((seg.rows + BK - 1) / BK + A.splits - 1) / A.splits * BK;
+    const int first = (int64_t)per * z < seg.rows ? per * z : seg.rows;
+    tile.sum = seg.rows - first < per ? seg.rows - first : per;
+    tile.m_here = (int)A.m_cols - tile.m0;
+    tile.p_row = tile.q_row = seg.first + first;
+    tile.out_row = ((int64_t)z * A.G + g) * A.m_cols + tile.m0;
+  } else {
+    tile.sum = (int)A.sum;
+    tile.m_here = seg.rows - tile.m0;
+    tile.p_row = tile.out_row = seg.first + tile.m0;
+    tile.q_row = (int64_t)g * A.q_rows + (q_is_col(F) ? 0 : tile.n0);
+  }
+  tile = {same(tile.p_row), same(tile.q_row), same(tile.out_row), same(tile.m0),
+          same(tile.n0),    same(tile.m_here), same(tile.n_here), same(tile.sum)};
+  return true;
+}
+
+// Quadrant `quad` of a tile twice as high and wide as S; false where it holds nothing.
+template <int F, class S>
+__device__ inline bool quarter(Tile& t, int quad) {
+  const int down = (quad >> 1) * S::M, across = (quad & 1) * (F == kGated ? S::N / 2 : S::N);
+  if (down >= t.m_here || across >= t.n_here) return false;
+  t.m0 += down;
+  t.m_here -= down;
+  t.out_row += down;
+  if (!p_is_col(F)) t.p_row += down;
+  t.n0 += across;
+  t.n_here -= across;
+  if (!q_is_col(F)) t.q_row += across;
+  return true;
+}
+
+// Tiles of shape S, one after the other, as `source` gives them (round 0, 1, ...; false: no more).  The next
+// tile's first stages are loaded while the epilogue of the last one writes.
+template <int F, class S, class Source>
+__device__ __forceinline__ void run_tiles(const BfArgs& A, uint8_t* smem, Source source) {
   constexpr int BM = S::M, BN = S::N, BK = S::K, FI = S::FI, FJ = S::FJ;
   const uint32_t lds_base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / S::WN, wn = wave % S::WN;
   const int l16 = lane & 15, q = lane >> 4;
-  const auto same = [](int v) { return __builtin_amdgcn_readfirstlane(v); };   // (equal in every lane: kept in a scalar)
-  const auto same64 = [&](int64_t v) { return (int64_t)same((int)(v >> 32)) << 32 | (uint32_t)same((int)v); };
-
-  // Tile t of the launch (in the order of kChunk-blocks, see launch_shape): where it lies, and how long its sum is.
-  struct Tile {
-    int64_t p_row, q_row, out_row;     // first row of P and Q (of the sum, for "col" operands), of the output
-    int m0, n0, m_here, n_here, sum;   // first output row and column in the segment's result; what is left from there
-  };
-  auto find = [&](int t, Tile& tile) -> bool {
-    const int lane = opaque(threadIdx.x & 63);
-    int g = 0, j = t, z = 0, mtg = A.m_tiles;
-    Segment seg;
-    if constexpr (F == kDw) {
-      const int each = A.m_tiles * A.n_tiles;
-      z = t / (A.G * each);
-      if (z >= A.splits) return false;
-      j = t - z * (A.G * each);
-      g = j / each;
-      j -= g * each;
-      seg = A.offsets ? segment_of(A.offsets, A.counts, g, A.M) : Segment{0, (int)A.M};
-    } else if (A.offsets == nullptr) {
-      seg = {0, (int)A.M};
-      mtg = (int)((A.M + BM - 1) / BM);
-      if (t >= mtg * A.n_tiles) return false;
-    } else {
-      int before = 0;
-      bool found = false;
-      for (int g0 = 0; g0 < A.G; g0 += 64) {
-        Segment mine = {0, 0};
-        if (g0 + lane < A.G) mine = segment_of(A.offsets, A.counts, g0 + lane, A.M);
-        const int tiles = (mine.rows + BM - 1) / BM * A.n_tiles;
-        int upto = tiles;
-        for (int d = 1; d < 64; d <<= 1) {
-          const int v = __shfl_up(upto, d);
-          if (lane >= d) upto += v;
-        }
-        const uint64_t hit = __ballot(before + upto > t);
-        if (hit) {
-          const int at = __builtin_ctzll(hit);
-          g = g0 + at;
-          j = t - (before + __builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(tiles, at));
-          seg.first = __builtin_amdgcn_readlane((int)mine.first, at);
-          seg.rows = __builtin_amdgcn_readlane(mine.rows, at);
-          found = true;
-          break;
-        }
-        before += __builtin_amdgcn_readlane(upto, 63);
-      }
-      if (!found) return false;
-      mtg = (seg.rows + BM - 1) / BM;
-    }
-    const int mb = j / (kSM * A.n_tiles), k_in = j - mb * kSM * A.n_tiles;
-    const int high = mtg - mb * kSM < kSM ? mtg - mb * kSM : kSM;
-    const int nt = k_in / high;
-    tile.m0 = (mb * kSM + k_in - nt * high) * BM;
-    tile.n0 = nt * (F == kGated ? BN / 2 : BN);
-    tile.n_here = (int)A.n_cols - tile.n0;
-    if constexpr (F == kDw) {
-      // part z of the sum over the segment's rows
-      const int per = ((seg.rows + BK - 1) / BK + A.splits - 1) / A.splits * BK;
-      const int first = (int64_t)per * z < seg.rows ? per * z : seg.rows;
-      tile.sum = seg.rows - first < per ? seg.rows - first : per;
-      tile.m_here = (int)A.m_cols - tile.m0;
-      tile.p_row = tile.q_row = seg.first + first;
-      tile.out_row = ((int64_t)z * A.G + g) * A.m_cols + tile.m0;
-    } else {
-      tile.sum = (int)A.sum;
-      tile.m_here = seg.rows - tile.m0;
-      tile.p_row = tile.out_row = seg.first + tile.m0;
-      tile.q_row = (int64_t)g * A.q_rows + (q_is_col(F) ? 0 : tile.n0);
-    }
-    tile = {same64(tile.p_row), same64(tile.q_row), same64(tile.out_row), same(tile.m0),
-            same(tile.n0),      same(tile.m_here),  same(tile.n_here),    same(tile.sum)};
-    return true;
-  };
 
   // What this wave loads: 1 KB pieces of both tiles; byte offsets from P and Q, kOutside past an edge.
   // "row": a piece is 1 KB of rows of BK elements; this lane's row in it and its chunk's place in memory
@@ -290,15 +330,8 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_bf16_kernel(const BfArgs 
       if (i < nk) issue(i, i);
   };
 
-  // The tiles of this workgroup.  Large: one workgroup per compute unit takes tile after tile, and the next
-  // tile's first stages are loaded while the epilogue of the last one writes.  The others: one tile each.
-  const int b = blockIdx.x;
-  auto tile_at = [&](int round) {
-    const int turn = b / kXcds + round * (int)(gridDim.x / kXcds);
-    return (turn / A.chunk * kXcds + b % kXcds) * A.chunk + turn % A.chunk;
-  };
   Tile cur;
-  if (!find(tile_at(0), cur)) return;
+  if (same((int)source(0, cur)) == 0) return;
   begin(cur);
   start();
 
@@ -332,7 +365,7 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_bf16_kernel(const BfArgs 
 
   for (int round = 1;; ++round) {
   Tile next;
-  const bool more = S::kPersistent && same((int)find(tile_at(round), next)) != 0;
+  const bool more = same((int)source(round, next)) != 0;
   v4f acc[FI][FJ];
 #pragma unroll
   for (int i = 0; i < FI; ++i)
@@ -435,8 +468,9 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_bf16_kernel(const BfArgs 
     }
   }
 
-  // (the last stage's barrier has passed: every buffer is free)
   if (more) {
+    // (pinned order: the last stage's barrier has passed, every buffer is free)
+    if (FJ != 4) block_barrier();
     begin(next);
     start();
   }
@@ -539,6 +573,40 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_bf16_kernel(const BfArgs 
   }
 }
 
+}  // namespace
+
+// Large: one workgroup per compute unit takes tile after tile; where the last round would leave half of them
+// without one, its tiles go in quarters.  The other shapes: one tile per workgroup, two workgroups per compute unit.
+template <int F, class S>
+__global__ void __launch_bounds__(S::kThreads, 2) gemm_bf16_kernel(const BfArgs A) {
+  __shared__ __align__(16) uint8_t smem[S::kLdsBytes];
+  const int b = blockIdx.x;
+  auto tile_at = [&](int round) {
+    const int turn = b / kXcds + round * (int)(gridDim.x / kXcds);
+    return (turn / A.chunk * kXcds + b % kXcds) * A.chunk + turn % A.chunk;
+  };
+  if constexpr (S::kPersistent) {
+    const int total = count_tiles<F, S>(A), rest = total % (int)gridDim.x;
+    const bool cut = 2 * rest <= (int)gridDim.x;
+    const int whole = cut ? total - rest : total;
+    run_tiles<F, S>(A, smem, [&](int round, Tile& t) {
+      const int at = tile_at(round);
+      return at < whole && find_tile<F, S>(A, at, t);
+    });
+    if (!cut) return;
+    // (the quarters of a tile on one XCD; one that holds nothing is an empty turn)
+    const int mine = b % kXcds * (int)(gridDim.x / kXcds) + b / kXcds;
+    for (int i = mine; i < 4 * rest; i += gridDim.x) {
+      run_tiles<F, Quarter>(A, smem, [&](int round, Tile& t) {
+        return round == 0 && find_tile<F, S>(A, whole + i / 4, t) && quarter<F, Quarter>(t, i & 3);
+      });
+      block_barrier();
+    }
+  } else {
+    run_tiles<F, S>(A, smem, [&](int round, Tile& t) { return round == 0 && find_tile<F, S>(A, tile_at(0), t); });
+  }
+}
+
 #define FGG_BF16_INFO(name, entry, form, S) \
   {"gemm_bf16_kernel<" name "," #S ">", entry, S::M, S::N, S::K, S::kThreads, S::kStages, S::kStageBytes, 0, \
    S::kLdsBytes, (const void*)gemm_bf16_kernel<form, S>}
@@ -588,9 +656,9 @@ hipError_t launch_shape(BfArgs a, int index, hipStream_t st) {
 
 // The shape whose estimated time is least.  A tile takes its stages (64 deep) one after the other; measured, in
 // microseconds a stage: 1.16 / 0.58 / 0.27 (Large / Medium / Small) where a compute unit has one workgroup, and
-// 1.57 / 0.92 / 0.37 for what it holds (1 / 2 / 2 workgroups) when the chip is full; plus 10 / 5 / 3 to begin and
-// end.  E.g. linear, one segment: 2048^3 50 / 26 / 33 us, 4096 x 2048 x 2048 53 / 36 / 55, 8192^3 803 / 943 /
-// 1520, 256 x 4096 x 4096 87 / 41 / 20.
+// 1.5 / 0.95 / 0.36 for a round of what it holds (1 / 2 / 2 workgroups) when the chip is full; plus 10 / 4 / 2 to
+// begin and end each.  E.g. linear, one segment: 2048^3 50 / 25 / 32 us, 4096 x 2048 x 2048 53 / 36 / 55, 8192^3
+// 791 / 943 / 1520, 256 x 4096 x 4096 87 / 41 / 20.
 struct Plan {
   int shape, splits;   // 0 Large, 1 Medium, 2 Small; parts of the sum
 };
@@ -598,12 +666,18 @@ struct Plan {
 double shape_us(int shape, double tiles, double stages, bool alike) {
   constexpr double kCus = 256.0;
   constexpr double one[3] = {1.16, 0.58, 0.27}, full[3] = {1.5, 0.95, 0.36}, ends[3] = {10.0, 4.0, 2.0};
-  constexpr double ragged[3] = {0.5, 0.9, 0.9};        // of a round, lost to uneven segments
+  constexpr double ragged[3] = {0.3, 0.9, 0.9};        // of a round, lost to uneven segments
   const double slots = shape == 0 ? kCus : 2 * kCus;
   if (tiles <= kCus)
     return stages * (one[shape] + (shape == 0 ? (full[0] - one[0]) * tiles / kCus : 0.0)) + ends[shape] + 1.0;
   double rounds = tiles / slots;
-  rounds = alike ? (double)(int64_t)(rounds + 0.999) : rounds + ragged[shape];
+  if (!alike) {
+    rounds += ragged[shape];
+  } else {
+    const double whole = (double)(int64_t)rounds, rest = rounds - whole;
+    // (Large: a last round of quarters)
+    rounds = whole + (rest == 0.0 ? 0.0 : shape == 0 && rest <= 0.25 ? 0.4 : shape == 0 && rest <= 0.5 ? 0.8 : 1.0);
+  }
   if (rounds < 1.0) rounds = 1.0;
   return rounds * (stages * full[shape] + ends[shape]);
 }

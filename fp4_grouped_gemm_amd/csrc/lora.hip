@@ -352,8 +352,7 @@ lora_expand_kernel(const float* __restrict__ part, int chunks, const int32_t* __
 namespace {
 
 // A launch's shape.  Many tokens: tiles of 32 (64 over B) read each factor less often where tokens share them, and the
-// sum over K is taken whole as soon as the tiles fill the chip.  Few tokens: it is cut so that a wave has about
-// two items, as long as a token's chunks stay few enough to add.
+// sum over K is taken whole as soon as the tiles fill the chip.  Few tokens: it is cut into up to 32 chunks.
 struct LoraPlan {
   int tile, chunk, chunks;     // of the first product
   int tile2, cols;             // of the second
@@ -368,9 +367,7 @@ LoraPlan plan(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K) {
     return n < L ? n : (int64_t)L;
   };
   const int64_t tiles = (T + p.tile - 1) / p.tile, spans = (K + kSpan - 1) / kSpan;
-  int64_t per = (2 * kWaves + distinct(p.tile) - 1) / distinct(p.tile);
-  const int64_t fill = (spans * tiles + 511) / 512;
-  if (per < fill) per = fill;
+  int64_t per = (spans * tiles + 511) / 512;
   if (per < (spans + 31) / 32) per = (spans + 31) / 32;
   if (per > spans) per = spans;
   p.chunk = (int)per * kSpan;
