@@ -44,14 +44,16 @@ __device__ inline int lane_adapter(const int32_t* ids, int64_t t0, int tokens, i
 
 }  // namespace
 
-// This wave's items of a tile: each adapter of the tile with each step of [from, to), dealt to the workgroup's waves
-// in turn.
+// This wave's items of a tile: each adapter of the tile that is this workgroup's (every `parts`-th) with each step of
+// [from, to), dealt to the workgroup's waves in turn.
 struct Items {
   uint64_t left;         // tokens whose adapter is still to come
   uint64_t match;        // the current adapter's tokens
   int cur;               // the current adapter
   int64_t at, from, to;  // current place
   int step, item, wave;
+  int parts, wait;       // workgroups that share the tile's adapters; adapters before this one's next
+  uint64_t mine;         // tokens of this workgroup's adapters so far
 
   // The next item of this wave; false when there is none.
   __device__ bool next(int id) {
@@ -61,6 +63,9 @@ struct Items {
         cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
         match = __ballot(id == cur);
         left &= ~match;
+        if (wait-- > 0) continue;
+        wait = parts - 1;
+        mine |= match;
         at = from - step;
       }
       // (the steps up to the wave's own are passed over at once)
@@ -80,7 +85,7 @@ struct Items {
 
 // part[chunk][t][j] = sum over the chunk's k of x[t][k] A[ids[t]][j][k];  TT tiles of 16 tokens, RT of 16 ranks.
 template <int TT, int RT>
-__global__ void __launch_bounds__(kThreads, TT + RT <= 2 ? 4 : 2)
+__global__ void __launch_bounds__(kThreads, TT + RT <= 2 || (TT == 1 && RT == 4) ? 4 : 2)
 lora_shrink_kernel(const uint16_t* __restrict__ x, int64_t ldx, const int32_t* __restrict__ ids,
                    const uint16_t* __restrict__ a, int64_t T, int L, int r, int64_t K, int chunk,
                    float* __restrict__ part) {
@@ -102,16 +107,16 @@ lora_shrink_kernel(const uint16_t* __restrict__ x, int64_t ldx, const int32_t* _
     v8bf x[TT][kSteps], a[RT][kSteps];
     uint64_t match;
   };
-  auto load = [&](const Items& it, Operands& o) {
+  auto load_a = [&](const Items& it, Operands& o, int i) {
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int64_t k = it.at + 32 * s + 8 * q;
+      const int row = 16 * i + l16;
+      o.a[i][s] = load_or_zero(a + ((int64_t)it.cur * r + row) * K + k, row < r && k < k1);
+    }
+  };
+  auto load_x = [&](const Items& it, Operands& o) {
     o.match = it.match;
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const int64_t k = it.at + 32 * s + 8 * q;
-        const int row = 16 * i + l16;
-        o.a[i][s] = load_or_zero(a + ((int64_t)it.cur * r + row) * K + k, row < r && k < k1);
-      }
 #pragma unroll
     for (int f = 0; f < TT; ++f)
 #pragma unroll
@@ -120,9 +125,14 @@ lora_shrink_kernel(const uint16_t* __restrict__ x, int64_t ldx, const int32_t* _
         o.x[f][s] = load_or_zero(x + (t0 + 16 * f + l16) * ldx + k, (it.match >> (16 * f + l16) & 1) && k < k1);
       }
   };
-  auto use = [&](const Operands& o) {
+  auto load = [&](const Items& it, Operands& o) {
+    load_x(it, o);
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
+    for (int i = 0; i < RT; ++i) load_a(it, o, i);
+  };
+  auto use = [&](const Operands& o, int from, int to) {
+#pragma unroll
+    for (int i = from; i < to; ++i)
 #pragma unroll
       for (int f = 0; f < TT; ++f) {
         v4f d = {0.f, 0.f, 0.f, 0.f};
@@ -133,7 +143,7 @@ lora_shrink_kernel(const uint16_t* __restrict__ x, int64_t ldx, const int32_t* _
         for (int e = 0; e < 4; ++e) sum[i][f][e] += on ? d[e] : 0.0f;
       }
   };
-  Items it = {__ballot(id >= 0), 0, -1, k1, k0, k1, kSpan, kWaves - 1, wave};
+  Items it = {__ballot(id >= 0), 0, -1, k1, k0, k1, kSpan, kWaves - 1, wave, (int)gridDim.z, (int)blockIdx.z, 0};
   if constexpr (TT + RT <= 4) {          // the next item's operands are loaded before this one's are waited for
     Operands o[2];
     bool more = it.next(id);
@@ -141,17 +151,22 @@ lora_shrink_kernel(const uint16_t* __restrict__ x, int64_t ldx, const int32_t* _
     while (more) {
       more = it.next(id);
       if (more) load(it, o[1]);
-      use(o[0]);
+      use(o[0], 0, RT);
       if (!more) break;
       more = it.next(id);
       if (more) load(it, o[0]);
-      use(o[1]);
+      use(o[1], 0, RT);
     }
-  } else {
+  } else {                               // (more would not fit the registers: other waves cover the waits)
     Operands o;
     while (it.next(id)) {
-      load(it, o);
-      use(o);
+      load_x(it, o);
+      load_a(it, o, 0);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        if (i + 1 < RT) load_a(it, o, i + 1);
+        use(o, i, i + 1);
+      }
     }
   }
 
@@ -169,7 +184,7 @@ lora_shrink_kernel(const uint16_t* __restrict__ x, int64_t ldx, const int32_t* _
       float total = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) total += red[w][t][j];
-      if (t0 + t < T && 16 * i + j < r) part[((int64_t)blockIdx.y * T + t0 + t) * r + 16 * i + j] = total;
+      if ((it.mine >> t & 1) && 16 * i + j < r) part[((int64_t)blockIdx.y * T + t0 + t) * r + 16 * i + j] = total;
     }
     __syncthreads();
   }
@@ -259,7 +274,7 @@ lora_expand_kernel(const float* __restrict__ part, int chunks, const int32_t* __
     }
   };
 
-  Items it = {__ballot(id >= 0), 0, -1, n_to, n_from, n_to, kCols, kWaves - 1, wave};
+  Items it = {__ballot(id >= 0), 0, -1, n_to, n_from, n_to, kCols, kWaves - 1, wave, 1, 0, 0};
   Operands o[2];
   bool more = it.next(id);
   if (more) load(it, o[0]);
@@ -354,7 +369,7 @@ namespace {
 // A launch's shape.  Many tokens: tiles of 32 (64 over B) read each factor less often where tokens share them, and the
 // sum over K is taken whole as soon as the tiles fill the chip.  Few tokens: it is cut into up to 32 chunks.
 struct LoraPlan {
-  int tile, chunk, chunks;     // of the first product
+  int tile, chunk, chunks, parts;   // of the first product; workgroups that share a tile's adapters
   int tile2, cols;             // of the second
 };
 
@@ -372,6 +387,10 @@ LoraPlan plan(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K) {
   if (per > spans) per = spans;
   p.chunk = (int)per * kSpan;
   p.chunks = (int)((spans + per - 1) / per);
+  // about one item a wave while there are compute units without a workgroup
+  p.parts = (int)((distinct(p.tile) * per + kWaves - 1) / kWaves);
+  const int64_t most = 256 / (tiles * p.chunks);
+  if (p.parts > most) p.parts = most < 1 ? 1 : (int)most;
 
   const int64_t tiles2 = (T + p.tile2 - 1) / p.tile2, steps = (N + kCols - 1) / kCols;
   int64_t cols = (steps * tiles2 + 511) / 512;
@@ -411,7 +430,7 @@ hipError_t launch_lora(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K, co
                        const int32_t* ids, const uint16_t* a, const uint16_t* b, const float* scales, const void* base,
                        int64_t ldb, void* out, bool f32, int64_t ldo, float* ws, hipStream_t st) {
   const LoraPlan p = plan(T, L, r, N, K);
-  const dim3 g1((unsigned)((T + p.tile - 1) / p.tile), (unsigned)p.chunks);
+  const dim3 g1((unsigned)((T + p.tile - 1) / p.tile), (unsigned)p.chunks, (unsigned)p.parts);
   const int first = (p.tile == 16 ? 0 : 4) + (r <= 16 ? 0 : r <= 32 ? 1 : r <= 64 ? 2 : 3);
   trace_launch(kInfoLora[first], g1, "T=%lld L=%d r=%d K=%lld", (long long)T, L, r, (long long)K);
   auto shrink = [&](auto* kernel) {
