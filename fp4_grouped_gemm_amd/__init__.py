@@ -844,10 +844,12 @@ def lora_add(base, x, ids, a, b, scales=None, out=None, workspace=None):
     _dense(scales, "scales", dev, torch.float32, (L,))
     out, ldo = _rows_out(out, (T, N), base, "out")
     if workspace is None:
-        workspace = torch.empty(lora_workspace_bytes(T, L, r, N, K), dtype=torch.uint8, device=dev)
+        nbytes = lora_workspace_bytes(T, L, r, N, K)
+        if nbytes > 0:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     else:
         _dense(workspace, "workspace", dev, torch.uint8)
     _call("fgg_lora_add", dev, T, L, r, N, K, x.data_ptr(), ldx, ids.data_ptr(), a.data_ptr(), b.data_ptr(),
-          _addr(scales), base.data_ptr(), ldb, out.data_ptr(), _FLOAT[base.dtype], ldo, workspace.data_ptr(),
-          workspace.numel())
+          _addr(scales), base.data_ptr(), ldb, out.data_ptr(), _FLOAT[base.dtype], ldo, _addr(workspace),
+          0 if workspace is None else workspace.numel())
     return out

@@ -763,10 +763,10 @@ fgg_status fgg_lora_add(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K, c
     return FGG_ERR_INVALID_VALUE;
   if (T == 0) return FGG_OK;
   if (base == out && ldb != ldo) return FGG_ERR_INVALID_VALUE;
-  if (!x || !ids || !a || !b || !base || !out || !workspace) return FGG_ERR_INVALID_VALUE;
+  const size_t need = fgg::lora_workspace_bytes(T, L, r, N, K);
+  if (!x || !ids || !a || !b || !base || !out || (need > 0 && !workspace)) return FGG_ERR_INVALID_VALUE;
   if (!aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(base, 16) || !aligned(out, 16) ||
-      !aligned(ids, 4) || !aligned(scales, 4) || !aligned(workspace, 16) ||
-      ws_bytes < fgg::lora_workspace_bytes(T, L, r, N, K))
+      !aligned(ids, 4) || !aligned(scales, 4) || !aligned(workspace, 16) || ws_bytes < need)
     return FGG_ERR_INVALID_VALUE;
   FGG_TRY(device_check(nullptr));
   return finish(fgg::launch_lora(T, L, r, N, K, (const uint16_t*)x, ldx, ids, (const uint16_t*)a, (const uint16_t*)b,

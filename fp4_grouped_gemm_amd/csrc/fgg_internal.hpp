@@ -41,7 +41,7 @@ extern const KernelInfo kInfoQuantE4m3_1x128, kInfoQuantE4m3_128x128, kInfoQuant
     kInfoW4a4Gemm, kInfoMxfp4Gemm, kInfoRoute, kInfoRowsScatter, kInfoRowsCollect, kInfoRowsScatterDot,
     kInfoRowsCollectDot;
 // (kernels with several forms: one entry for each that differs in its workgroup)
-constexpr int kRouteBackwardForms = 7, kGemvForms = 21, kGemmBf16Forms = 15, kLoraForms = 20;
+constexpr int kRouteBackwardForms = 7, kGemvForms = 21, kGemmBf16Forms = 15, kLoraForms = 30;
 extern const KernelInfo kInfoRouteBackward[kRouteBackwardForms], kInfoGemvFp4[kGemvForms],
     kInfoGemmBf16[kGemmBf16Forms], kInfoLora[kLoraForms], kInfoRowsBf16[2],
     kInfoDwJoin[4];

@@ -18,14 +18,15 @@
 //  * the partial sums of the chunks and waves are added in a fixed order.
 #include "fgg_device.hpp"
 #include "fgg_internal.hpp"
+#include "fgg_segments.hpp"
+#include "fgg_wave.hpp"
 
 namespace fgg {
 
 namespace {
 
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
+constexpr int kFewWaves = 16, kFewThreads = 64 * kFewWaves;
 constexpr int kSpan = 128;               // of the sum over K per item
 constexpr int kCols = 32;                // columns per item of the second product
 
@@ -364,6 +365,110 @@ lora_expand_kernel(const float* __restrict__ part, int chunks, const int32_t* __
   }
 }
 
+// Few tokens: one workgroup of sixteen waves takes a token and 1024 columns, and both products (no workspace, one
+// launch).  Each workgroup forms its token's low-rank sums anew: reading A again from the caches costs less than a
+// second launch.  The waves share the sum over K in pieces of 64; a load takes whole 128-byte lines of eight rows
+// of A (a compute unit's cache serves lines, not bytes: the matrix operand's order, half lines of sixteen rows,
+// ran at half the rate), eight lanes a row, whose products meet by lane exchanges.  Then a thread takes a column.
+// RG: groups of eight ranks.
+template <int RG, bool F32>
+__global__ void __launch_bounds__(kFewThreads, 4)
+lora_few_kernel(const uint16_t* __restrict__ x, int64_t ldx, const int32_t* __restrict__ ids,
+                const uint16_t* __restrict__ a, const uint16_t* __restrict__ b, const float* __restrict__ scales,
+                const void* base, int64_t ldb, void* out, int64_t ldo, int L, int r, int64_t N, int64_t K) {
+  __shared__ float red[kFewWaves][8 * RG];
+  __shared__ float vs[8 * RG];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t = blockIdx.y, n = (int64_t)blockIdx.x * kFewThreads + threadIdx.x;
+  const int id = ids[t];
+  const bool has = id >= 0 && id < L;
+  if (!has && out == base) return;
+  float y = 0.0f;
+  if (n < N) y = F32 ? ((const float*)base)[t * ldb + n] : bf16_to_f32(((const uint16_t*)base)[t * ldb + n]);
+  if (has) {
+    float acc[RG];
+#pragma unroll
+    for (int g = 0; g < RG; ++g) acc[g] = 0.0f;
+    const uint16_t* xl = x + t * ldx + 8 * (lane & 7);
+    const uint16_t* al = a + ((int64_t)id * r + (lane >> 3)) * K + 8 * (lane & 7);
+    // kU pieces' loads fly together; ALL: all of them lie inside the sum (else what is past it is zero)
+    constexpr int kU = RG <= 2 ? 4 : RG == 4 ? 3 : RG == 8 ? 2 : 1;
+    auto take = [&](auto all_tag, int64_t p) {
+      constexpr bool ALL = decltype(all_tag)::value;
+      uint4 aw[kU][RG], xw[kU];
+      // (past the sum: some piece inside it, then zeros in its place; ranks past r: the first rows again, dropped)
+      bool on[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        int64_t k = (p + u * kFewWaves) * 64;
+        on[u] = ALL || k + 8 * (lane & 7) < K;
+        if (!on[u]) k = -8 * (lane & 7);
+        xw[u] = *reinterpret_cast<const uint4*>(xl + k);
+#pragma unroll
+        for (int g = 0; g < RG; ++g) aw[u][g] = *reinterpret_cast<const uint4*>(al + (8 * g < r ? 8 * g : 0) * K + k);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (!ALL) {
+        auto keep = [](uint4 v, bool on) { return make_uint4(on ? v.x : 0, on ? v.y : 0, on ? v.z : 0, on ? v.w : 0); };
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          xw[u] = keep(xw[u], on[u]);
+#pragma unroll
+          for (int g = 0; g < RG; ++g) aw[u][g] = keep(aw[u][g], on[u]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const uint32_t xs[4] = {xw[u].x, xw[u].y, xw[u].z, xw[u].w};
+#pragma unroll
+        for (int g = 0; g < RG; ++g) {
+          const uint32_t as[4] = {aw[u][g].x, aw[u][g].y, aw[u][g].z, aw[u][g].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            acc[g] = fmaf(__uint_as_float(as[e] << 16), __uint_as_float(xs[e] << 16), acc[g]);
+            acc[g] = fmaf(__uint_as_float(as[e] & 0xFFFF0000u), __uint_as_float(xs[e] & 0xFFFF0000u), acc[g]);
+          }
+        }
+      }
+    };
+    int64_t p = wave;
+    for (; (p + (kU - 1) * kFewWaves + 1) * 64 <= K; p += kU * kFewWaves) take(std::true_type{}, p);
+    for (; p * 64 < K; p += kU * kFewWaves) take(std::false_type{}, p);
+#pragma unroll
+    for (int g = 0; g < RG; ++g) {
+      float v = acc[g];
+      v += dpp_move<0xB1>(v);              // lane ^ 1, ^ 2, mirror of 8
+      v += dpp_move<0x4E>(v);
+      v += dpp_move<0x141>(v);
+      if ((lane & 7) == 0) red[wave][8 * g + (lane >> 3)] = v;
+    }
+    __syncthreads();
+    if (threadIdx.x < 8 * RG) {
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kFewWaves; ++w) v += red[w][threadIdx.x];
+      vs[threadIdx.x] = scales ? v * scales[id] : v;
+    }
+    __syncthreads();
+    if (n < N) {
+      const uint16_t* bl = b + ((int64_t)id * N + n) * r;
+      float s = 0.0f;
+#pragma unroll 4
+      for (int j = 0; j < r; j += 8) {
+        float w[8];
+        load8<true>(bl, j, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf(vs[j + e], w[e], s);
+      }
+      y += s;
+    }
+  }
+  if (n < N) {
+    if (F32) ((float*)out)[t * ldo + n] = y;
+    else ((uint16_t*)out)[t * ldo + n] = (uint16_t)bf16x2_rne(y, 0.0f);
+  }
+}
+
 namespace {
 
 // A launch's shape.  Many tokens: tiles of 32 (64 over B) read each factor less often where tokens share them, and the
@@ -372,6 +477,17 @@ struct LoraPlan {
   int tile, chunk, chunks, parts;   // of the first product; workgroups that share a tile's adapters
   int tile2, cols;             // of the second
 };
+
+// Whether the one-launch kernel takes the call.  One of its workgroups fills a compute unit for about 1.5 us and
+// the time that A takes at 65 bytes a nanosecond; the two kernels take 10 to 20 us for the token counts in question
+// (captured; the second launch and the workspace cost the host 4 us more).  Measured, one / two launches: 16 tokens
+// of 16 requests, N 4096, K 7168, r 16 6.1 / 10.1 us, K 4096, r 64 12.8 / 12.7; 256 of 32, K 4096, r 16 16.7 / 21;
+// 256 of 2, r 64 43 / 12; 512 of 8, r 16 29 / 13.
+bool few_tokens(int64_t T, int32_t r, int64_t N, int64_t K) {
+  if (T > 65535) return false;
+  const int64_t rounds = (T * ((N + kFewThreads - 1) / kFewThreads) + 255) / 256;
+  return (double)rounds * (1.5 + (double)r * (double)K * 2.0 / 65000.0) <= 15.0;
+}
 
 LoraPlan plan(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K) {
   LoraPlan p;
@@ -408,6 +524,9 @@ LoraPlan plan(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K) {
   {"lora_expand_kernel<" #tt "," #rs "," name ">", "fgg_lora_add", 16 * tt, kCols, 32 * rs, kThreads, 0, 0, \
    (f32 ? 3 : 2) * 16 * tt * (32 * rs + 8) * 2 + kRed(tt, rs), \
    (f32 ? 3 : 2) * 16 * tt * (32 * rs + 8) * 2 + kRed(tt, rs), (const void*)lora_expand_kernel<tt, rs, f32>}
+#define FGG_LORA_FEW(rg, f32, name) \
+  {"lora_few_kernel<" #rg "," name ">", "fgg_lora_add", 1, kFewThreads, 64, kFewThreads, 0, 0, (kFewWaves + 1) * 8 * rg * 4, \
+   (kFewWaves + 1) * 8 * rg * 4, (const void*)lora_few_kernel<rg, f32>}
 // (the runs' sums: only where a tile has fewer quads than threads)
 constexpr int kRed(int tt, int rs) { return 16 * tt * 8 * rs < kThreads ? kThreads * 16 : 0; }
 
@@ -420,18 +539,46 @@ const KernelInfo kInfoLora[kLoraForms] = {
     FGG_LORA_EXPAND(1, 1, true, "f32"), FGG_LORA_EXPAND(1, 2, true, "f32"), FGG_LORA_EXPAND(1, 4, true, "f32"),
     FGG_LORA_EXPAND(4, 1, false, "bf16"), FGG_LORA_EXPAND(4, 2, false, "bf16"), FGG_LORA_EXPAND(4, 4, false, "bf16"),
     FGG_LORA_EXPAND(4, 1, true, "f32"), FGG_LORA_EXPAND(4, 2, true, "f32"), FGG_LORA_EXPAND(4, 4, true, "f32"),
+    FGG_LORA_FEW(1, false, "bf16"), FGG_LORA_FEW(2, false, "bf16"), FGG_LORA_FEW(4, false, "bf16"),
+    FGG_LORA_FEW(8, false, "bf16"), FGG_LORA_FEW(16, false, "bf16"), FGG_LORA_FEW(1, true, "f32"),
+    FGG_LORA_FEW(2, true, "f32"), FGG_LORA_FEW(4, true, "f32"), FGG_LORA_FEW(8, true, "f32"),
+    FGG_LORA_FEW(16, true, "f32"),
 };
 
 size_t lora_workspace_bytes(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K) {
-  return T == 0 ? 0 : (size_t)plan(T, L, r, N, K).chunks * (size_t)T * (size_t)r * 4;
+  return T == 0 || few_tokens(T, r, N, K) ? 0 : (size_t)plan(T, L, r, N, K).chunks * (size_t)T * (size_t)r * 4;
 }
 
 hipError_t launch_lora(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K, const uint16_t* x, int64_t ldx,
                        const int32_t* ids, const uint16_t* a, const uint16_t* b, const float* scales, const void* base,
                        int64_t ldb, void* out, bool f32, int64_t ldo, float* ws, hipStream_t st) {
+  const int ranks = r <= 16 ? 0 : r <= 32 ? 1 : r <= 64 ? 2 : 3;
+  if (few_tokens(T, r, N, K)) {
+    const dim3 grid((unsigned)((N + kFewThreads - 1) / kFewThreads), (unsigned)T);
+    const int form = (f32 ? 5 : 0) + (r <= 8 ? 0 : ranks + 1);
+    trace_launch(kInfoLora[20 + form], grid, "T=%lld L=%d r=%d N=%lld K=%lld", (long long)T, L, r, (long long)N,
+                 (long long)K);
+    auto few = [&](auto* kernel) {
+      hipLaunchKernelGGL(kernel, grid, dim3(kFewThreads), 0, st, x, ldx, ids, a, b, scales, base, ldb, out, ldo, L, r, N,
+                         K);
+    };
+    switch (form) {
+      case 0: few(lora_few_kernel<1, false>); break;
+      case 1: few(lora_few_kernel<2, false>); break;
+      case 2: few(lora_few_kernel<4, false>); break;
+      case 3: few(lora_few_kernel<8, false>); break;
+      case 4: few(lora_few_kernel<16, false>); break;
+      case 5: few(lora_few_kernel<1, true>); break;
+      case 6: few(lora_few_kernel<2, true>); break;
+      case 7: few(lora_few_kernel<4, true>); break;
+      case 8: few(lora_few_kernel<8, true>); break;
+      default: few(lora_few_kernel<16, true>); break;
+    }
+    return hipGetLastError();
+  }
   const LoraPlan p = plan(T, L, r, N, K);
   const dim3 g1((unsigned)((T + p.tile - 1) / p.tile), (unsigned)p.chunks, (unsigned)p.parts);
-  const int first = (p.tile == 16 ? 0 : 4) + (r <= 16 ? 0 : r <= 32 ? 1 : r <= 64 ? 2 : 3);
+  const int first = (p.tile == 16 ? 0 : 4) + ranks;
   trace_launch(kInfoLora[first], g1, "T=%lld L=%d r=%d K=%lld", (long long)T, L, r, (long long)K);
   auto shrink = [&](auto* kernel) {
     hipLaunchKernelGGL(kernel, g1, dim3(kThreads), 0, st, x, ldx, ids, a, T, L, r, K, p.chunk, ws);

@@ -145,11 +145,11 @@ for acc in (False, True):
     for t in (torch.float32, torch.bfloat16):
         fgg.grouped_linear_backward_weight(z(20000, 520), z(20000, 264), 1, accumulate=acc,
                                            out=torch.zeros(1, 520, 264, dtype=t, device="cuda"))
-for T in (4, 600):
-    for r in (8, 32, 64, 128):
+for T, N, K in ((4, 64, 72), (300, 2048, 16384), (5000, 2048, 1032)):
+    for r in (8, 16, 32, 64, 128):
         for t in (torch.float32, torch.bfloat16):
-            fgg.lora_add(torch.zeros(T, 64, dtype=t, device="cuda"), z(T, 72), torch.zeros(T, dtype=torch.int32, device="cuda"),
-                         z(2, r, 72), z(2, 64, r))
+            fgg.lora_add(torch.zeros(T, N, dtype=t, device="cuda"), z(T, K), torch.zeros(T, dtype=torch.int32, device="cuda"),
+                         z(2, r, K), z(2, N, r))
 torch.cuda.synchronize()
 """
     r = subprocess.run([sys.executable, "-c", code], env=dict(os.environ, FGG_DEBUG="1"), capture_output=True, text=True,
@@ -158,5 +158,5 @@ torch.cuda.synchronize()
     seen = {line.split("[fgg] ")[1].split(":")[0] for line in r.stderr.splitlines() if "[fgg] " in line}
     new = [k["kernel"] for k in fgg.kernel_table()
            if k["kernel"].startswith(("gemm_bf16", "rows_bf16", "dw_join", "lora_"))]
-    assert len(new) == 15 + 2 + 4 + 20
+    assert len(new) == 15 + 2 + 4 + 30
     assert not set(new) - seen, sorted(set(new) - seen)

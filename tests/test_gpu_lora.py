@@ -53,7 +53,10 @@ def check(got, base, x, ids, a, b, scales, dtype):
 @pytest.mark.parametrize("T,L,r,N,K", [(1, 1, 8, 8, 8), (1, 3, 16, 264, 4104), (5, 4, 24, 40, 136), (16, 16, 16, 1000, 1992),
                                        (17, 40, 64, 96, 520), (70, 6, 128, 136, 72), (200, 300, 8, 64, 264),
                                        (513, 5, 16, 200, 328), (600, 3, 40, 1032, 136), (530, 9, 128, 72, 264),
-                                       (1300, 64, 32, 72, 40), (2000, 2, 104, 264, 392)])
+                                       (1300, 64, 32, 72, 40), (2000, 2, 104, 264, 392), (300, 5, 16, 2056, 16392),
+                                       (260, 3, 32, 4104, 8200), (300, 40, 64, 2048, 4104), (130, 4, 128, 4104, 4104),
+                                       (3000, 4, 16, 2056, 1032), (2500, 3, 32, 4104, 520), (6000, 7, 64, 1032, 264),
+                                       (1500, 2, 128, 2056, 2056), (4000, 5, 8, 3080, 136)])
 def test_adapters(T, L, r, N, K, dtype, kind):
     base, x, ids, a, b, scales = inputs(T, L, r, N, K, dtype, kind)
     before = base.clone()

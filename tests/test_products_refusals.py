@@ -91,13 +91,21 @@ def lora(T=5, L=3, r=16, N=32, K=48, x=g, ldx=48, ids=g, a=g, b=g, s=None, base=
     (dict(K=(1 << 20) + 8), UNSUPPORTED), (dict(T=(1 << 26) + 1), UNSUPPORTED), (dict(dt=E4M3), UNSUPPORTED),
     (dict(ldx=40), INVALID), (dict(ldx=52), INVALID), (dict(ldb=24), INVALID), (dict(ldo=24), INVALID),
     (dict(ldo=36), INVALID), (dict(x=None), INVALID), (dict(ids=None), INVALID), (dict(a=None), INVALID),
-    (dict(b=None), INVALID), (dict(base=None), INVALID), (dict(out=None), INVALID), (dict(ws=None), INVALID),
+    (dict(b=None), INVALID), (dict(base=None), INVALID), (dict(out=None), INVALID),
     (dict(x=off16), INVALID), (dict(a=off16), INVALID), (dict(b=off16), INVALID), (dict(base=off16), INVALID),
     (dict(out=off16), INVALID), (dict(ids=odd), INVALID), (dict(s=odd), INVALID), (dict(ws=off16), INVALID),
-    (dict(nb=0), INVALID), (dict(out=g, ldo=40), INVALID),
+    (dict(out=g, ldo=40), INVALID),
 ])
 def test_lora(bad, status):
     assert lora(**bad) == status
+
+
+MANY = dict(T=2000, r=64, N=1024, K=4096, ldx=4096, ldb=1024, ldo=1024)
+
+
+@pytest.mark.parametrize("bad", [dict(ws=None), dict(nb=0), dict(ws=off16), dict(nb=2000 * 64 * 4 - 1)])
+def test_lora_of_many_tokens_needs_its_workspace(bad):
+    assert lora(**MANY, **bad) == INVALID
 
 
 def test_lora_nothing_to_do():
@@ -105,7 +113,8 @@ def test_lora_nothing_to_do():
     n = ctypes.c_size_t(1)
     ws = fgg.load_library().fgg_lora_workspace
     assert ws(0, 3, 16, 32, 48, ctypes.byref(n)) == 0 and n.value == 0
-    assert ws(5, 3, 16, 32, 48, ctypes.byref(n)) == 0 and n.value >= 5 * 16 * 4
+    assert ws(5, 3, 16, 32, 48, ctypes.byref(n)) == 0 and n.value == 0        # few tokens: one launch
+    assert ws(2000, 3, 64, 1024, 4096, ctypes.byref(n)) == 0 and n.value >= 2000 * 64 * 4
     assert ws(5, 3, 16, 32, 48, None) == INVALID and ws(5, 3, 12, 32, 48, ctypes.byref(n)) == UNSUPPORTED
 
 
