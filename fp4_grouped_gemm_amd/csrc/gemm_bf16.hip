@@ -498,12 +498,38 @@ __device__ __forceinline__ void run_tiles(const BfArgs& A, uint8_t* smem, Source
     for (int e = 0; e < V / 2; ++e) w[e] = bf16x2_rne(v[2 * e], v[2 * e + 1]);
     __builtin_memcpy(__builtin_assume_aligned((uint16_t*)base + at, 2 * V), w, 2 * V);
   };
-  auto get = [&](const void* base, int64_t at, float* v) {
+  struct Packed {                      // V bf16 values
     uint32_t w[V / 2];
-    __builtin_memcpy(w, __builtin_assume_aligned((const uint16_t*)base + at, 2 * V), 2 * V);
-#pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
   };
+  auto fetch = [&](const void* base, int64_t at) {
+    Packed p;
+    __builtin_memcpy(p.w, __builtin_assume_aligned((const uint16_t*)base + at, 2 * V), 2 * V);
+    return p;
+  };
+  auto unpack = [&](const Packed& p, float* v) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = __uint_as_float(e & 1 ? p.w[e / 2] & 0xFFFF0000u : p.w[e / 2] << 16);
+  };
+  // gated_backward: the pre-activations of kDeep row fragments are under way, where the registers hold them (in a
+  // Large tile they would spill: 538 -> 585 us for 8192 rows of 8 segments, 4096 -> 7168)
+  constexpr int kDeep = F != kGatedBwd || FI == 8 ? 1 : FI < 3 ? FI : 3, kPieces = kAcross / (V / 4);
+  Packed pre[kDeep][kPieces][2];
+  auto fetch_pre = [&](int i) {
+    const int r = 16 * (S::WM * i + wm) + l16_e;
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      const int c = 16 * (kAcross * wn + k * (V / 4)) + c_lane;
+      if (r < cur.m_here && c < cur.n_here) {
+        const int64_t at = (cur.out_row + r) * A.ldh + cur.n0 + c;
+        pre[i % kDeep][k][0] = fetch(A.h, at);
+        pre[i % kDeep][k][1] = fetch(A.h, at + A.n_cols);
+      }
+    }
+  };
+  if constexpr (kDeep > 1) {
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) fetch_pre(i);
+  }
 #pragma unroll
   for (int i = 0; i < FI; ++i) {
     const int r = 16 * (S::WM * i + wm) + l16_e;
@@ -544,8 +570,13 @@ __device__ __forceinline__ void run_tiles(const BfArgs& A, uint8_t* smem, Source
         put(A.out, at, v);
       } else if constexpr (F == kGatedBwd) {
         float gate[V], up[V], dg[V];
-        get(A.h, row * A.ldh + cur.n0 + c, gate);
-        get(A.h, row * A.ldh + cur.n0 + c + A.n_cols, up);
+        if constexpr (kDeep == 1) {
+          const int64_t from = row * A.ldh + cur.n0 + c;
+          pre[0][0][0] = fetch(A.h, from);
+          pre[0][0][1] = fetch(A.h, from + A.n_cols);
+        }
+        unpack(pre[i % kDeep][kDeep == 1 ? 0 : n / (V / 4)][0], gate);
+        unpack(pre[i % kDeep][kDeep == 1 ? 0 : n / (V / 4)][1], up);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           const float s = sigmoid(gate[e]), silu = gate[e] * s;
@@ -559,12 +590,15 @@ __device__ __forceinline__ void run_tiles(const BfArgs& A, uint8_t* smem, Source
       } else {
         if (F == kDw && A.accumulate) {
           float old[V];
-          get(A.out, at, old);
+          unpack(fetch(A.out, at), old);
 #pragma unroll
           for (int e = 0; e < V; ++e) v[e] += old[e];
         }
         put(A.out, at, v);
       }
+    }
+    if constexpr (kDeep > 1) {
+      if (i + kDeep < FI) fetch_pre(i + kDeep);
     }
   }
 
@@ -655,8 +689,8 @@ hipError_t launch_shape(BfArgs a, int index, hipStream_t st) {
 }
 
 // The shape whose estimated time is least.  A tile takes its stages (64 deep) one after the other; measured, in
-// microseconds a stage: 1.16 / 0.58 / 0.27 (Large / Medium / Small) where a compute unit has one workgroup, and
-// 1.5 / 0.95 / 0.36 for a round of what it holds (1 / 2 / 2 workgroups) when the chip is full; plus 10 / 4 / 2 to
+// microseconds a stage: 1.16 / 0.58 to 0.9 / 0.27 (Large / Medium / Small; Medium loads one stage ahead and waits
+// for cold operands) where a compute unit has one workgroup, and 1.5 / 0.95 / 0.37 to 0.42 for a round of what it holds (1 / 2 / 2 workgroups) when the chip is full; plus 10 / 4 / 2 to
 // begin and end each.  E.g. linear, one segment: 2048^3 50 / 25 / 32 us, 4096 x 2048 x 2048 53 / 36 / 55, 8192^3
 // 791 / 943 / 1520, 256 x 4096 x 4096 87 / 41 / 20.
 struct Plan {
@@ -665,7 +699,7 @@ struct Plan {
 
 double shape_us(int shape, double tiles, double stages, bool alike) {
   constexpr double kCus = 256.0;
-  constexpr double one[3] = {1.16, 0.58, 0.27}, full[3] = {1.5, 0.95, 0.36}, ends[3] = {10.0, 4.0, 2.0};
+  constexpr double one[3] = {1.16, 0.72, 0.27}, full[3] = {1.5, 0.95, 0.40}, ends[3] = {10.0, 4.0, 2.0};
   constexpr double ragged[3] = {0.3, 0.9, 0.9};        // of a round, lost to uneven segments
   const double slots = shape == 0 ? kCus : 2 * kCus;
   if (tiles <= kCus)
