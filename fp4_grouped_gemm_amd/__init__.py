@@ -712,11 +712,18 @@ def _segments(offsets, counts, G, dev):
     assert offsets is not None or G == 1, "offsets"
 
 
+def _rows_of(t, name, dtype=None):
+    """_float_rows, with a single row's stride taken as its width (whatever matrix it is a row of)."""
+    ld = _float_rows(t, name, dtype)
+    return ld if t.shape[0] > 1 else t.shape[1]
+
+
 def _bf16_out(out, shape, dtype, dev, name):
     """The given output (checked) or a new one, and its row stride."""
     if out is None:
+        assert dtype in _FLOAT, name
         return torch.empty(shape, dtype=dtype, device=dev), shape[1]
-    ld = _float_rows(out, name)
+    ld = _rows_of(out, name)
     assert out.shape == shape and out.device == dev, name
     return out, ld
 
@@ -725,7 +732,7 @@ def grouped_linear(x, w, offsets=None, counts=None, out=None, out_dtype=torch.bf
     """Rows times their segment's weights (fgg_grouped_linear): x bf16 [M, K] (rows may be strided), w bf16
     [G, N, K], segment g the rows [offsets[g], offsets[g + 1]) (of which the first counts[g]); without
     offsets one segment (G = 1).  Returns [M, N], bf16 or fp32; rows of no segment are left as ``out`` had them."""
-    ldx = _float_rows(x, "x", torch.bfloat16)
+    ldx = _rows_of(x, "x", torch.bfloat16)
     (M, K), dev = x.shape, x.device
     G, N = w.shape[0], w.shape[1]
     _dense(w, "w", dev, torch.bfloat16, (G, N, K))
@@ -739,7 +746,7 @@ def grouped_linear(x, w, offsets=None, counts=None, out=None, out_dtype=torch.bf
 def grouped_linear_backward_input(dy, w, offsets=None, counts=None, out=None, out_dtype=torch.bfloat16):
     """Gradient of grouped_linear's rows (fgg_grouped_linear_backward_input): dy bf16 [M, N], w bf16 [G, N, K];
     returns [M, K], bf16 or fp32, rows of no segment left as ``out`` had them."""
-    lddy = _float_rows(dy, "dy", torch.bfloat16)
+    lddy = _rows_of(dy, "dy", torch.bfloat16)
     (M, N), dev = dy.shape, dy.device
     G, K = w.shape[0], w.shape[2]
     _dense(w, "w", dev, torch.bfloat16, (G, N, K))
@@ -761,12 +768,12 @@ def grouped_linear_backward_weight(dy, x, num_groups, offsets=None, counts=None,
                                    accumulate=False, workspace=None):
     """Gradient of grouped_linear's weights (fgg_grouped_linear_backward_weight): dy bf16 [M, N], x bf16 [M, K];
     returns [G, N, K], fp32 or bf16 (0 for an empty segment); accumulate adds to ``out``."""
-    lddy, ldx = _float_rows(dy, "dy", torch.bfloat16), _float_rows(x, "x", torch.bfloat16)
+    lddy, ldx = _rows_of(dy, "dy", torch.bfloat16), _rows_of(x, "x", torch.bfloat16)
     (M, N), K, dev, G = dy.shape, x.shape[1], dy.device, int(num_groups)
     assert x.shape[0] == M and x.device == dev, "x"
     _segments(offsets, counts, G, dev)
     if out is None:
-        assert not accumulate, "accumulate adds to out"
+        assert not accumulate and out_dtype in _FLOAT, "accumulate adds to out"
         out = torch.empty((G, N, K), dtype=out_dtype, device=dev)
     else:
         assert out.dtype in _FLOAT, "out"
@@ -785,7 +792,7 @@ def grouped_gated(x, w, offsets=None, counts=None, out=None, h=None):
     """The gated block's first half (fgg_grouped_gated): x bf16 [M, K], w bf16 [G, 2I, K] ([gate | up] rows);
     a = silu(gate) * up, bf16 [M, I].  h (bf16 [M, 2I], optional) receives the pre-activations that
     the backward pass needs.  Returns (a, h); rows of no segment are left as they were."""
-    ldx = _float_rows(x, "x", torch.bfloat16)
+    ldx = _rows_of(x, "x", torch.bfloat16)
     (M, K), dev = x.shape, x.device
     G, I = w.shape[0], w.shape[1] // 2
     _dense(w, "w", dev, torch.bfloat16, (G, 2 * I, K))
@@ -794,7 +801,7 @@ def grouped_gated(x, w, offsets=None, counts=None, out=None, h=None):
     assert out.dtype == torch.bfloat16, "out"
     ldh = 0
     if h is not None:
-        ldh = _float_rows(h, "h", torch.bfloat16)
+        ldh = _rows_of(h, "h", torch.bfloat16)
         assert h.shape == (M, 2 * I) and h.device == dev, "h"
     _call("fgg_grouped_gated", dev, G, M, I, K, x.data_ptr(), ldx, w.data_ptr(), _addr(offsets), _addr(counts),
           out.data_ptr(), lda, _addr(h), ldh)
@@ -805,7 +812,7 @@ def grouped_gated_backward(dy, w_down, h, offsets=None, counts=None, out=None, a
     """From the gradient of the block's output to that of its pre-activations (fgg_grouped_gated_backward):
     dy bf16 [M, N], w_down bf16 [G, N, I], h bf16 [M, 2I] from grouped_gated; returns (dh bf16 [M, 2I], a).
     a (bf16 [M, I], optional) receives the activation again, which w_down's gradient needs."""
-    lddy, ldh = _float_rows(dy, "dy", torch.bfloat16), _float_rows(h, "h", torch.bfloat16)
+    lddy, ldh = _rows_of(dy, "dy", torch.bfloat16), _rows_of(h, "h", torch.bfloat16)
     (M, N), dev = dy.shape, dy.device
     G, I = w_down.shape[0], w_down.shape[2]
     _dense(w_down, "w_down", dev, torch.bfloat16, (G, N, I))
@@ -815,7 +822,7 @@ def grouped_gated_backward(dy, w_down, h, offsets=None, counts=None, out=None, a
     assert out.dtype == torch.bfloat16, "out"
     lda = 0
     if a is not None:
-        lda = _float_rows(a, "a", torch.bfloat16)
+        lda = _rows_of(a, "a", torch.bfloat16)
         assert a.shape == (M, I) and a.device == dev, "a"
     _call("fgg_grouped_gated_backward", dev, G, M, I, N, dy.data_ptr(), lddy, w_down.data_ptr(), h.data_ptr(), ldh,
           _addr(offsets), _addr(counts), out.data_ptr(), ldo, _addr(a), lda)
@@ -834,7 +841,7 @@ def lora_add(base, x, ids, a, b, scales=None, out=None, workspace=None):
     """Low-rank adapters beside a shared projection (fgg_lora_add): out[t] = base[t] + scales[i] (x[t] a[i]^T) b[i]^T,
     i = ids[t] (outside [0, L): base[t]).  base [T, N] fp32 or bf16, x bf16 [T, K], ids int32 [T], a bf16 [L, r, K],
     b bf16 [L, N, r], scales fp32 [L].  ``out`` may be ``base`` itself; workspace: lora_workspace_bytes, uint8."""
-    ldb, ldx = _float_rows(base, "base"), _float_rows(x, "x", torch.bfloat16)
+    ldb, ldx = _rows_of(base, "base"), _rows_of(x, "x", torch.bfloat16)
     (T, K), N, dev = x.shape, base.shape[1], x.device
     L, r = a.shape[0], a.shape[1]
     assert base.shape[0] == T and base.device == dev, "base"
@@ -842,7 +849,11 @@ def lora_add(base, x, ids, a, b, scales=None, out=None, workspace=None):
     _dense(a, "a", dev, torch.bfloat16, (L, r, K))
     _dense(b, "b", dev, torch.bfloat16, (L, N, r))
     _dense(scales, "scales", dev, torch.float32, (L,))
-    out, ldo = _rows_out(out, (T, N), base, "out")
+    if out is None:
+        out, ldo = base.new_empty((T, N)), N
+    else:
+        ldo = _rows_of(out, "out", base.dtype)
+        assert out.shape == (T, N) and out.device == dev, "out"
     if workspace is None:
         nbytes = lora_workspace_bytes(T, L, r, N, K)
         if nbytes > 0:

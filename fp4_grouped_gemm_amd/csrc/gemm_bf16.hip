@@ -13,21 +13,28 @@
 // linear and gated row x row, the rows' gradients row x col, the weights' gradient col x col.
 //
 // gfx950 mapping:
-//  * workgroup tile 256 x 256, 64 deep: 8 waves (two per SIMD) of 128 x 64 outputs, 8 x 4
-//    accumulators of v_mfma_f32_16x16x32_bf16.  The n operand is the instruction's first, so a
-//    lane holds four consecutive columns of one row.
-//  * two LDS stages of 64 KB filled by buffer loads straight into LDS, the next one's issued
-//    before the current one is computed.  A buffer descriptor's range check writes zeros for
-//    what lies outside (rows past the segment, columns past the edge, the end of the sum), so
-//    ragged sizes cost no branch in the loop and what lies there never enters a product.
-//  * "row" tiles: 128-byte LDS rows, 16-byte chunk c of row r at chunk c ^ (r & 7): the sixteen
-//    lanes that one cycle of a ds_read_b128 serves hit sixteen different chunks.
-//  * "col" tiles: LDS rows of 256 outputs for one summed index, read by ds_read_b64_tr_b16, which
-//    turns 4 x 16 blocks in the read; 32-byte unit u of row c at u ^ (c & 3 | (c >> 3 & 1) << 2).
-//  * one workgroup per tile; a tile's segment is found by a scan over the segments' row counts
-//    in each wave's lanes (no table, no workspace).  Workgroups are dealt to the 8 XCDs in turn,
-//    and 32 consecutive tiles (8 high, 4 wide) go to one XCD, whose L2 then holds what they share.
-
+//  * v_mfma_f32_16x16x32_bf16 with the n operand first, so a lane holds four consecutive columns of
+//    one row; fp32 accumulators, rounded once.
+//  * three workgroup shapes, chosen by an estimate (plan_rows, plan_dw).  Large: 256 x 256 outputs, 64 deep,
+//    8 waves (two per SIMD) of 128 x 64, two LDS stages of 64 KB; per 64 deep a wave reads 24 KB of LDS for
+//    64 MFMAs, which is what the LDS delivers in the MFMAs' time.  8192^3: 790 us, 1.39 PFLOP/s (row x row;
+//    row x col and col x col within 3 %).  Medium: 128 x 128 by 4 waves, two workgroups per compute unit, for
+//    tiles that would not fill the chip.  Small: 64 x 64, four stages, where time is the sum's latency or
+//    the weights' bytes (16 rows onto 16384 columns, sum 4096: 21 us, 6.4 TB/s).
+//  * stages are filled by buffer loads straight into LDS, the next one's issued before the current one is
+//    computed.  A buffer descriptor's range check writes zeros for what lies outside (rows past the
+//    segment, columns past the edge, the end of the sum), so ragged sizes cost no branch in the loop
+//    and what lies there never enters a product.
+//  * "row" tiles: LDS rows of the tile's depth, 16-byte chunks mixed by row (row_key) so that the sixteen
+//    lanes that one cycle of a ds_read_b128 serves hit sixteen different chunks.  "col" tiles: LDS rows of
+//    the tile's outputs for one summed index, read by ds_read_b64_tr_b16, which turns 4 x 16 blocks in the
+//    read; 32-byte units mixed by row (col_key).
+//  * a tile's segment is found by a scan over the segments' row counts in each wave's lanes (no table, no
+//    workspace).  Workgroups are dealt to the 8 XCDs in turn, and 32 consecutive tiles (8 high, 4 wide)
+//    go to one XCD, whose L2 then holds what they share.
+//  * what bounds the Large shape: the matrix cores at the clock that the card holds under them, and writing:
+//    without its stores the weights' gradient of 8 x 14336 x 4096 in fp32 (1.9 GB) takes 775 us instead of
+//    1170, in every shape alike, so that the stores' 4.7 TB/s do not hide behind the products.
 #include "fgg_device.hpp"
 #include "fgg_internal.hpp"
 #include "fgg_segments.hpp"
@@ -42,31 +49,30 @@ typedef short v8s __attribute__((ext_vector_type(8)));
 constexpr int kXcds = 8, kSM = 8, kChunk = 32;           // tiles of one XCD at a time: 8 high, 4 wide
 constexpr uint32_t kOutside = 0x80000000u;               // offset that the range check rejects
 
-// A workgroup's shape: MxN outputs by WM x WN waves, STAGES buffers of K (32 or 64) deep.
-template <int M_, int N_, int WM_, int WN_, int K_, int STAGES_>
+constexpr int BK = 64;                                   // depth of a stage
+
+// A workgroup's shape: M x N outputs by WM x WN waves, STAGES buffers.
+template <int M_, int N_, int WM_, int WN_, int STAGES_>
 struct Shape {
-  static constexpr int M = M_, N = N_, WM = WM_, WN = WN_, K = K_, kStages = STAGES_;
+  static constexpr int M = M_, N = N_, WM = WM_, WN = WN_, kStages = STAGES_;
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr bool kPersistent = kWaves == 8;
   static constexpr int FI = M / WM / 16, FJ = N / WN / 16;     // a wave's 16 x 16 accumulators
-  static constexpr int kPBytes = M * K * 2, kQBytes = N * K * 2;
+  static constexpr int kPBytes = M * BK * 2, kQBytes = N * BK * 2;
   static constexpr int kQOff = kStages * kPBytes;              // LDS: P stages, then Q stages
   static constexpr int kStageBytes = kPBytes + kQBytes, kLdsBytes = kStages * kStageBytes;
   static constexpr int kPDma = kPBytes / 1024 / kWaves, kQDma = kQBytes / 1024 / kWaves;   // 1 KB loads per wave
 };
-using Large = Shape<256, 256, 2, 4, 64, 2>;
-using Medium = Shape<128, 128, 2, 2, 64, 2>;
-using Small = Shape<64, 64, 2, 2, 64, 4>;
-using Quarter = Shape<128, 128, 2, 4, 64, 4>;            // of a Large tile, by its eight waves
+using Large = Shape<256, 256, 2, 4, 2>;
+using Medium = Shape<128, 128, 2, 2, 2>;
+using Small = Shape<64, 64, 2, 2, 4>;
+using Quarter = Shape<128, 128, 2, 4, 4>;            // of a Large tile, by its eight waves
 static_assert(Quarter::kThreads == Large::kThreads && Quarter::kLdsBytes <= Large::kLdsBytes, "one workgroup");
 
-// "row" tiles: the 16-byte chunk c of row r lies at chunk c ^ row_key(r), such that the sixteen lanes that one
-// cycle of a ds_read_b128 serves (rows 0..3 and 12..15 of one chunk, 4..11 of the next) hit different chunks.
-template <int K>
-__device__ inline int row_key(int r) {
-  const int b = (r >> 2) & 3;
-  return K == 64 ? r & 7 : ((b ^ (b >> 1)) & 1) << 1 | b >> 1;
-}
+// "row" tiles (128-byte LDS rows): the 16-byte chunk c of row r lies at chunk c ^ row_key(r), such that the sixteen
+// lanes that one cycle of a ds_read_b128 serves (rows 0..3 and 12..15 of one chunk, 4..11 of the next) hit
+// different chunks.
+__device__ inline int row_key(int r) { return r & 7; }
 
 enum Form { kLinear, kGated, kDx, kGatedBwd, kDw };
 constexpr bool p_is_col(int f) { return f == kDw; }
@@ -163,7 +169,7 @@ __device__ inline int count_tiles(const BfArgs& A) {
 // Tile t of the launch, segment by segment, in blocks 8 high; false past the last one.
 template <int F, class S>
 __device__ inline bool find_tile(const BfArgs& A, int t, Tile& tile) {
-  constexpr int BM = S::M, BN = S::N, BK = S::K;
+  constexpr int BM = S::M, BN = S::N;
   const int lane = opaque(threadIdx.x & 63);
   int g = 0, j = t, z = 0, mtg = A.m_tiles;
   Segment seg;
@@ -250,7 +256,7 @@ __device__ inline bool quarter(Tile& t, int quad) {
 // tile's first stages are loaded while the epilogue of the last one writes.
 template <int F, class S, class Source>
 __device__ __forceinline__ void run_tiles(const BfArgs& A, uint8_t* smem, Source source) {
-  constexpr int BM = S::M, BN = S::N, BK = S::K, FI = S::FI, FJ = S::FJ;
+  constexpr int BM = S::M, BN = S::N, FI = S::FI, FJ = S::FJ;
   const uint32_t lds_base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -259,7 +265,7 @@ __device__ __forceinline__ void run_tiles(const BfArgs& A, uint8_t* smem, Source
 
   // What this wave loads: 1 KB pieces of both tiles; byte offsets from P and Q, kOutside past an edge.
   // "row": a piece is 1 KB of rows of BK elements; this lane's row in it and its chunk's place in memory
-  const int r_chunk = (lane % (BK / 8)) ^ row_key<BK>(lane / (BK / 8));
+  const int r_chunk = (lane % (BK / 8)) ^ row_key(lane / (BK / 8));
   // "col": a piece is 1 KB of rows of W outputs; this lane's row in it (and, in begin, its first output)
   auto c_row = [&](int W, int piece) { return piece * (512 / W) + lane / (W / 8); };
   uint32_t voff_p[S::kPDma], voff_q[S::kQDma];
@@ -267,7 +273,7 @@ __device__ __forceinline__ void run_tiles(const BfArgs& A, uint8_t* smem, Source
   int sum, nk;
   auto begin = [&](const Tile& t) {
     const int lane = opaque(threadIdx.x & 63);
-    const int r_row = lane / (BK / 8), r_chunk = (lane % (BK / 8)) ^ row_key<BK>(r_row);
+    const int r_row = lane / (BK / 8), r_chunk = (lane % (BK / 8)) ^ row_key(r_row);
     auto c_row = [&](int W, int piece) { return piece * (512 / W) + lane / (W / 8); };
     auto c_col = [&](auto w_tag, int piece) {
       constexpr int W = decltype(w_tag)::value;
@@ -345,8 +351,8 @@ __device__ __forceinline__ void run_tiles(const BfArgs& A, uint8_t* smem, Source
       return tr_read<BM>(base + at + s * 32 * BM * 2);
     } else {
       // (fragments go to the waves in turn, so that a part-filled tile is spread over them)
-      return *reinterpret_cast<const v8bf*>(base + ((16 * wm + l16) * (BK * 2) + (((4 * s + q) ^ row_key<BK>(l16)) << 4)) +
-                                            i * (S::WM * 16 * BK * 2));
+      const int at = (16 * wm + l16) * (BK * 2) + (((4 * s + q) ^ row_key(l16)) << 4);
+      return *reinterpret_cast<const v8bf*>(base + at + i * (S::WM * 16 * BK * 2));
     }
   };
   auto read_q = [&](int stage, int s, int n) -> v8bf {
@@ -358,252 +364,252 @@ __device__ __forceinline__ void run_tiles(const BfArgs& A, uint8_t* smem, Source
       constexpr int kHalf = FJ / 2;
       const int row = (F == kGated ? 16 * kHalf : 16 * FJ) * wn + l16;
       const int further = F == kGated ? n % kHalf * 16 + n / kHalf * (BN / 2) : 16 * n;
-      return *reinterpret_cast<const v8bf*>(base + (row * (BK * 2) + (((4 * s + q) ^ row_key<BK>(l16)) << 4)) +
-                                            further * (BK * 2));
+      const int at = row * (BK * 2) + (((4 * s + q) ^ row_key(l16)) << 4);
+      return *reinterpret_cast<const v8bf*>(base + at + further * (BK * 2));
     }
   };
 
   for (int round = 1;; ++round) {
-  Tile next;
-  const bool more = same((int)source(round, next)) != 0;
-  v4f acc[FI][FJ];
+    Tile next;
+    const bool more = same((int)source(round, next)) != 0;
+    v4f acc[FI][FJ];
 #pragma unroll
-  for (int i = 0; i < FI; ++i)
+    for (int i = 0; i < FI; ++i)
 #pragma unroll
-    for (int n = 0; n < FJ; ++n) acc[i][n] = v4f{0.f, 0.f, 0.f, 0.f};
+      for (int n = 0; n < FJ; ++n) acc[i][n] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  if constexpr (FJ == 4) {
-    // One stage: NG groups (32-deep steps x row fragments) of 4 MFMAs.  A group's row fragment is read
-    // two groups ahead, the column fragments of a stage's second step during its first.  Two groups
-    // before the end every fragment of the stage has been read: there the next stage's loads are
-    // awaited, the waves meet, the stage kStages further goes into this stage's buffers, and the last two
-    // groups read the next stage's first fragments, so that the matrix cores have work while those
-    // reads run.  The order is pinned.  NI: row fragments of each wave that hold rows (a tile that is
-    // at most half full does half the work).
-    constexpr int KS = BK / 32, kAhead = S::kStages - 1;
-    v8bf fp[3], fq[2][4];
-    auto step = [&](auto ni_tag, auto no_tag, int kb) {
-      constexpr int NI = decltype(ni_tag)::value, NG = KS * NI;
-      constexpr int NO = decltype(no_tag)::value;        // kb mod 6
-      constexpr int ST = NO % S::kStages, NEXT = (NO + 1) % S::kStages;
-      constexpr int R = NO * NG % 3;                     // place of the stage's first row fragment in fp
+    if constexpr (FJ == 4) {
+      // One stage: NG groups (two 32-deep steps x row fragments) of 4 MFMAs.  A group's row fragment is read
+      // two groups ahead, the column fragments of the second step during the first.  Two groups before the
+      // end every fragment of the stage has been read: there the next stage's loads are awaited, the
+      // waves meet, the stage kStages further goes into this stage's buffers, and the last two groups read
+      // the next stage's first fragments, so that the matrix cores have work while those reads run.  The
+      // order is pinned.  NI: row fragments of each wave that hold rows (a Large tile that is at most half
+      // full does half the work).
+      constexpr int kAhead = S::kStages - 1;
+      v8bf fp[3], fq[2][4];
+      auto step = [&](auto ni_tag, auto no_tag, int kb) {
+        constexpr int NI = decltype(ni_tag)::value, NG = 2 * NI;
+        constexpr int NO = decltype(no_tag)::value;        // kb mod 6
+        constexpr int ST = NO % S::kStages, NEXT = (NO + 1) % S::kStages;
+        constexpr int R = NO * NG % 3;                     // place of the stage's first row fragment in fp
+        constexpr int kFirstQ = NI == 8 ? 3 : 0;           // group of the second step's first column fragment
 #pragma unroll
-      for (int gi = 0; gi < NG; ++gi) {
-        const int s = gi / NI, i = gi % NI, now = (KS * NO + s) & 1;
-        if (gi == NG - 2) {
-          __builtin_amdgcn_s_waitcnt(kLgkmZero);
-          if (kb + kAhead < nk) wait_vmcnt<(kAhead - 1) * (S::kPDma + S::kQDma)>();
-          else wait_vmcnt<0>();
-          block_barrier();
-          if (kb + S::kStages < nk) issue(kb + S::kStages, ST);
-        }
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[now][n], fp[(R + gi) % 3], acc[i][n], 0, 0, 0);
-          __builtin_amdgcn_sched_barrier(0);
-          const int ahead = gi + 2;                       // (of the next stage in the last two groups)
-          if (n == 0) fp[(R + ahead) % 3] = ahead < NG ? read_p(ST, ahead / NI, ahead % NI) : read_p(NEXT, 0, ahead - NG);
-          if (KS == 2 && n == 2 && s == 0) {
-            if (NI == 8 ? gi >= 3 && gi < 7 : true) fq[now ^ 1][NI == 8 ? gi - 3 : gi] = read_q(ST, 1, NI == 8 ? gi - 3 : gi);
+        for (int gi = 0; gi < NG; ++gi) {
+          const int s = gi / NI, i = gi % NI;
+          if (gi == NG - 2) {
+            __builtin_amdgcn_s_waitcnt(kLgkmZero);
+            if (kb + kAhead < nk) wait_vmcnt<(kAhead - 1) * (S::kPDma + S::kQDma)>();
+            else wait_vmcnt<0>();
+            block_barrier();
+            if (kb + S::kStages < nk) issue(kb + S::kStages, ST);
           }
-          if ((n == 1 || n == 3) && gi >= NG - 2) {
-            const int k = 2 * (gi - NG + 2) + (n >> 1);
-            fq[now ^ 1][k] = read_q(NEXT, 0, k);
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[s][n], fp[(R + gi) % 3], acc[i][n], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            const int ahead = gi + 2;                       // (of the next stage in the last two groups)
+            if (n == 0 && ahead < NG) fp[(R + ahead) % 3] = read_p(ST, ahead / NI, ahead % NI);
+            if (n == 0 && ahead >= NG) fp[(R + ahead) % 3] = read_p(NEXT, 0, ahead - NG);
+            if (n == 2 && gi >= kFirstQ && gi < kFirstQ + 4) fq[1][gi - kFirstQ] = read_q(ST, 1, gi - kFirstQ);
+            if ((n == 1 || n == 3) && gi >= NG - 2) {
+              const int k = 2 * (gi - NG + 2) + (n >> 1);
+              fq[0][k] = read_q(NEXT, 0, k);
+            }
+            __builtin_amdgcn_sched_barrier(0);
           }
-          __builtin_amdgcn_sched_barrier(0);
         }
-      }
-    };
-    auto run = [&](auto ni_tag) {
+      };
+      auto run = [&](auto ni_tag) {
 #pragma unroll
-      for (int n = 0; n < 4; ++n) fq[0][n] = read_q(0, 0, n);
-      fp[0] = read_p(0, 0, 0), fp[1] = read_p(0, 0, 1);
-      for (int kb = 0; kb < nk; kb += 6) {
-        step(ni_tag, std::integral_constant<int, 0>{}, kb);
-        if (kb + 1 < nk) step(ni_tag, std::integral_constant<int, 1>{}, kb + 1);
-        if (kb + 2 < nk) step(ni_tag, std::integral_constant<int, 2>{}, kb + 2);
-        if (kb + 3 < nk) step(ni_tag, std::integral_constant<int, 3>{}, kb + 3);
-        if (kb + 4 < nk) step(ni_tag, std::integral_constant<int, 4>{}, kb + 4);
-        if (kb + 5 < nk) step(ni_tag, std::integral_constant<int, 5>{}, kb + 5);
-      }
-    };
-    if (nk > 0) {
-      // (after the first tile the last one's stores are under way too, in no order with the loads)
-      if (nk >= S::kStages && round == 1) wait_vmcnt<kAhead * (S::kPDma + S::kQDma)>();
-      else wait_vmcnt<0>();
-      block_barrier();
-      if (FI == 8 && cur.m_here <= BM / 2) run(std::integral_constant<int, 4>{});
-      else run(std::integral_constant<int, FI>{});
-    }
-  } else {
-    // The smaller shapes: kStages - 1 stages in flight, several workgroups on a compute unit cover each
-    // other's waits.
-    constexpr int kAhead = S::kStages - 1;
-    auto compute = [&](int stage) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        v8bf fq[FJ], fp[FI];
-#pragma unroll
-        for (int n = 0; n < FJ; ++n) fq[n] = read_q(stage, s, n);
-#pragma unroll
-        for (int i = 0; i < FI; ++i) fp[i] = read_p(stage, s, i);
-#pragma unroll
-        for (int i = 0; i < FI; ++i)
-#pragma unroll
-          for (int n = 0; n < FJ; ++n)
-            acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[n], fp[i], acc[i][n], 0, 0, 0);
-      }
-    };
-    for (int kb = 0; kb < nk; kb += S::kStages) {
-#pragma unroll
-      for (int st = 0; st < S::kStages; ++st) {
-        if (kb + st >= nk) break;
-        // this stage has landed for every wave, and every wave has read the one before
-        if (kb + st + kAhead <= nk) wait_vmcnt<(kAhead - 1) * (S::kPDma + S::kQDma)>();
+        for (int n = 0; n < 4; ++n) fq[0][n] = read_q(0, 0, n);
+        fp[0] = read_p(0, 0, 0), fp[1] = read_p(0, 0, 1);
+        for (int kb = 0; kb < nk; kb += 6) {
+          step(ni_tag, std::integral_constant<int, 0>{}, kb);
+          if (kb + 1 < nk) step(ni_tag, std::integral_constant<int, 1>{}, kb + 1);
+          if (kb + 2 < nk) step(ni_tag, std::integral_constant<int, 2>{}, kb + 2);
+          if (kb + 3 < nk) step(ni_tag, std::integral_constant<int, 3>{}, kb + 3);
+          if (kb + 4 < nk) step(ni_tag, std::integral_constant<int, 4>{}, kb + 4);
+          if (kb + 5 < nk) step(ni_tag, std::integral_constant<int, 5>{}, kb + 5);
+        }
+      };
+      if (nk > 0) {
+        // (after the first tile the last one's stores are under way too, in no order with the loads)
+        if (nk >= S::kStages && round == 1) wait_vmcnt<kAhead * (S::kPDma + S::kQDma)>();
         else wait_vmcnt<0>();
         block_barrier();
-        if (kb + st + kAhead < nk) issue(kb + st + kAhead, (st + kAhead) % S::kStages);
-        compute(st);
+        if (FI == 8 && cur.m_here <= BM / 2) run(std::integral_constant<int, 4>{});
+        else run(std::integral_constant<int, FI>{});
+      }
+    } else {
+      // The smaller shapes: kStages - 1 stages in flight, several workgroups on a compute unit cover each
+      // other's waits.
+      constexpr int kAhead = S::kStages - 1;
+      auto compute = [&](int stage) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          v8bf fq[FJ], fp[FI];
+#pragma unroll
+          for (int n = 0; n < FJ; ++n) fq[n] = read_q(stage, s, n);
+#pragma unroll
+          for (int i = 0; i < FI; ++i) fp[i] = read_p(stage, s, i);
+#pragma unroll
+          for (int i = 0; i < FI; ++i)
+#pragma unroll
+            for (int n = 0; n < FJ; ++n)
+              acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[n], fp[i], acc[i][n], 0, 0, 0);
+        }
+      };
+      for (int kb = 0; kb < nk; kb += S::kStages) {
+#pragma unroll
+        for (int st = 0; st < S::kStages; ++st) {
+          if (kb + st >= nk) break;
+          // this stage has landed for every wave, and every wave has read the one before
+          if (kb + st + kAhead <= nk) wait_vmcnt<(kAhead - 1) * (S::kPDma + S::kQDma)>();
+          else wait_vmcnt<0>();
+          block_barrier();
+          if (kb + st + kAhead < nk) issue(kb + st + kAhead, (st + kAhead) % S::kStages);
+          compute(st);
+        }
       }
     }
-  }
 
-  if (more) {
-    // (pinned order: the last stage's barrier has passed, every buffer is free)
-    if (FJ != 4) block_barrier();
-    begin(next);
-    start();
-  }
+    if (more) {
+      // (pinned order: the last stage's barrier has passed, every buffer is free)
+      if (FJ != 4) block_barrier();
+      begin(next);
+      start();
+    }
 
-  // Outputs.  A lane holds columns 4 q + (0..3) of each fragment for row l16; two neighbouring fragments are
-  // exchanged between lanes 16 apart, so that it holds eight consecutive ones (V) of one of them.
-  constexpr int kAcross = F == kGated ? FJ / 2 : FJ, V = kAcross % 2 == 0 ? 8 : 4;
-  const int lane_e = opaque(lane), l16_e = lane_e & 15, q_e = lane_e >> 4;
-  const int c_lane = V == 8 ? 16 * (q_e & 1) + 8 * (q_e >> 1) : 4 * q_e;
-  auto gather = [&](int i, int n, float* v) {
+    // Outputs.  A lane holds columns 4 q + (0..3) of each fragment for row l16; two neighbouring fragments are
+    // exchanged between lanes 16 apart, so that it holds eight consecutive ones (V) of one of them.
+    constexpr int kAcross = F == kGated ? FJ / 2 : FJ, V = kAcross % 2 == 0 ? 8 : 4;
+    const int lane_e = opaque(lane), l16_e = lane_e & 15, q_e = lane_e >> 4;
+    const int c_lane = V == 8 ? 16 * (q_e & 1) + 8 * (q_e >> 1) : 4 * q_e;
+    auto gather = [&](int i, int n, float* v) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if constexpr (V == 8) {
-        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i][n][e]), __float_as_uint(acc[i][n + 1][e]),
-                                                        false, false);
-        v[e] = __uint_as_float(r[0]), v[4 + e] = __uint_as_float(r[1]);
-      } else {
-        v[e] = acc[i][n][e];
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (V == 8) {
+          const uint32_t a = __float_as_uint(acc[i][n][e]), b = __float_as_uint(acc[i][n + 1][e]);
+          const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+          v[e] = __uint_as_float(r[0]), v[4 + e] = __uint_as_float(r[1]);
+        } else {
+          v[e] = acc[i][n][e];
+        }
       }
-    }
-  };
-  auto put = [&](void* base, int64_t at, const float* v) {      // V values in bf16
-    uint32_t w[V / 2];
+    };
+    auto put = [&](void* base, int64_t at, const float* v) {      // V values in bf16
+      uint32_t w[V / 2];
 #pragma unroll
-    for (int e = 0; e < V / 2; ++e) w[e] = bf16x2_rne(v[2 * e], v[2 * e + 1]);
-    __builtin_memcpy(__builtin_assume_aligned((uint16_t*)base + at, 2 * V), w, 2 * V);
-  };
-  struct Packed {                      // V bf16 values
-    uint32_t w[V / 2];
-  };
-  auto fetch = [&](const void* base, int64_t at) {
-    Packed p;
-    __builtin_memcpy(p.w, __builtin_assume_aligned((const uint16_t*)base + at, 2 * V), 2 * V);
-    return p;
-  };
-  auto unpack = [&](const Packed& p, float* v) {
+      for (int e = 0; e < V / 2; ++e) w[e] = bf16x2_rne(v[2 * e], v[2 * e + 1]);
+      __builtin_memcpy(__builtin_assume_aligned((uint16_t*)base + at, 2 * V), w, 2 * V);
+    };
+    struct Packed {                      // V bf16 values
+      uint32_t w[V / 2];
+    };
+    auto fetch = [&](const void* base, int64_t at) {
+      Packed p;
+      __builtin_memcpy(p.w, __builtin_assume_aligned((const uint16_t*)base + at, 2 * V), 2 * V);
+      return p;
+    };
+    auto unpack = [&](const Packed& p, float* v) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = __uint_as_float(e & 1 ? p.w[e / 2] & 0xFFFF0000u : p.w[e / 2] << 16);
-  };
-  // gated_backward: the pre-activations of kDeep row fragments are under way, where the registers hold them (in a
-  // Large tile they would spill: 538 -> 585 us for 8192 rows of 8 segments, 4096 -> 7168)
-  constexpr int kDeep = F != kGatedBwd || FI == 8 ? 1 : FI < 3 ? FI : 3, kPieces = kAcross / (V / 4);
-  Packed pre[kDeep][kPieces][2];
-  auto fetch_pre = [&](int i) {
-    const int r = 16 * (S::WM * i + wm) + l16_e;
+      for (int e = 0; e < V; ++e) v[e] = __uint_as_float(e & 1 ? p.w[e / 2] & 0xFFFF0000u : p.w[e / 2] << 16);
+    };
+    // gated_backward: the pre-activations of kDeep row fragments are under way, where the registers hold them (in a
+    // Large tile they would spill: 538 -> 585 us for 8192 rows of 8 segments, 4096 -> 7168)
+    constexpr int kDeep = F != kGatedBwd || FI == 8 ? 1 : FI < 3 ? FI : 3, kPieces = kAcross / (V / 4);
+    Packed pre[kDeep][kPieces][2];
+    auto fetch_pre = [&](int i) {
+      const int r = 16 * (S::WM * i + wm) + l16_e;
 #pragma unroll
-    for (int k = 0; k < kPieces; ++k) {
-      const int c = 16 * (kAcross * wn + k * (V / 4)) + c_lane;
-      if (r < cur.m_here && c < cur.n_here) {
-        const int64_t at = (cur.out_row + r) * A.ldh + cur.n0 + c;
-        pre[i % kDeep][k][0] = fetch(A.h, at);
-        pre[i % kDeep][k][1] = fetch(A.h, at + A.n_cols);
+      for (int k = 0; k < kPieces; ++k) {
+        const int c = 16 * (kAcross * wn + k * (V / 4)) + c_lane;
+        if (r < cur.m_here && c < cur.n_here) {
+          const int64_t at = (cur.out_row + r) * A.ldh + cur.n0 + c;
+          pre[i % kDeep][k][0] = fetch(A.h, at);
+          pre[i % kDeep][k][1] = fetch(A.h, at + A.n_cols);
+        }
       }
-    }
-  };
-  if constexpr (kDeep > 1) {
-#pragma unroll
-    for (int i = 0; i < kDeep; ++i) fetch_pre(i);
-  }
-#pragma unroll
-  for (int i = 0; i < FI; ++i) {
-    const int r = 16 * (S::WM * i + wm) + l16_e;
-    const int64_t row = cur.out_row + r;
-#pragma unroll
-    for (int n = 0; n < kAcross; n += V / 4) {
-      if (F != kGated && F != kGatedBwd && A.out_f32) {
-        // four fp32 values are a lane's 16 bytes already
-#pragma unroll
-        for (int k = 0; k < V / 4; ++k) {
-          const int c = 16 * (kAcross * wn + n + k) + 4 * q_e;
-          if (r >= cur.m_here || c >= cur.n_here) continue;
-          float4* o = reinterpret_cast<float4*>((float*)A.out + row * A.ldo + cur.n0 + c);
-          const v4f a = acc[i][n + k];
-          float4 w = make_float4(a[0], a[1], a[2], a[3]);
-          if (F == kDw && A.accumulate) {
-            const float4 old = *o;
-            w.x += old.x, w.y += old.y, w.z += old.z, w.w += old.w;
-          }
-          *o = w;
-        }
-        continue;
-      }
-      const int c = 16 * (kAcross * wn + n) + c_lane;
-      float v[V];
-      gather(i, n, v);                 // (every lane takes part)
-      float u[V];
-      if constexpr (F == kGated) gather(i, n + FJ / 2, u);
-      if (r >= cur.m_here || c >= cur.n_here) continue;
-      const int64_t at = row * A.ldo + cur.n0 + c;
-      if constexpr (F == kGated) {
-        if (A.out2) {
-          put(A.out2, row * A.ldo2 + cur.n0 + c, v);
-          put(A.out2, row * A.ldo2 + cur.n0 + c + A.n_cols, u);
-        }
-#pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = v[e] * sigmoid(v[e]) * u[e];
-        put(A.out, at, v);
-      } else if constexpr (F == kGatedBwd) {
-        float gate[V], up[V], dg[V];
-        if constexpr (kDeep == 1) {
-          const int64_t from = row * A.ldh + cur.n0 + c;
-          pre[0][0][0] = fetch(A.h, from);
-          pre[0][0][1] = fetch(A.h, from + A.n_cols);
-        }
-        unpack(pre[i % kDeep][kDeep == 1 ? 0 : n / (V / 4)][0], gate);
-        unpack(pre[i % kDeep][kDeep == 1 ? 0 : n / (V / 4)][1], up);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float s = sigmoid(gate[e]), silu = gate[e] * s;
-          dg[e] = v[e] * up[e] * fmaf(silu, 1.0f - s, s);
-          v[e] *= silu;
-          up[e] *= silu;
-        }
-        put(A.out, at, dg);
-        put(A.out, at + A.n_cols, v);
-        if (A.out2) put(A.out2, row * A.ldo2 + cur.n0 + c, up);
-      } else {
-        if (F == kDw && A.accumulate) {
-          float old[V];
-          unpack(fetch(A.out, at), old);
-#pragma unroll
-          for (int e = 0; e < V; ++e) v[e] += old[e];
-        }
-        put(A.out, at, v);
-      }
-    }
+    };
     if constexpr (kDeep > 1) {
-      if (i + kDeep < FI) fetch_pre(i + kDeep);
+#pragma unroll
+      for (int i = 0; i < kDeep; ++i) fetch_pre(i);
     }
-  }
+#pragma unroll
+    for (int i = 0; i < FI; ++i) {
+      const int r = 16 * (S::WM * i + wm) + l16_e;
+      const int64_t row = cur.out_row + r;
+#pragma unroll
+      for (int n = 0; n < kAcross; n += V / 4) {
+        if (F != kGated && F != kGatedBwd && A.out_f32) {
+          // four fp32 values are a lane's 16 bytes already
+#pragma unroll
+          for (int k = 0; k < V / 4; ++k) {
+            const int c = 16 * (kAcross * wn + n + k) + 4 * q_e;
+            if (r >= cur.m_here || c >= cur.n_here) continue;
+            float4* o = reinterpret_cast<float4*>((float*)A.out + row * A.ldo + cur.n0 + c);
+            const v4f a = acc[i][n + k];
+            float4 w = make_float4(a[0], a[1], a[2], a[3]);
+            if (F == kDw && A.accumulate) {
+              const float4 old = *o;
+              w.x += old.x, w.y += old.y, w.z += old.z, w.w += old.w;
+            }
+            *o = w;
+          }
+          continue;
+        }
+        const int c = 16 * (kAcross * wn + n) + c_lane;
+        float v[V];
+        gather(i, n, v);                 // (every lane takes part)
+        float u[V];
+        if constexpr (F == kGated) gather(i, n + FJ / 2, u);
+        if (r >= cur.m_here || c >= cur.n_here) continue;
+        const int64_t at = row * A.ldo + cur.n0 + c;
+        if constexpr (F == kGated) {
+          if (A.out2) {
+            put(A.out2, row * A.ldo2 + cur.n0 + c, v);
+            put(A.out2, row * A.ldo2 + cur.n0 + c + A.n_cols, u);
+          }
+#pragma unroll
+          for (int e = 0; e < V; ++e) v[e] = v[e] * sigmoid(v[e]) * u[e];
+          put(A.out, at, v);
+        } else if constexpr (F == kGatedBwd) {
+          float gate[V], up[V], dg[V];
+          if constexpr (kDeep == 1) {
+            const int64_t from = row * A.ldh + cur.n0 + c;
+            pre[0][0][0] = fetch(A.h, from);
+            pre[0][0][1] = fetch(A.h, from + A.n_cols);
+          }
+          unpack(pre[i % kDeep][kDeep == 1 ? 0 : n / (V / 4)][0], gate);
+          unpack(pre[i % kDeep][kDeep == 1 ? 0 : n / (V / 4)][1], up);
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const float s = sigmoid(gate[e]), silu = gate[e] * s;
+            dg[e] = v[e] * up[e] * fmaf(silu, 1.0f - s, s);
+            v[e] *= silu;
+            up[e] *= silu;
+          }
+          put(A.out, at, dg);
+          put(A.out, at + A.n_cols, v);
+          if (A.out2) put(A.out2, row * A.ldo2 + cur.n0 + c, up);
+        } else {
+          if (F == kDw && A.accumulate) {
+            float old[V];
+            unpack(fetch(A.out, at), old);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] += old[e];
+          }
+          put(A.out, at, v);
+        }
+      }
+      if constexpr (kDeep > 1) {
+        if (i + kDeep < FI) fetch_pre(i + kDeep);
+      }
+    }
 
-  if (!more) break;
-  cur = next;
+    if (!more) break;
+    cur = next;
   }
 }
 
@@ -642,7 +648,7 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_bf16_kernel(const BfArgs 
 }
 
 #define FGG_BF16_INFO(name, entry, form, S) \
-  {"gemm_bf16_kernel<" name "," #S ">", entry, S::M, S::N, S::K, S::kThreads, S::kStages, S::kStageBytes, 0, \
+  {"gemm_bf16_kernel<" name "," #S ">", entry, S::M, S::N, BK, S::kThreads, S::kStages, S::kStageBytes, 0, \
    S::kLdsBytes, (const void*)gemm_bf16_kernel<form, S>}
 #define FGG_BF16_SHAPES(name, entry, form) \
   FGG_BF16_INFO(name, entry, form, Large), FGG_BF16_INFO(name, entry, form, Medium), \
@@ -678,7 +684,8 @@ hipError_t launch_shape(BfArgs a, int index, hipStream_t st) {
   a.m_tiles = F == kDw ? (int)up(a.m_cols, S::M) : 0;
   const int64_t tiles = tiles_of<F, S>(a) * a.splits;
   // tiles of one XCD side by side; with few tiles, an eighth of them.  Large: a workgroup per compute unit.
-  const int64_t most = S::kPersistent && a.num_cus / kXcds < kChunk ? (a.num_cus < kXcds ? 1 : a.num_cus / kXcds) : kChunk;
+  int64_t most = kChunk;
+  if (S::kPersistent && a.num_cus / kXcds < kChunk) most = a.num_cus < kXcds ? 1 : a.num_cus / kXcds;
   a.chunk = (int)(tiles >= kXcds * most ? most : up(tiles, kXcds));
   const int64_t round = (int64_t)kXcds * a.chunk;
   const dim3 grid((unsigned)(S::kPersistent ? round : up(tiles, round) * round));
@@ -689,10 +696,11 @@ hipError_t launch_shape(BfArgs a, int index, hipStream_t st) {
 }
 
 // The shape whose estimated time is least.  A tile takes its stages (64 deep) one after the other; measured, in
-// microseconds a stage: 1.16 / 0.58 to 0.9 / 0.27 (Large / Medium / Small; Medium loads one stage ahead and waits
-// for cold operands) where a compute unit has one workgroup, and 1.5 / 0.95 / 0.37 to 0.42 for a round of what it holds (1 / 2 / 2 workgroups) when the chip is full; plus 10 / 4 / 2 to
-// begin and end each.  E.g. linear, one segment: 2048^3 50 / 25 / 32 us, 4096 x 2048 x 2048 53 / 36 / 55, 8192^3
-// 791 / 943 / 1520, 256 x 4096 x 4096 87 / 41 / 20.
+// microseconds a stage (Large / Medium / Small): 1.16 / 0.58 to 0.9 / 0.27 where a compute unit has one workgroup
+// (Medium loads one stage ahead and waits for cold operands), 1.5 / 0.95 / 0.37 to 0.42 for a round of what it
+// holds (1 / 2 / 2 workgroups) when the chip is full; plus 10 / 4 / 2 to begin and end each.  E.g. linear, one
+// segment: 2048^3 50 / 25 / 32 us, 4096 x 2048 x 2048 53 / 36 / 55, 8192^3 791 / 943 / 1520, 256 x 4096 x 4096
+// 87 / 41 / 20.
 struct Plan {
   int shape, splits;   // 0 Large, 1 Medium, 2 Small; parts of the sum
 };
