@@ -101,7 +101,7 @@ int kernel_table(const KernelInfo* const** out) {
   };
   constexpr int kSingle = (int)(sizeof single / sizeof single[0]);
   static const auto table = [] {
-    std::array<const KernelInfo*, kSingle + kRouteBackwardForms + kGemvForms + kGemmBf16Forms + kLoraForms + 6> t{};
+    std::array<const KernelInfo*, kSingle + kRouteBackwardForms + kGemvForms + kGemmBf16Forms + kLoraForms + 7> t{};
     int n = 0;
     for (const KernelInfo* k : single) t[n++] = k;
     for (const KernelInfo& k : kInfoRouteBackward) t[n++] = &k;
@@ -110,6 +110,7 @@ int kernel_table(const KernelInfo* const** out) {
     for (const KernelInfo& k : kInfoLora) t[n++] = &k;
     for (const KernelInfo& k : kInfoRowsBf16) t[n++] = &k;
     for (const KernelInfo& k : kInfoDwJoin) t[n++] = &k;
+    t[n++] = &kInfoLoraTiles;
     return t;
   }();
   *out = table.data();
@@ -759,6 +760,7 @@ fgg_status fgg_lora_add(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K, c
   FGG_TRY(lora_check(T, L, r, N, K));
   if (!float_type(dtype)) return FGG_ERR_UNSUPPORTED;
   const int64_t el = (int64_t)float_size(dtype);
+  if (ldx > fgg::kMaxBf16Width) return FGG_ERR_UNSUPPORTED;   // (32-bit offsets of 64 rows)
   if (ldx < K || ldx % 8 != 0 || ldb < N || ldo < N || ldb * el % 16 != 0 || ldo * el % 16 != 0)
     return FGG_ERR_INVALID_VALUE;
   if (T == 0) return FGG_OK;

@@ -41,10 +41,10 @@ extern const KernelInfo kInfoQuantE4m3_1x128, kInfoQuantE4m3_128x128, kInfoQuant
     kInfoW4a4Gemm, kInfoMxfp4Gemm, kInfoRoute, kInfoRowsScatter, kInfoRowsCollect, kInfoRowsScatterDot,
     kInfoRowsCollectDot;
 // (kernels with several forms: one entry for each that differs in its workgroup)
-constexpr int kRouteBackwardForms = 7, kGemvForms = 21, kGemmBf16Forms = 15, kLoraForms = 30;
+constexpr int kRouteBackwardForms = 7, kGemvForms = 21, kGemmBf16Forms = 15, kLoraForms = 26;
 extern const KernelInfo kInfoRouteBackward[kRouteBackwardForms], kInfoGemvFp4[kGemvForms],
     kInfoGemmBf16[kGemmBf16Forms], kInfoLora[kLoraForms], kInfoRowsBf16[2],
-    kInfoDwJoin[4];
+    kInfoDwJoin[4], kInfoLoraTiles;
 
 enum class QuantKind { E4M3_1x128, E4M3_128x128, E2M1_1x16, E2M1_E8M0_1x32 };
 
@@ -188,6 +188,9 @@ hipError_t launch_grouped_gated_backward(const Segments& s, int64_t I, int64_t N
 hipError_t launch_rows_bf16(const Segments& s, bool gated, int64_t N, int64_t K, const uint16_t* x, int64_t ldx,
                             const uint16_t* w, void* out, bool out_f32, int64_t ldo, uint16_t* h, int64_t ldh,
                             hipStream_t st);
+// The adapters' first product for many tokens, in tiles of 64: part[chunk][T][r] for the tokens that have one.
+hipError_t launch_lora_tiles(int64_t T, int32_t L, int32_t r, int64_t K, const uint16_t* x, int64_t ldx,
+                             const int32_t* ids, const uint16_t* a, int chunk, int chunks, float* part, hipStream_t st);
 // Low-rank adapters: the per-token low-rank sums (workspace: the chunks' fp32 sums), then the result on top of base.
 size_t lora_workspace_bytes(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K);
 hipError_t launch_lora(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K, const uint16_t* x, int64_t ldx,

@@ -74,7 +74,7 @@ static_assert(Quarter::kThreads == Large::kThreads && Quarter::kLdsBytes <= Larg
 // different chunks.
 __device__ inline int row_key(int r) { return r & 7; }
 
-enum Form { kLinear, kGated, kDx, kGatedBwd, kDw };
+enum Form { kLinear, kGated, kDx, kGatedBwd, kDw, kAdapters };
 constexpr bool p_is_col(int f) { return f == kDw; }
 constexpr bool q_is_col(int f) { return f == kDx || f == kGatedBwd || f == kDw; }
 
@@ -138,6 +138,8 @@ struct BfArgs {
   int chunk;                           // consecutive tiles of one XCD
   int num_cus;
   int splits;                          // kDw: parts of the sum, each with its own fp32 result
+  const int32_t* ids;                  // kAdapters: the rows' adapters,
+  int shift;                           // and the columns of one of them in a tile, 2^shift
 };
 
 namespace {
@@ -152,7 +154,12 @@ __device__ inline int64_t same(int64_t v) {
 struct Tile {
   int64_t p_row, q_row, out_row;     // first row of P and Q (of the sum, for "col" operands), of the output
   int m0, n0, m_here, n_here, sum;   // first output row and column in the segment's result; what is left from there
+  int slot[4];                       // kAdapters: the adapters side by side in the tile, -1 for none
 };
+
+__device__ inline int slot_of(const Tile& t, int i) {
+  return i == 0 ? t.slot[0] : i == 1 ? t.slot[1] : i == 2 ? t.slot[2] : t.slot[3];
+}
 
 // Tiles of the whole launch.
 template <int F, class S>
@@ -233,7 +240,7 @@ __device__ inline bool find_tile(const BfArgs& A, int t, Tile& tile) {
     tile.q_row = (int64_t)g * A.q_rows + (q_is_col(F) ? 0 : tile.n0);
   }
   tile = {same(tile.p_row), same(tile.q_row), same(tile.out_row), same(tile.m0),
-          same(tile.n0),    same(tile.m_here), same(tile.n_here), same(tile.sum)};
+          same(tile.n0),    same(tile.m_here), same(tile.n_here), same(tile.sum), {}};
   return true;
 }
 
@@ -306,6 +313,13 @@ __device__ __forceinline__ void run_tiles(const BfArgs& A, uint8_t* smem, Source
       } else {
         int row = piece * (512 / BK) + r_row;
         if (F == kGated) row &= BN / 2 - 1;  // tile rows: gate columns, then the up columns of the same index
+        if constexpr (F == kAdapters) {
+          const int slot = slot_of(t, piece * (512 / BK) >> A.shift);
+          row &= (1 << A.shift) - 1;
+          const uint32_t at = (uint32_t)(A.shift == 6 ? row : slot * (int)A.q_rows + row) * (uint32_t)(A.ldq * 2);
+          voff_q[i] = slot >= 0 && row < t.n_here ? at + r_chunk * 16 : kOutside;
+          continue;
+        }
         voff_q[i] = row < t.n_here ? (uint32_t)row * (uint32_t)(A.ldq * 2) + r_chunk * 16 : kOutside;
       }
     }
@@ -465,6 +479,7 @@ __device__ __forceinline__ void run_tiles(const BfArgs& A, uint8_t* smem, Source
         for (int st = 0; st < S::kStages; ++st) {
           if (kb + st >= nk) break;
           // this stage has landed for every wave, and every wave has read the one before
+          __builtin_amdgcn_s_waitcnt(kLgkmZero);
           if (kb + st + kAhead <= nk) wait_vmcnt<(kAhead - 1) * (S::kPDma + S::kQDma)>();
           else wait_vmcnt<0>();
           block_barrier();
@@ -476,7 +491,10 @@ __device__ __forceinline__ void run_tiles(const BfArgs& A, uint8_t* smem, Source
 
     if (more) {
       // (pinned order: the last stage's barrier has passed, every buffer is free)
-      if (FJ != 4) block_barrier();
+      if (FJ != 4) {
+        __builtin_amdgcn_s_waitcnt(kLgkmZero);
+        block_barrier();
+      }
       begin(next);
       start();
     }
@@ -547,6 +565,13 @@ __device__ __forceinline__ void run_tiles(const BfArgs& A, uint8_t* smem, Source
 #pragma unroll
           for (int k = 0; k < V / 4; ++k) {
             const int c = 16 * (kAcross * wn + n + k) + 4 * q_e;
+            if constexpr (F == kAdapters) {
+              const int j = c & ((1 << A.shift) - 1), slot = slot_of(cur, 16 * (kAcross * wn + n + k) >> A.shift);
+              if (r >= cur.m_here || j >= cur.n_here || slot < 0 || A.ids[row] != slot) continue;
+              const v4f a = acc[i][n + k];
+              *reinterpret_cast<float4*>((float*)A.out + row * A.ldo + cur.n0 + j) = make_float4(a[0], a[1], a[2], a[3]);
+              continue;
+            }
             if (r >= cur.m_here || c >= cur.n_here) continue;
             float4* o = reinterpret_cast<float4*>((float*)A.out + row * A.ldo + cur.n0 + c);
             const v4f a = acc[i][n + k];
@@ -645,6 +670,59 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_bf16_kernel(const BfArgs 
   } else {
     run_tiles<F, S>(A, smem, [&](int round, Tile& t) { return round == 0 && find_tile<F, S>(A, tile_at(0), t); });
   }
+}
+
+// The first product of the adapters of many tokens (see lora.hip): x A^T of a tile of 64 tokens over each adapter among
+// them, of which a token takes its own: part[chunk][t][j] in fp32.  Up to four adapters lie side by side in a tile of
+// 64 columns, 2^shift of them each (8192 tokens of 64 adapters in any order, rank 16, 1024 -> 1024: 98 us, one
+// adapter a tile 148).
+__global__ void __launch_bounds__(Small::kThreads, 2)
+lora_tiles_kernel(const uint16_t* __restrict__ x, int64_t ldx, const int32_t* __restrict__ ids,
+                  const uint16_t* __restrict__ a, int64_t T, int L, int r, int64_t K, int chunk, int shift,
+                  float* part) {
+  __shared__ __align__(16) uint8_t smem[Small::kLdsBytes];
+  const int lane = threadIdx.x & 63;
+  const int64_t t0 = (int64_t)blockIdx.x * Small::M, k0 = (int64_t)blockIdx.y * chunk;
+  BfArgs A{};
+  A.p = x + k0, A.ldp = ldx, A.q = a + k0, A.ldq = K, A.q_rows = r;
+  A.out = part + (int64_t)blockIdx.y * T * r, A.ldo = r, A.out_f32 = 1;
+  A.ids = ids, A.shift = shift;
+  const int sum = (int)(K - k0 < chunk ? K - k0 : chunk), here = (int)(T - t0 < Small::M ? T - t0 : Small::M);
+  int id = lane < here ? ids[t0 + lane] : -1;
+  if (id >= L) id = -1;
+  uint64_t left = __ballot(id >= 0);
+  int slot[4] = {-1, -1, -1, -1}, n0 = r;
+  run_tiles<kAdapters, Small>(A, smem, [&](int, Tile& t) {
+    if (n0 >= r) {                       // the next adapters
+      if (!left) return false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        slot[i] = -1;
+        if (i << shift >= Small::N || !left) continue;
+        slot[i] = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+        left &= ~__ballot(id == slot[i]);
+      }
+      n0 = 0;
+    }
+    t = {t0,     shift == 6 ? (int64_t)slot[0] * r + n0 : 0, t0, 0, n0, here, r - n0, sum,
+         {slot[0], slot[1], slot[2], slot[3]}};
+    n0 += Small::N;
+    return true;
+  });
+}
+
+const KernelInfo kInfoLoraTiles = {"lora_tiles_kernel", "fgg_lora_add", Small::M, Small::N, BK, Small::kThreads,
+                                   Small::kStages, Small::kStageBytes, 0, Small::kLdsBytes,
+                                   (const void*)lora_tiles_kernel};
+
+hipError_t launch_lora_tiles(int64_t T, int32_t L, int32_t r, int64_t K, const uint16_t* x, int64_t ldx,
+                             const int32_t* ids, const uint16_t* a, int chunk, int chunks, float* part, hipStream_t st) {
+  const dim3 grid((unsigned)((T + Small::M - 1) / Small::M), (unsigned)chunks);
+  // (side by side, adapters are 32-bit byte offsets from the first)
+  const int shift = r > 32 || (int64_t)L * r * K >= 1 << 30 ? 6 : r > 16 ? 5 : 4;
+  trace_launch(kInfoLoraTiles, grid, "T=%lld L=%d r=%d K=%lld", (long long)T, L, r, (long long)K);
+  hipLaunchKernelGGL(lora_tiles_kernel, grid, dim3(Small::kThreads), 0, st, x, ldx, ids, a, T, L, r, K, chunk, shift, part);
+  return hipGetLastError();
 }
 
 #define FGG_BF16_INFO(name, entry, form, S) \

@@ -85,28 +85,25 @@ struct Items {
   }
 };
 
-// part[chunk][t][j] = sum over the chunk's k of x[t][k] A[ids[t]][j][k];  TT tiles of 16 tokens, RT of 16 ranks.
-template <int TT, int RT>
-__global__ void __launch_bounds__(kThreads, TT + RT <= 2 || (TT == 1 && RT == 4) ? 4 : 2)
+// part[chunk][t][j] = sum over the chunk's k of x[t][k] A[ids[t]][j][k] for a tile of 16 tokens; RT tiles of 16 ranks.
+template <int RT>
+__global__ void __launch_bounds__(kThreads, RT == 1 || RT == 4 ? 4 : 2)
 lora_shrink_kernel(const uint16_t* __restrict__ x, int64_t ldx, const int32_t* __restrict__ ids,
                    const uint16_t* __restrict__ a, int64_t T, int L, int r, int64_t K, int chunk,
                    float* __restrict__ part) {
-  __shared__ float red[kWaves][16 * TT][16 + 1];
+  __shared__ float red[kWaves][16][16 + 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, q = lane >> 4;
-  const int64_t t0 = (int64_t)blockIdx.x * (16 * TT);
+  const int64_t t0 = (int64_t)blockIdx.x * 16;
   const int64_t k0 = (int64_t)blockIdx.y * chunk, k1 = k0 + chunk < K ? k0 + chunk : K;
-  const int id = lane_adapter(ids, t0, 16 * TT, T, L, lane);
+  const int id = lane_adapter(ids, t0, 16, T, L, lane);
 
-  v4f sum[RT][TT];
+  v4f sum[RT];
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int f = 0; f < TT; ++f) sum[i][f] = v4f{0.f, 0.f, 0.f, 0.f};
-
+  for (int i = 0; i < RT; ++i) sum[i] = v4f{0.f, 0.f, 0.f, 0.f};
   constexpr int kSteps = kSpan / 32;
   struct Operands {
-    v8bf x[TT][kSteps], a[RT][kSteps];
+    v8bf x[kSteps], a[RT][kSteps];
     uint64_t match;
   };
   auto load_a = [&](const Items& it, Operands& o, int i) {
@@ -120,12 +117,10 @@ lora_shrink_kernel(const uint16_t* __restrict__ x, int64_t ldx, const int32_t* _
   auto load_x = [&](const Items& it, Operands& o) {
     o.match = it.match;
 #pragma unroll
-    for (int f = 0; f < TT; ++f)
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const int64_t k = it.at + 32 * s + 8 * q;
-        o.x[f][s] = load_or_zero(x + (t0 + 16 * f + l16) * ldx + k, (it.match >> (16 * f + l16) & 1) && k < k1);
-      }
+    for (int s = 0; s < kSteps; ++s) {
+      const int64_t k = it.at + 32 * s + 8 * q;
+      o.x[s] = load_or_zero(x + (t0 + l16) * ldx + k, (it.match >> l16 & 1) && k < k1);
+    }
   };
   auto load = [&](const Items& it, Operands& o) {
     load_x(it, o);
@@ -134,19 +129,17 @@ lora_shrink_kernel(const uint16_t* __restrict__ x, int64_t ldx, const int32_t* _
   };
   auto use = [&](const Operands& o, int from, int to) {
 #pragma unroll
-    for (int i = from; i < to; ++i)
+    for (int i = from; i < to; ++i) {
+      v4f d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int f = 0; f < TT; ++f) {
-        v4f d = {0.f, 0.f, 0.f, 0.f};
+      for (int s = 0; s < kSteps; ++s) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(o.a[i][s], o.x[s], d, 0, 0, 0);
+      const bool on = o.match >> l16 & 1;
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(o.a[i][s], o.x[f][s], d, 0, 0, 0);
-        const bool on = o.match >> (16 * f + l16) & 1;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sum[i][f][e] += on ? d[e] : 0.0f;
-      }
+      for (int e = 0; e < 4; ++e) sum[i][e] += on ? d[e] : 0.0f;
+    }
   };
   Items it = {__ballot(id >= 0), 0, -1, k1, k0, k1, kSpan, kWaves - 1, wave, (int)gridDim.z, (int)blockIdx.z, 0};
-  if constexpr (TT + RT <= 4) {          // the next item's operands are loaded before this one's are waited for
+  if constexpr (RT <= 2) {               // the next item's operands are loaded before this one's are waited for
     Operands o[2];
     bool more = it.next(id);
     if (more) load(it, o[0]);
@@ -177,12 +170,10 @@ lora_shrink_kernel(const uint16_t* __restrict__ x, int64_t ldx, const int32_t* _
   for (int i = 0; i < RT; ++i) {
     if (16 * i >= r) break;
 #pragma unroll
-    for (int f = 0; f < TT; ++f)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) red[wave][16 * f + l16][4 * q + e] = sum[i][f][e];
+    for (int e = 0; e < 4; ++e) red[wave][l16][4 * q + e] = sum[i][e];
     __syncthreads();
-    for (int v = threadIdx.x; v < 256 * TT; v += kThreads) {
-      const int t = v >> 4, j = v & 15;
+    if (threadIdx.x < 256) {
+      const int t = threadIdx.x >> 4, j = threadIdx.x & 15;
       float total = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) total += red[w][t][j];
@@ -472,8 +463,9 @@ lora_few_kernel(const uint16_t* __restrict__ x, int64_t ldx, const int32_t* __re
 
 namespace {
 
-// A launch's shape.  Many tokens: tiles of 32 (64 over B) read each factor less often where tokens share them, and the
-// sum over K is taken whole as soon as the tiles fill the chip.  Few tokens: it is cut into up to 32 chunks.
+// A launch's shape.  Many tokens (512): tiles of 64, the first product staged through LDS (lora_tiles_kernel, whose
+// loads take whole lines), the sum over K cut so that about 512 workgroups run.  Fewer: tiles of 16, the sum cut into
+// up to 32 chunks, a tile's adapters shared between workgroups.
 struct LoraPlan {
   int tile, chunk, chunks, parts;   // of the first product; workgroups that share a tile's adapters
   int tile2, cols;             // of the second
@@ -492,8 +484,7 @@ bool few_tokens(int64_t T, int32_t r, int64_t N, int64_t K) {
 
 LoraPlan plan(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K) {
   LoraPlan p;
-  p.tile = T < 512 ? 16 : 32;
-  p.tile2 = T < 512 ? 16 : 64;
+  p.tile = p.tile2 = T < 512 ? 16 : 64;
   auto distinct = [&](int64_t tile) {
     const int64_t n = T < tile ? T : tile;
     return n < L ? n : (int64_t)L;
@@ -501,6 +492,7 @@ LoraPlan plan(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K) {
   const int64_t tiles = (T + p.tile - 1) / p.tile, spans = (K + kSpan - 1) / kSpan;
   int64_t per = (spans * tiles + 511) / 512;
   if (per < (spans + 31) / 32) per = (spans + 31) / 32;
+  if (p.tile == 64 && per < 2) per = 2;                // (four stages at least)
   if (per > spans) per = spans;
   p.chunk = (int)per * kSpan;
   p.chunks = (int)((spans + per - 1) / per);
@@ -518,9 +510,9 @@ LoraPlan plan(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K) {
   return p;
 }
 
-#define FGG_LORA_SHRINK(tt, rt) \
-  {"lora_shrink_kernel<" #tt "," #rt ">", "fgg_lora_add", 16 * tt, 16 * rt, kSpan, kThreads, 0, 0, \
-   kWaves * 16 * tt * 17 * 4, kWaves * 16 * tt * 17 * 4, (const void*)lora_shrink_kernel<tt, rt>}
+#define FGG_LORA_SHRINK(rt) \
+  {"lora_shrink_kernel<" #rt ">", "fgg_lora_add", 16, 16 * rt, kSpan, kThreads, 0, 0, kWaves * 16 * 17 * 4, \
+   kWaves * 16 * 17 * 4, (const void*)lora_shrink_kernel<rt>}
 #define FGG_LORA_EXPAND(tt, rs, f32, name) \
   {"lora_expand_kernel<" #tt "," #rs "," name ">", "fgg_lora_add", 16 * tt, kCols, 32 * rs, kThreads, 0, 0, \
    (f32 ? 3 : 2) * 16 * tt * (32 * rs + 8) * 2 + kRed(tt, rs), \
@@ -534,8 +526,7 @@ constexpr int kRed(int tt, int rs) { return 16 * tt * 8 * rs < kThreads ? kThrea
 }  // namespace
 
 const KernelInfo kInfoLora[kLoraForms] = {
-    FGG_LORA_SHRINK(1, 1), FGG_LORA_SHRINK(1, 2), FGG_LORA_SHRINK(1, 4), FGG_LORA_SHRINK(1, 8),
-    FGG_LORA_SHRINK(2, 1), FGG_LORA_SHRINK(2, 2), FGG_LORA_SHRINK(2, 4), FGG_LORA_SHRINK(2, 8),
+    FGG_LORA_SHRINK(1), FGG_LORA_SHRINK(2), FGG_LORA_SHRINK(4), FGG_LORA_SHRINK(8),
     FGG_LORA_EXPAND(1, 1, false, "bf16"), FGG_LORA_EXPAND(1, 2, false, "bf16"), FGG_LORA_EXPAND(1, 4, false, "bf16"),
     FGG_LORA_EXPAND(1, 1, true, "f32"), FGG_LORA_EXPAND(1, 2, true, "f32"), FGG_LORA_EXPAND(1, 4, true, "f32"),
     FGG_LORA_EXPAND(4, 1, false, "bf16"), FGG_LORA_EXPAND(4, 2, false, "bf16"), FGG_LORA_EXPAND(4, 4, false, "bf16"),
@@ -557,7 +548,7 @@ hipError_t launch_lora(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K, co
   if (few_tokens(T, r, N, K)) {
     const dim3 grid((unsigned)((N + kFewThreads - 1) / kFewThreads), (unsigned)T);
     const int form = (f32 ? 5 : 0) + (r <= 8 ? 0 : ranks + 1);
-    trace_launch(kInfoLora[20 + form], grid, "T=%lld L=%d r=%d N=%lld K=%lld", (long long)T, L, r, (long long)N,
+    trace_launch(kInfoLora[16 + form], grid, "T=%lld L=%d r=%d N=%lld K=%lld", (long long)T, L, r, (long long)N,
                  (long long)K);
     auto few = [&](auto* kernel) {
       hipLaunchKernelGGL(kernel, grid, dim3(kFewThreads), 0, st, x, ldx, ids, a, b, scales, base, ldb, out, ldo, L, r,
@@ -578,27 +569,27 @@ hipError_t launch_lora(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K, co
     return hipGetLastError();
   }
   const LoraPlan p = plan(T, L, r, N, K);
-  const dim3 g1((unsigned)((T + p.tile - 1) / p.tile), (unsigned)p.chunks, (unsigned)p.parts);
-  const int first = (p.tile == 16 ? 0 : 4) + ranks;
-  trace_launch(kInfoLora[first], g1, "T=%lld L=%d r=%d K=%lld", (long long)T, L, r, (long long)K);
-  auto shrink = [&](auto* kernel) {
-    hipLaunchKernelGGL(kernel, g1, dim3(kThreads), 0, st, x, ldx, ids, a, T, L, r, K, p.chunk, ws);
-  };
-  switch (first) {
-    case 0: shrink(lora_shrink_kernel<1, 1>); break;
-    case 1: shrink(lora_shrink_kernel<1, 2>); break;
-    case 2: shrink(lora_shrink_kernel<1, 4>); break;
-    case 3: shrink(lora_shrink_kernel<1, 8>); break;
-    case 4: shrink(lora_shrink_kernel<2, 1>); break;
-    case 5: shrink(lora_shrink_kernel<2, 2>); break;
-    case 6: shrink(lora_shrink_kernel<2, 4>); break;
-    default: shrink(lora_shrink_kernel<2, 8>); break;
+  if (p.tile == 64) {
+    const hipError_t e = launch_lora_tiles(T, L, r, K, x, ldx, ids, a, p.chunk, p.chunks, ws, st);
+    if (e != hipSuccess) return e;
+  } else {
+    const dim3 grid((unsigned)((T + p.tile - 1) / p.tile), (unsigned)p.chunks, (unsigned)p.parts);
+    trace_launch(kInfoLora[ranks], grid, "T=%lld L=%d r=%d K=%lld", (long long)T, L, r, (long long)K);
+    auto shrink = [&](auto* kernel) {
+      hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, st, x, ldx, ids, a, T, L, r, K, p.chunk, ws);
+    };
+    switch (ranks) {
+      case 0: shrink(lora_shrink_kernel<1>); break;
+      case 1: shrink(lora_shrink_kernel<2>); break;
+      case 2: shrink(lora_shrink_kernel<4>); break;
+      default: shrink(lora_shrink_kernel<8>); break;
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
   const dim3 g2((unsigned)((T + p.tile2 - 1) / p.tile2), (unsigned)((N + p.cols - 1) / p.cols));
   const int second = (p.tile2 == 16 ? 0 : 6) + (f32 ? 3 : 0) + (r <= 32 ? 0 : r <= 64 ? 1 : 2);
-  trace_launch(kInfoLora[8 + second], g2, "T=%lld L=%d r=%d N=%lld", (long long)T, L, r, (long long)N);
+  trace_launch(kInfoLora[4 + second], g2, "T=%lld L=%d r=%d N=%lld", (long long)T, L, r, (long long)N);
   auto expand = [&](auto* kernel) {
     hipLaunchKernelGGL(kernel, g2, dim3(kThreads), 0, st, ws, p.chunks, ids, b, scales, base, ldb, out, ldo, T, L, r,
                        N, p.cols);

@@ -605,7 +605,7 @@ fgg_status fgg_grouped_gated_backward(int32_t G, int64_t M, int64_t I, int64_t N
  * x: bf16 [T][ldx], ids: [T] int32, a: bf16 [L][r][K], b: bf16 [L][N][r], scales: fp32 [L] or NULL (1);
  * base, out: [T][ldb], [T][ldo] of dtype (FGG_BF16 or FGG_F32); out may be base itself (same pointer
  * and stride), else it must not overlap an input.  Base pointers are 16-byte aligned and row strides
- * whole 16-byte pieces; N, K and r are multiples of 8, r <= 128, N, K <= 2^20, T <= 2^26
+ * whole 16-byte pieces; N, K and r are multiples of 8, r <= 128, N, K <= 2^20, ldx < 2^22, T <= 2^26
  * (FGG_ERR_UNSUPPORTED beyond).  workspace: fgg_lora_workspace bytes, 16-byte aligned (0 for few
  * tokens: may be NULL); its contents need not be kept or cleared, and calls that may overlap in time
  * need one each.  T == 0 is a no-op.

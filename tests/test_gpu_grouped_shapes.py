@@ -158,5 +158,5 @@ torch.cuda.synchronize()
     seen = {line.split("[fgg] ")[1].split(":")[0] for line in r.stderr.splitlines() if "[fgg] " in line}
     new = [k["kernel"] for k in fgg.kernel_table()
            if k["kernel"].startswith(("gemm_bf16", "rows_bf16", "dw_join", "lora_"))]
-    assert len(new) == 15 + 2 + 4 + 30
+    assert len(new) == 15 + 2 + 4 + 27
     assert not set(new) - seen, sorted(set(new) - seen)

@@ -89,3 +89,11 @@ def test_nan_stays_with_its_token_and_adapter(T):
     assert torch.equal(got[apart], clean[apart])
     assert got[ids == 1].isnan().all() and got[4].isnan().all()
     assert not got[ids == 2].isfinite().any()
+
+
+@pytest.mark.parametrize("L,r,K", [(2100, 16, 32768), (2040, 16, 32768), (1030, 24, 65536)])
+def test_factors_past_32_bit_offsets(L, r, K):
+    # (2 GiB of factors and just less, read as one array, by tokens whose adapters lie anywhere in it)
+    base, x, ids, a, b, scales = inputs(600, L, r, 40, K, F32, "any", 3)
+    ids[-1], ids[-2] = L - 1, 0
+    check(fgg.lora_add(base, x, ids, a, b, scales), base, x, ids, a, b, scales, F32)
