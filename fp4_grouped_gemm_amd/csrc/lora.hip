@@ -3,9 +3,10 @@
 //   out[t] = base[t] + scales[i] (x[t] A_i^T) B_i^T,   i = ids[t];   out[t] = base[t] without an adapter
 //
 // Few tokens: one kernel for both products (lora_few_kernel).  Else two: x A^T into fp32 sums per token (the sum over
-// K cut into chunks, a workgroup per chunk and tile of tokens), and the product with B on top of base.  What bounds
-// them is memory: every adapter's factors once, x, base and out (8192 tokens of prompts, rank 64, 4096 -> 4096: 65 us
-// for 210 MB; 16 tokens of 16 requests, rank 16, 7168 -> 4096: 6 us for 5 MB).
+// K cut into chunks, a workgroup per chunk and tile of tokens; lora_shrink_kernel, for many tokens lora_tiles_kernel),
+// and the product with B on top of base (lora_expand_kernel).  What bounds them is memory: every adapter's factors once, x,
+// base and out (8192 tokens of 8 prompts, rank 64, 4096 -> 4096: 50 us for 210 MB; 16 tokens of 16 requests, rank 16,
+// 7168 -> 4096: 6 us for 5 MB).
 //
 //  * tokens come in any order, in tiles of 16 to 64.  A wave finds the tile's distinct adapters by
 //    ballots over the tokens' ids; the work is cut into items of one adapter and one piece of the
@@ -464,8 +465,10 @@ lora_few_kernel(const uint16_t* __restrict__ x, int64_t ldx, const int32_t* __re
 namespace {
 
 // A launch's shape.  Many tokens (512): tiles of 64, the first product staged through LDS (lora_tiles_kernel, whose
-// loads take whole lines), the sum over K cut so that about 512 workgroups run.  Fewer: tiles of 16, the sum cut into
-// up to 32 chunks, a tile's adapters shared between workgroups.
+// loads take whole lines), the sum over K cut so that about 512 workgroups run (operands from memory, 8192 tokens of 8
+// runs, rank 64: 84 us, with 256 workgroups 85 to 94).  Fewer: tiles of 16, the sum cut into up to 32 chunks, a tile's
+// adapters shared between workgroups.  The second product: 512 workgroups (8192 tokens of 8 runs, rank 64, replayed:
+// 50 us; with 256 55, with 1024 53).
 struct LoraPlan {
   int tile, chunk, chunks, parts;   // of the first product; workgroups that share a tile's adapters
   int tile2, cols;             // of the second
