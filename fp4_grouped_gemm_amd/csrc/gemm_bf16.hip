@@ -665,6 +665,7 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_bf16_kernel(const BfArgs 
       run_tiles<F, Quarter>(A, smem, [&](int round, Tile& t) {
         return round == 0 && find_tile<F, S>(A, whole + i / 4, t) && quarter<F, Quarter>(t, i & 3);
       });
+      __builtin_amdgcn_s_waitcnt(kLgkmZero);
       block_barrier();
     }
   } else {
