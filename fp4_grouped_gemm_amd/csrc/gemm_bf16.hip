@@ -675,7 +675,8 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_bf16_kernel(const BfArgs 
 
 // The first product of the adapters of many tokens (see lora.hip): x A^T of a tile of 64 tokens over each adapter among
 // them, of which a token takes its own: part[chunk][t][j] in fp32.  Up to four adapters lie side by side in a tile of
-// 64 columns, 2^shift of them each (8192 tokens of 64 adapters in any order, rank 16, 1024 -> 1024: 98 us, one
+// 64 columns, 2^shift of them each; of more than 64 ranks two workgroups take half each where the chip is not full
+// (651 tokens of 8 runs, rank 128, 456 -> 664: 17 us, both halves in one 28) (8192 tokens of 64 adapters in any order, rank 16, 1024 -> 1024: 98 us, one
 // adapter a tile 148).
 __global__ void __launch_bounds__(Small::kThreads, 2)
 lora_tiles_kernel(const uint16_t* __restrict__ x, int64_t ldx, const int32_t* __restrict__ ids,
@@ -703,11 +704,11 @@ lora_tiles_kernel(const uint16_t* __restrict__ x, int64_t ldx, const int32_t* __
         slot[i] = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
         left &= ~__ballot(id == slot[i]);
       }
-      n0 = 0;
+      n0 = Small::N * blockIdx.z;
     }
     t = {t0,     shift == 6 ? (int64_t)slot[0] * r + n0 : 0, t0, 0, n0, here, r - n0, sum,
          {slot[0], slot[1], slot[2], slot[3]}};
-    n0 += Small::N;
+    n0 += Small::N * gridDim.z;
     return true;
   });
 }
@@ -718,7 +719,8 @@ const KernelInfo kInfoLoraTiles = {"lora_tiles_kernel", "fgg_lora_add", Small::M
 
 hipError_t launch_lora_tiles(int64_t T, int32_t L, int32_t r, int64_t K, const uint16_t* x, int64_t ldx,
                              const int32_t* ids, const uint16_t* a, int chunk, int chunks, float* part, hipStream_t st) {
-  const dim3 grid((unsigned)((T + Small::M - 1) / Small::M), (unsigned)chunks);
+  const int64_t tiles = (T + Small::M - 1) / Small::M;
+  const dim3 grid((unsigned)tiles, (unsigned)chunks, r > Small::N && tiles * chunks < 256 ? 2 : 1);
   // (side by side, adapters are 32-bit byte offsets from the first)
   const int shift = r > 32 || (int64_t)L * r * K >= 1 << 30 ? 6 : r > 16 ? 5 : 4;
   trace_launch(kInfoLoraTiles, grid, "T=%lld L=%d r=%d K=%lld", (long long)T, L, r, (long long)K);

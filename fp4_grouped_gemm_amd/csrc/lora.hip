@@ -474,15 +474,16 @@ struct LoraPlan {
   int tile2, cols;             // of the second
 };
 
-// Whether the one-launch kernel takes the call.  One of its workgroups fills a compute unit for about 1.5 us and
-// the time that A takes at 65 bytes a nanosecond; the two kernels take 10 to 20 us for the token counts in question
-// (captured; the second launch and the workspace cost the host 4 us more).  Measured, one / two launches: 16 tokens
-// of 16 requests, N 4096, K 7168, r 16 6.1 / 10.1 us, K 4096, r 64 12.8 / 12.7; 256 of 32, K 4096, r 16 16.7 / 21;
-// 256 of 2, r 64 43 / 12; 512 of 8, r 16 29 / 13.
+// Whether the one-launch kernel takes the call.  One of its workgroups fills a compute unit for about 1.5 us, the
+// time that A takes at 65 bytes a nanosecond, and 0.053 us a rank for the rows of B, of which a lane has one; the two
+// kernels take 10 to 20 us for the token counts in question (captured; the second launch and the workspace cost the
+// host 4 us more).  Measured, one / two launches: 16 tokens of 16 requests, N 4096, K 7168, r 16 6.1 / 10.1 us, K 4096,
+// r 64 12.8 / 12.7; 256 of 32, K 4096, r 16 16.7 / 21; 256 of 2, r 64 43 / 12; 512 of 8, r 16 29 / 13; 168 of 6, N
+// 6104, K 104, r 64 25 / 17.
 bool few_tokens(int64_t T, int32_t r, int64_t N, int64_t K) {
   if (T > 65535) return false;
   const int64_t rounds = (T * ((N + kFewThreads - 1) / kFewThreads) + 255) / 256;
-  return (double)rounds * (1.5 + (double)r * (double)K * 2.0 / 65000.0) <= 15.0;
+  return (double)rounds * (1.5 + (double)r * ((double)K * 2.0 / 65000.0 + 0.053)) <= 18.0;
 }
 
 LoraPlan plan(int64_t T, int32_t L, int32_t r, int64_t N, int64_t K) {
