@@ -569,7 +569,8 @@ __device__ __forceinline__ void run_tiles(const BfArgs& A, uint8_t* smem, Source
               const int j = c & ((1 << A.shift) - 1), slot = slot_of(cur, 16 * (kAcross * wn + n + k) >> A.shift);
               if (r >= cur.m_here || j >= cur.n_here || slot < 0 || A.ids[row] != slot) continue;
               const v4f a = acc[i][n + k];
-              *reinterpret_cast<float4*>((float*)A.out + row * A.ldo + cur.n0 + j) = make_float4(a[0], a[1], a[2], a[3]);
+              float4* o = reinterpret_cast<float4*>((float*)A.out + row * A.ldo + cur.n0 + j);
+              *o = make_float4(a[0], a[1], a[2], a[3]);
               continue;
             }
             if (r >= cur.m_here || c >= cur.n_here) continue;
@@ -675,9 +676,9 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_bf16_kernel(const BfArgs 
 
 // The first product of the adapters of many tokens (see lora.hip): x A^T of a tile of 64 tokens over each adapter among
 // them, of which a token takes its own: part[chunk][t][j] in fp32.  Up to four adapters lie side by side in a tile of
-// 64 columns, 2^shift of them each; of more than 64 ranks two workgroups take half each where the chip is not full
-// (651 tokens of 8 runs, rank 128, 456 -> 664: 17 us, both halves in one 28) (8192 tokens of 64 adapters in any order, rank 16, 1024 -> 1024: 98 us, one
-// adapter a tile 148).
+// 64 columns, 2^shift of them each (8192 tokens of 64 adapters in any order, rank 16, 1024 -> 1024: 98 us, one adapter
+// a tile 148); of more than 64 ranks two workgroups take half each where the chip is not full (651 tokens of 8 runs,
+// rank 128, 456 -> 664: 17 us, both halves in one 28).
 __global__ void __launch_bounds__(Small::kThreads, 2)
 lora_tiles_kernel(const uint16_t* __restrict__ x, int64_t ldx, const int32_t* __restrict__ ids,
                   const uint16_t* __restrict__ a, int64_t T, int L, int r, int64_t K, int chunk, int shift,
@@ -724,7 +725,8 @@ hipError_t launch_lora_tiles(int64_t T, int32_t L, int32_t r, int64_t K, const u
   // (side by side, adapters are 32-bit byte offsets from the first)
   const int shift = r > 32 || (int64_t)L * r * K >= 1 << 30 ? 6 : r > 16 ? 5 : 4;
   trace_launch(kInfoLoraTiles, grid, "T=%lld L=%d r=%d K=%lld", (long long)T, L, r, (long long)K);
-  hipLaunchKernelGGL(lora_tiles_kernel, grid, dim3(Small::kThreads), 0, st, x, ldx, ids, a, T, L, r, K, chunk, shift, part);
+  hipLaunchKernelGGL(lora_tiles_kernel, grid, dim3(Small::kThreads), 0, st, x, ldx, ids, a, T, L, r, K, chunk, shift,
+                     part);
   return hipGetLastError();
 }
 

@@ -4,9 +4,9 @@
 //
 // Few tokens: one kernel for both products (lora_few_kernel).  Else two: x A^T into fp32 sums per token (the sum over
 // K cut into chunks, a workgroup per chunk and tile of tokens; lora_shrink_kernel, for many tokens lora_tiles_kernel),
-// and the product with B on top of base (lora_expand_kernel).  What bounds them is memory: every adapter's factors once, x,
-// base and out (8192 tokens of 8 prompts, rank 64, 4096 -> 4096: 50 us for 210 MB; 16 tokens of 16 requests, rank 16,
-// 7168 -> 4096: 6 us for 5 MB).
+// and the product with B on top of base (lora_expand_kernel).  What bounds them is memory: every adapter's factors
+// once, x, base and out (8192 tokens of 8 prompts, rank 64, 4096 -> 4096: 50 us for 210 MB; 16 tokens of 16 requests,
+// rank 16, 7168 -> 4096: 6 us for 5 MB).
 //
 //  * tokens come in any order, in tiles of 16 to 64.  A wave finds the tile's distinct adapters by
 //    ballots over the tokens' ids; the work is cut into items of one adapter and one piece of the
@@ -478,8 +478,8 @@ struct LoraPlan {
 // time that A takes at 65 bytes a nanosecond, and 0.053 us a rank for the rows of B, of which a lane has one; the two
 // kernels take 10 to 20 us for the token counts in question (captured; the second launch and the workspace cost the
 // host 4 us more).  Measured, one / two launches: 16 tokens of 16 requests, N 4096, K 7168, r 16 6.1 / 10.1 us, K 4096,
-// r 64 12.8 / 12.7; 256 of 32, K 4096, r 16 16.7 / 21; 256 of 2, r 64 43 / 12; 512 of 8, r 16 29 / 13; 168 of 6, N
-// 6104, K 104, r 64 25 / 17.
+// r 64 12.8 / 12.7; 256 of 32, K 4096, r 16 16.7 / 21; 256 of 2, r 64 43 / 12; 512 of 8, r 16 29 / 13; 168 of 6,
+// N 6104, K 104, r 64 25 / 17.
 bool few_tokens(int64_t T, int32_t r, int64_t N, int64_t K) {
   if (T > 65535) return false;
   const int64_t rounds = (T * ((N + kFewThreads - 1) / kFewThreads) + 255) / 256;
