@@ -179,7 +179,10 @@ __device__ inline void load8(const void* base, int64_t idx, float* f) {
 // The LDS destination is M0 (+ 16 or 4 bytes per lane, consecutive lanes consecutive);
 // M0 is saved and restored around the load.  The source is a wave-uniform base (an
 // SGPR pair) plus a per-lane 32-bit offset.  Their completion is counted in vmcnt like
-// any vector-memory load.
+// any vector-memory load.  The hardware asks for a wait state between the write of M0 and the
+// load, and for five between a vector instruction's write of the base (v_readfirstlane) and
+// the load; the compiler adds none inside an asm, so s_nop 2 (three) stands there: with the
+// two moves before it that is five.
 
 // 16 bytes per lane from sbase + voff into LDS at m0 + 16 * lane.
 __device__ inline void dma16(const void* sbase, uint32_t voff, uint32_t lds) {
@@ -187,6 +190,7 @@ __device__ inline void dma16(const void* sbase, uint32_t voff, uint32_t lds) {
   asm volatile(
       "s_mov_b32 %0, m0\n\t"
       "s_mov_b32 m0, %3\n\t"
+      "s_nop 2\n\t"
       "global_load_lds_dwordx4 %1, %2\n\t"
       "s_mov_b32 m0, %0"
       : "=&s"(save)
@@ -200,6 +204,7 @@ __device__ inline void dma4(const void* sbase, uint32_t voff, uint32_t lds) {
   asm volatile(
       "s_mov_b32 %0, m0\n\t"
       "s_mov_b32 m0, %3\n\t"
+      "s_nop 2\n\t"
       "global_load_lds_dword %1, %2\n\t"
       "s_mov_b32 m0, %0"
       : "=&s"(save)

@@ -85,7 +85,8 @@ __device__ inline int opaque(int x) {
   return x;
 }
 
-// 16 bytes per lane from base + voff into LDS at lds + 16 * lane; zeros where voff is kOutside.
+// 16 bytes per lane from base + voff into LDS at lds + 16 * lane; zeros where voff is kOutside.  (The wait states
+// after the writes of M0 and of the descriptor as in dma16.)
 __device__ inline void buf_dma16(const void* base, uint32_t voff, uint32_t lds) {
   const uint64_t b = (uint64_t)(uintptr_t)base;
   const v4i rs = {__builtin_amdgcn_readfirstlane((int)(uint32_t)b),
@@ -94,6 +95,7 @@ __device__ inline void buf_dma16(const void* base, uint32_t voff, uint32_t lds) 
   asm volatile(
       "s_mov_b32 %0, m0\n\t"
       "s_mov_b32 m0, %3\n\t"
+      "s_nop 2\n\t"
       "buffer_load_dwordx4 %1, %2, 0 offen lds\n\t"
       "s_mov_b32 m0, %0"
       : "=&s"(save)
