@@ -146,6 +146,22 @@ struct BfArgs {
 
 namespace {
 
+// Stages of a sum (0 to 2^31 - 1: rounded up in 32 bits without a sign).
+__host__ __device__ constexpr int stages_of(int sum) { return (int)(((uint32_t)sum + BK - 1) / BK); }
+
+// Part z of `splits` of the sum over a segment's rows, in whole stages.
+struct Part {
+  int first, rows;
+};
+__host__ __device__ constexpr Part part_of(int rows, int splits, int z) {
+  const uint32_t per = (uint32_t)((stages_of(rows) + splits - 1) / splits) * BK;     // (2^31 at most)
+  const int64_t first = (int64_t)per * z < rows ? (int64_t)per * z : rows;
+  return {(int)first, (int)(rows - first < per ? rows - first : per)};
+}
+static_assert(part_of(INT32_MAX, 1, 0).rows == INT32_MAX && stages_of(INT32_MAX) == 1 << 25, "the longest sum");
+static_assert(part_of(INT32_MAX, 32, 31).first + part_of(INT32_MAX, 32, 31).rows == INT32_MAX, "its last part");
+static_assert(part_of(0, 32, 5).rows == 0 && part_of(65, 3, 1).rows == 1 && part_of(65, 3, 2).rows == 0, "short sums");
+
 // (equal in every lane: kept in a scalar register)
 __device__ inline int same(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ inline int64_t same(int64_t v) {
@@ -228,12 +244,10 @@ __device__ inline bool find_tile(const BfArgs& A, int t, Tile& tile) {
   tile.n0 = nt * (F == kGated ? BN / 2 : BN);
   tile.n_here = (int)A.n_cols - tile.n0;
   if constexpr (F == kDw) {
-    // part z of the sum over the segment's rows
-    const int per = ((seg.rows + BK - 1) / BK + A.splits - 1) / A.splits * BK;
-    const int first = (int64_t)per * z < seg.rows ? per * z : seg.rows;
-    tile.sum = seg.rows - first < per ? seg.rows - first : per;
+    const Part part = part_of(seg.rows, A.splits, z);
+    tile.sum = part.rows;
     tile.m_here = (int)A.m_cols - tile.m0;
-    tile.p_row = tile.q_row = seg.first + first;
+    tile.p_row = tile.q_row = seg.first + part.first;
     tile.out_row = ((int64_t)z * A.G + g) * A.m_cols + tile.m0;
   } else {
     tile.sum = (int)A.sum;
@@ -290,7 +304,7 @@ __device__ __forceinline__ void run_tiles(const BfArgs& A, uint8_t* smem, Source
       return ((in >> 1) ^ col_key<W>(c_row(W, piece))) * 16 + (in & 1) * 8;
     };
     sum = t.sum;
-    nk = (sum + BK - 1) / BK;
+    nk = stages_of(sum);
     P = A.p + t.p_row * A.ldp + (p_is_col(F) ? t.m0 : 0);
     Q = A.q + t.q_row * A.ldq + (q_is_col(F) ? t.n0 : 0);
     // (gated: the second half of the waves loads the up rows, n_cols rows further)
