@@ -679,6 +679,7 @@ fgg_status fgg_grouped_linear_backward_input(int32_t G, int64_t M, int64_t N, in
 
 fgg_status fgg_grouped_linear_backward_weight_workspace(int32_t G, int64_t M, int64_t N, int64_t K, size_t* bytes) {
   if (!bytes || G < 1 || G > 1024 || M < 0 || N < 0 || K < 0) return FGG_ERR_INVALID_VALUE;
+  if (N > fgg::kMaxBf16Width || K > fgg::kMaxBf16Width || M > (int64_t)INT32_MAX) return FGG_ERR_UNSUPPORTED;
   *bytes = fgg::gemm_bf16_dw_workspace(G, M, N, K);
   return FGG_OK;
 }

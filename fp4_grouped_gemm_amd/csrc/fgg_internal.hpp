@@ -161,10 +161,11 @@ struct Segments {
   int64_t M;
   int num_cus;
 };
-// Workgroups of a launch at most (the rows' forms; the weights' gradient).
+// Tiles of the largest shape (the rows' forms; the weights' gradient), of which a call has at most kMaxBf16Tiles: 64
+// segments' tiles stay below 2^31.  A smaller shape is taken where its tiles are a grid: kMaxBf16Grid workgroups.
 int64_t gemm_bf16_tiles(const int32_t* offsets, int32_t G, int64_t M, int64_t cols, bool gated);
 int64_t gemm_bf16_dw_tiles(int32_t G, int64_t N, int64_t K);
-constexpr int64_t kMaxBf16Tiles = 0xFFFFFFFFll / 512 - 256;
+constexpr int64_t kMaxBf16Tiles = (int64_t(1) << 25) - 1, kMaxBf16Grid = 0xFFFFFFFFll / 512 - 256;
 // Row strides and widths at most: 256 rows of them stay below 2^31 bytes.
 constexpr int64_t kMaxBf16Width = (int64_t(1) << 22) - 8;
 

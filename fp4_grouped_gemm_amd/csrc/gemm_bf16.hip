@@ -179,16 +179,26 @@ __device__ inline int slot_of(const Tile& t, int i) {
   return i == 0 ? t.slot[0] : i == 1 ? t.slot[1] : i == 2 ? t.slot[2] : t.slot[3];
 }
 
-// Tiles of the whole launch.
+// Tiles of height BM that a segment takes (0 to 2^31 - 1 rows: rounded up without a sign).
+template <int BM>
+__device__ inline int tiles_down(int rows) {
+  return (int)(((uint32_t)rows + BM - 1) / BM);
+}
+
+// Tiles of the whole launch (kMaxBf16Tiles at most, also where offsets fall and segments overlap).
 template <int F, class S>
 __device__ inline int count_tiles(const BfArgs& A) {
   if (F == kDw) return A.splits * A.G * A.m_tiles * A.n_tiles;
-  if (A.offsets == nullptr) return (int)((A.M + S::M - 1) / S::M) * A.n_tiles;
-  const int lane = threadIdx.x & 63;
+  if (A.offsets == nullptr) return tiles_down<S::M>((int)A.M) * A.n_tiles;
+  const int lane = threadIdx.x & 63, most = (int)(kMaxBf16Tiles / A.n_tiles);
   int n = 0;
-  for (int g = lane; g < A.G; g += 64) n += (segment_of(A.offsets, A.counts, g, A.M).rows + S::M - 1) / S::M;
+  for (int g = lane; g < A.G; g += 64) {
+    n += tiles_down<S::M>(segment_of(A.offsets, A.counts, g, A.M).rows);
+    if (n > most) n = most;
+  }
   for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d);
-  return same(n) * A.n_tiles;
+  n = same(n);
+  return (n < most ? n : most) * A.n_tiles;
 }
 
 // Tile t of the launch, segment by segment, in blocks 8 high; false past the last one.
@@ -208,25 +218,25 @@ __device__ inline bool find_tile(const BfArgs& A, int t, Tile& tile) {
     seg = A.offsets ? segment_of(A.offsets, A.counts, g, A.M) : Segment{0, (int)A.M};
   } else if (A.offsets == nullptr) {
     seg = {0, (int)A.M};
-    mtg = (int)((A.M + BM - 1) / BM);
+    mtg = tiles_down<BM>(seg.rows);
     if (t >= mtg * A.n_tiles) return false;
   } else {
-    int before = 0;
+    uint32_t before = 0;                 // (at most t; the 64 segments after it have less than 2^31 tiles)
     bool found = false;
     for (int g0 = 0; g0 < A.G; g0 += 64) {
       Segment mine = {0, 0};
       if (g0 + lane < A.G) mine = segment_of(A.offsets, A.counts, g0 + lane, A.M);
-      const int tiles = (mine.rows + BM - 1) / BM * A.n_tiles;
+      const int tiles = tiles_down<BM>(mine.rows) * A.n_tiles;
       int upto = tiles;
       for (int d = 1; d < 64; d <<= 1) {
         const int v = __shfl_up(upto, d);
         if (lane >= d) upto += v;
       }
-      const uint64_t hit = __ballot(before + upto > t);
+      const uint64_t hit = __ballot(before + upto > (uint32_t)t);
       if (hit) {
         const int at = __builtin_ctzll(hit);
         g = g0 + at;
-        j = t - (before + __builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(tiles, at));
+        j = t - (int)before - (__builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(tiles, at));
         seg.first = __builtin_amdgcn_readlane((int)mine.first, at);
         seg.rows = __builtin_amdgcn_readlane(mine.rows, at);
         found = true;
@@ -235,7 +245,7 @@ __device__ inline bool find_tile(const BfArgs& A, int t, Tile& tile) {
       before += __builtin_amdgcn_readlane(upto, 63);
     }
     if (!found) return false;
-    mtg = (seg.rows + BM - 1) / BM;
+    mtg = tiles_down<BM>(seg.rows);
   }
   const int mb = j / (kSM * A.n_tiles), k_in = j - mb * kSM * A.n_tiles;
   const int high = mtg - mb * kSM < kSM ? mtg - mb * kSM : kSM;
@@ -823,20 +833,24 @@ double shape_us(int shape, double tiles, double stages, bool alike) {
   return rounds * (stages * full[shape] + ends[shape]);
 }
 
+// Whether a launch of so many tiles of this shape is a grid (Large takes any number with a workgroup per compute unit).
+bool fits_grid(int shape, int64_t tiles) { return shape == 0 || tiles <= kMaxBf16Grid; }
+
 // Rows' forms: segments are taken to be alike, with half a tile of each lost at its end.
 Plan plan_rows(const Segments& s, int64_t cols, int64_t sum, bool gated) {
   constexpr int kSide[3] = {256, 128, 64};
-  Plan best = {2, 1};
+  Plan best = {0, 1};
   double least = 1e30;
   for (int i = 0; i < 3; ++i) {
+    const int64_t across = up(cols, gated ? kSide[i] / 2 : kSide[i]);
+    if (!fits_grid(i, row_tiles(s.offsets, s.G, s.M, kSide[i]) * across)) break;
     double down = (double)up(s.M, kSide[i]);
     if (s.G > 1) {
       const double live = (double)(s.G < s.M ? s.G : s.M);
       down = (double)s.M / kSide[i] + 0.5 * live;
       if (down < live) down = live;
     }
-    const double us = shape_us(i, down * (double)up(cols, gated ? kSide[i] / 2 : kSide[i]), (double)up(sum, 64),
-                               s.G == 1);
+    const double us = shape_us(i, down * (double)across, (double)up(sum, 64), s.G == 1);
     if (us < least) least = us, best.shape = i;
   }
   return best;
@@ -846,10 +860,11 @@ Plan plan_rows(const Segments& s, int64_t cols, int64_t sum, bool gated) {
 // about 4 bytes a picosecond) a second kernel adds: 30000 rows onto 1024 x 1160, 588 us in one part.
 Plan plan_dw(int32_t G, int64_t M, int64_t N, int64_t K) {
   constexpr int kSide[3] = {256, 128, 64};
-  Plan best = {2, 1};
+  Plan best = {0, 1};
   double least = 1e30;
   const double each = (double)up(up(M, G), 64);
   for (int i = 0; i < 3; ++i) {
+    if (!fits_grid(i, G * up(N, kSide[i]) * up(K, kSide[i]))) break;
     const double tiles = (double)G * (double)up(N, kSide[i]) * (double)up(K, kSide[i]);
     for (int z = 1; z <= 32; ++z) {
       const double stages = (double)(int64_t)((each + z - 1) / z);
@@ -919,10 +934,10 @@ const KernelInfo kInfoDwJoin[4] = {
 };
 
 int64_t gemm_bf16_tiles(const int32_t* offsets, int32_t G, int64_t M, int64_t cols, bool gated) {
-  return row_tiles(offsets, G, M, Small::M) * up(cols, gated ? Small::N / 2 : Small::N);
+  return row_tiles(offsets, G, M, Large::M) * up(cols, gated ? Large::N / 2 : Large::N);
 }
 
-int64_t gemm_bf16_dw_tiles(int32_t G, int64_t N, int64_t K) { return (int64_t)G * up(N, Small::M) * up(K, Small::N); }
+int64_t gemm_bf16_dw_tiles(int32_t G, int64_t N, int64_t K) { return (int64_t)G * up(N, Large::M) * up(K, Large::N); }
 
 size_t gemm_bf16_dw_workspace(int32_t G, int64_t M, int64_t N, int64_t K) {
   if (M == 0 || N == 0 || K == 0) return 0;
@@ -979,7 +994,7 @@ hipError_t launch_grouped_gated_backward(const Segments& s, int64_t I, int64_t N
 hipError_t launch_grouped_dw(const Segments& s, int64_t N, int64_t K, const uint16_t* dy, int64_t lddy,
                              const uint16_t* x, int64_t ldx, void* dw, bool dw_f32, bool accumulate, float* ws,
                              hipStream_t st) {
-  const Plan p = s.M == 0 ? Plan{2, 1} : plan_dw(s.G, s.M, N, K);
+  const Plan p = plan_dw(s.G, s.M, N, K);
   BfArgs a{};
   a.p = dy, a.ldp = lddy, a.q = x, a.ldq = ldx;
   a.offsets = s.offsets, a.counts = s.counts, a.G = s.G, a.M = s.M, a.num_cus = s.num_cus;

@@ -567,8 +567,9 @@ fgg_status fgg_moe_gemv_fp4(int32_t G, int64_t T, int32_t k, int64_t N, int64_t 
  * dense, w [G][N][K] (gated: [G][2I][K], w_down [G][N][I]); dw is dense [G][N][K].  Rows may be strided
  * (ld >= the row's width).  Base pointers are 16-byte aligned and strides whole 16-byte pieces.
  * N, K (and I) are multiples of 8 from 8 to 2^22 - 8, strides at most that, 1 <= G <= 1024,
- * M < 2^31 (FGG_ERR_UNSUPPORTED beyond).  M == 0 is a no-op, except that backward_weight
- * writes zeros.  Outputs must not overlap inputs.  Results do not depend on an order of arrival:
+ * M < 2^31, and a call has fewer than 2^25 tiles of 256 x 256 outputs (gated: 256 x 128 of a), where each segment
+ * may have one more than its rows fill (FGG_ERR_UNSUPPORTED beyond).  M == 0 is a no-op, except that
+ * backward_weight writes zeros.  Outputs must not overlap inputs.  Results do not depend on an order of arrival:
  * the same call gives the same bits.
  * workspace: fgg_grouped_linear_backward_weight_workspace bytes, 16-byte aligned (0: may be NULL);
  * contents need not be kept or cleared, and calls that may overlap in time need one each.
