@@ -601,8 +601,8 @@ fgg_status fgg_grouped_gated_backward(int32_t G, int64_t M, int64_t I, int64_t N
  * factors for every row, here each token brings its own; tokens of one adapter need not be
  * neighbours (they cost least when they are).  No token's result depends on another adapter's or
  * token's contents.  Sums run in fp32, the inner sums enter the outer product to 2^-17 (out bf16)
- * or 2^-24 (out fp32) of their value, and the result is rounded once.  The same call gives the
- * same bits.
+ * or 2^-24 (out fp32) of their value, and the result is rounded once.  Infinite factors give the infinities
+ * (or NaN) of the formula.  The same call gives the same bits.
  * x: bf16 [T][ldx], ids: [T] int32, a: bf16 [L][r][K], b: bf16 [L][N][r], scales: fp32 [L] or NULL (1);
  * base, out: [T][ldb], [T][ldo] of dtype (FGG_BF16 or FGG_F32); out may be base itself (same pointer
  * and stride), else it must not overlap an input.  Base pointers are 16-byte aligned and row strides
