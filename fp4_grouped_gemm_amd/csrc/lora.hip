@@ -31,6 +31,7 @@ constexpr int kWaves = 8, kThreads = 64 * kWaves;
 constexpr int kFewWaves = 16, kFewThreads = 64 * kFewWaves;
 constexpr int kSpan = 128;               // of the sum over K per item
 constexpr int kCols = 32;                // columns per item of the second product
+constexpr float kMaxBf16 = 0x1.FEp127f;
 
 __device__ inline v8bf load_or_zero(const uint16_t* p, bool on) {
   uint4 u = make_uint4(0, 0, 0, 0);
@@ -363,7 +364,11 @@ lora_expand_kernel(const float* __restrict__ part, int chunks, const int32_t* __
     for (int e = 0; e < 4; ++e) v[e] = on ? v[e] * scale : 0.0f;
 #pragma unroll
     for (int p = 0; p < kParts; ++p) {
-      uint32_t w[2] = {bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
+      float c[4];                        // (a finite sum past the largest bf16 value stays finite)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        c[e] = fabsf(v[e]) < INFINITY ? __builtin_amdgcn_fmed3f(v[e], -kMaxBf16, kMaxBf16) : v[e];
+      const uint32_t w[2] = {bf16x2_rne(c[0], c[1]), bf16x2_rne(c[2], c[3])};
       *reinterpret_cast<uint2*>(&vs[p][t][j]) = make_uint2(w[0], w[1]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {      // (an infinite or NaN part carries the whole)

@@ -60,3 +60,19 @@ def test_infinite_rows_of_x_and_a(T, r, N, K, two, dtype):
     up[3], down[T - 1] = True, True
     assert (got[up] == INF).all() and (got[down] == -INF).all()
     assert torch.equal(got[~up & ~down], clean[~up & ~down])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,r,N,K,two", FORMS)
+def test_sums_past_the_largest_bf16_value(T, r, N, K, two, dtype):
+    """Inner sums between the largest bf16 value and the largest fp32 value, scaled down by b: exact in 24 bits."""
+    base, x, ids, a, b, _ = form(T, r, N, K, two, dtype, "runs", 6)
+    top = 255 * 2.0 ** 120
+    x[:], a[:], b[:], base[:] = 0, 0, 0, 0
+    x[3, 0], x[3, 1] = top, 2.0 ** 119                   # the sum: top + 3/4 of the step that 2^127 has in bf16
+    a[:, 0, 0], a[:, 0, 1] = 1, 1.5
+    b[:, :, 0] = 2.0 ** -127
+    got = fgg.lora_add(base, x, ids, a, b).double()
+    want = (top + 1.5 * 2.0 ** 119) * 2.0 ** -127
+    assert (got[3] == torch.tensor(want, dtype=torch.float64).to(dtype).double().item()).all()
+    assert (got[:3] == 0).all() and (got[4:] == 0).all()
