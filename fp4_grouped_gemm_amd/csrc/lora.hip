@@ -438,7 +438,8 @@ lora_few_kernel(const uint16_t* __restrict__ x, int64_t ldx, const int32_t* __re
   __shared__ float red[kFewWaves][8 * RG];
   __shared__ float vs[8 * RG];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t = blockIdx.y, n = (int64_t)blockIdx.x * kFewThreads + threadIdx.x;
+  const int64_t t = blockIdx.y;
+  const int n = (int)blockIdx.x * kFewThreads + threadIdx.x;       // (N is at most 2^20)
   const int id = ids[t];
   const bool has = id >= 0 && id < L;
   if (!has && out == base) return;
@@ -448,8 +449,9 @@ lora_few_kernel(const uint16_t* __restrict__ x, int64_t ldx, const int32_t* __re
     float acc[RG];
 #pragma unroll
     for (int g = 0; g < RG; ++g) acc[g] = 0.0f;
-    const uint16_t* xl = x + t * ldx + 8 * (lane & 7);
-    const uint16_t* al = a + ((int64_t)id * r + (lane >> 3)) * K + 8 * (lane & 7);
+    // (row addresses in scalar registers, and a lane's 32-bit offset in bytes: 64-bit addresses of 128 ranks spill)
+    const uint16_t *xt = x + t * ldx, *at = a + (int64_t)id * r * K;
+    const uint32_t row = (uint32_t)(lane >> 3) * (uint32_t)(K * 2);
     // kU pieces' loads fly together; ALL: all of them lie inside the sum (else what is past it is zero)
     constexpr int kU = RG <= 2 ? 4 : RG == 4 ? 3 : RG == 8 ? 2 : 1;
     auto take = [&](auto all_tag, int64_t p) {
@@ -459,12 +461,13 @@ lora_few_kernel(const uint16_t* __restrict__ x, int64_t ldx, const int32_t* __re
       bool on[kU];
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        int64_t k = (p + u * kFewWaves) * 64;
-        on[u] = ALL || k + 8 * (lane & 7) < K;
-        if (!on[u]) k = -8 * (lane & 7);
-        xw[u] = *reinterpret_cast<const uint4*>(xl + k);
+        uint32_t k = (uint32_t)(p + u * kFewWaves) * 64 + 8 * (lane & 7);
+        on[u] = ALL || k < K;
+        k = on[u] ? 2 * k : 0;
+        xw[u] = *reinterpret_cast<const uint4*>((const char*)xt + k);
 #pragma unroll
-        for (int g = 0; g < RG; ++g) aw[u][g] = *reinterpret_cast<const uint4*>(al + (8 * g < r ? 8 * g : 0) * K + k);
+        for (int g = 0; g < RG; ++g)
+          aw[u][g] = *reinterpret_cast<const uint4*>((const char*)(at + (8 * g < r ? 8 * g : 0) * K) + (row + k));
       }
       __builtin_amdgcn_sched_barrier(0);
       if (!ALL) {
