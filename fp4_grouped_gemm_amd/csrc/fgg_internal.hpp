@@ -185,7 +185,8 @@ hipError_t launch_grouped_gated_backward(const Segments& s, int64_t I, int64_t N
                                          const uint16_t* w_down, const uint16_t* h, int64_t ldh, uint16_t* dh,
                                          int64_t lddh, uint16_t* act, int64_t lda, hipStream_t st);
 
-// The linear layer and the gated block for few rows per segment (gated: h nullable, out bf16).
+// The linear layer and the gated block for few rows per segment, kFewRows at most in all (gated: h nullable, out bf16).
+constexpr int64_t kFewRows = 256;
 hipError_t launch_rows_bf16(const Segments& s, bool gated, int64_t N, int64_t K, const uint16_t* x, int64_t ldx,
                             const uint16_t* w, void* out, bool out_f32, int64_t ldo, uint16_t* h, int64_t ldh,
                             hipStream_t st);

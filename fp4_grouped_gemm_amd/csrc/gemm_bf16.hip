@@ -913,11 +913,15 @@ __global__ void __launch_bounds__(256) dw_join_kernel(const float4* __restrict__
 }
 
 // Few rows take the few-row kernel where the smallest tiles would leave half the chip without one: they then wait
-// out one tile's whole sum (K 7168: 30 us; the few-row kernel shares it between eight waves: 12 us for one row
-// onto 4096 columns, 16 for 16 rows; onto 16384 columns, 256 tiles, 34 against 21 us).
+// out one tile's whole sum, which the few-row kernel shares between eight waves.  Its rows cost more the more there
+// are of a segment: 16 on average where the tiles are 128, to 32 where they are 64 and fewer.  Few-row / tiles, us, rows
+// spread evenly: one row 7168 -> 4096 12.6 / 32, 32 rows 21.7 / 32; 16 segments 2048 -> 512, 4 rows each 8.6 / 12.3,
+// 16 11.3 / 12.4, 32 15.3 / 12.5; 4 segments 4096 -> 2048, 16 rows each 19.4 / 21.0, 24 22.7 / 21.5.  How the rows are
+// spread is not known here: with all of them in one segment, passes of 64 run side by side, and 256 rows bound what
+// that costs (16 segments 2048 -> 512, 64 rows 12.0 / 11.8, 128 12.4 / 12.0, 256 21 / 12.2; 512 rows 40 / 12.3).
 bool few_rows(const Segments& s, int64_t cols, bool gated) {
-  const int64_t live = s.G < s.M ? s.G : s.M;
-  return s.M <= 32 * live && live * up(cols, gated ? Small::N / 2 : Small::N) <= 128;
+  const int64_t live = s.G < s.M ? s.G : s.M, tiles = live * up(cols, gated ? Small::N / 2 : Small::N);
+  return s.M <= kFewRows && s.M <= 32 * live && tiles <= 128 && s.M * tiles <= 2048 * live;
 }
 
 }  // namespace

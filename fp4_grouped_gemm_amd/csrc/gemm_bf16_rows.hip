@@ -5,7 +5,7 @@
 //
 // What bounds it is reading the weights once, by enough waves (one row, 7168 -> 4096: 11.9 us for 59 MB, 4.9
 // TB/s; the smallest tiles of gemm_bf16.hip, 64 of them, take 30).  A workgroup takes 16 weight rows of one
-// segment (gated: 8 gate and the 8 up rows of the same index) against all of the segment's rows: eight
+// segment (gated: 8 gate and the 8 up rows of the same index) against 64 of the segment's rows: eight
 // waves share the sum over k in pieces of 64 (a whole 128-byte line of each weight row per piece), weights go
 // from memory straight into the operands of v_mfma_f32_16x16x32_bf16 (first operand: weight rows, second: 16
 // rows of x, which come from the caches), with several pieces' loads in flight per wave.  The waves' sums
@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
 constexpr int kPiece = 64;
+constexpr int kPass = 64;                // rows that a workgroup takes at a time
 
 }  // namespace
 
@@ -33,7 +34,8 @@ rows_bf16_kernel(const uint16_t* __restrict__ x, int64_t ldx, const uint16_t* __
   const int l16 = lane & 15, q = lane >> 4;
   const int g = blockIdx.y;
   const Segment seg = offsets ? segment_of(offsets, counts, g, M) : Segment{0, (int)M};
-  if (seg.rows == 0) return;
+  const int first = kPass * blockIdx.z;
+  if (first >= seg.rows) return;
 
   // columns of the output per workgroup, and each lane's weight row (one inside the matrix
   // for columns past the edge: their sums are dropped)
@@ -133,19 +135,10 @@ rows_bf16_kernel(const uint16_t* __restrict__ x, int64_t ldx, const uint16_t* __
     }
   };
 
-  for (int r0 = 0; r0 < seg.rows;) {
-    const int left = seg.rows - r0;
-    if (left <= 16) {
-      body(std::integral_constant<int, 1>{}, r0);
-      r0 += 16;
-    } else if (left <= 32) {
-      body(std::integral_constant<int, 2>{}, r0);
-      r0 += 32;
-    } else {
-      body(std::integral_constant<int, 4>{}, r0);
-      r0 += 64;
-    }
-  }
+  const int here = seg.rows - first;
+  if (here <= 16) body(std::integral_constant<int, 1>{}, first);
+  else if (here <= 32) body(std::integral_constant<int, 2>{}, first);
+  else body(std::integral_constant<int, kPass / 16>{}, first);
 }
 
 #define FGG_ROWS_INFO(gated, name, entry) \
@@ -159,7 +152,8 @@ hipError_t launch_rows_bf16(const Segments& s, bool gated, int64_t N, int64_t K,
                             const uint16_t* w, void* out, bool out_f32, int64_t ldo, uint16_t* h, int64_t ldh,
                             hipStream_t st) {
   const int cols = gated ? 8 : 16;
-  const dim3 grid((unsigned)((N + cols - 1) / cols), (unsigned)s.G);
+  // (a segment may have all the rows: a workgroup for each pass, which ends at once where the segment has fewer)
+  const dim3 grid((unsigned)((N + cols - 1) / cols), (unsigned)s.G, (unsigned)((s.M + kPass - 1) / kPass));
   trace_launch(kInfoRowsBf16[gated ? 1 : 0], grid, "G=%d M=%lld columns=%lld sum=%lld%s", s.G, (long long)s.M,
                (long long)N, (long long)K, s.counts ? " counts" : "");
   auto go = [&](auto* kernel) {
