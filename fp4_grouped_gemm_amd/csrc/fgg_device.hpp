@@ -198,6 +198,47 @@ __device__ inline void dma16(const void* sbase, uint32_t voff, uint32_t lds) {
       : "memory");
 }
 
+// N of them, from sbase[i] + voff[i] into LDS at lds + 1024 * i + 16 * lane, with M0 saved and set up once.
+template <int N>
+__device__ inline void dma16_run(const void* const* sbase, const uint32_t* voff, uint32_t lds) {
+  static_assert(N == 2 || N == 4 || N == 7, "loads of one asm");
+  uint32_t save;
+#define FGG_FIRST(v, s) "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 2\n\tglobal_load_lds_dwordx4 " v ", " s "\n\t"
+#define FGG_NEXT(v, s) "s_addk_i32 m0, 0x400\n\ts_nop 0\n\tglobal_load_lds_dwordx4 " v ", " s "\n\t"
+#define FGG_LAST "s_mov_b32 m0, %0"
+  if constexpr (N == 2)
+    asm volatile(FGG_FIRST("%2", "%4") FGG_NEXT("%3", "%5") FGG_LAST
+                 : "=&s"(save)
+                 : "s"(lds), "v"(voff[0]), "v"(voff[1]), "s"(sbase[0]), "s"(sbase[1])
+                 : "memory", "scc");
+  else if constexpr (N == 4)
+    asm volatile(FGG_FIRST("%2", "%6") FGG_NEXT("%3", "%7") FGG_NEXT("%4", "%8") FGG_NEXT("%5", "%9") FGG_LAST
+                 : "=&s"(save)
+                 : "s"(lds), "v"(voff[0]), "v"(voff[1]), "v"(voff[2]), "v"(voff[3]), "s"(sbase[0]), "s"(sbase[1]),
+                   "s"(sbase[2]), "s"(sbase[3])
+                 : "memory", "scc");
+  else
+    asm volatile(FGG_FIRST("%2", "%9") FGG_NEXT("%3", "%10") FGG_NEXT("%4", "%11") FGG_NEXT("%5", "%12")
+                     FGG_NEXT("%6", "%13") FGG_NEXT("%7", "%14") FGG_NEXT("%8", "%15") FGG_LAST
+                 : "=&s"(save)
+                 : "s"(lds), "v"(voff[0]), "v"(voff[1]), "v"(voff[2]), "v"(voff[3]), "v"(voff[4]), "v"(voff[5]),
+                   "v"(voff[6]), "s"(sbase[0]), "s"(sbase[1]), "s"(sbase[2]), "s"(sbase[3]), "s"(sbase[4]),
+                   "s"(sbase[5]), "s"(sbase[6])
+                 : "memory", "scc");
+#undef FGG_FIRST
+#undef FGG_NEXT
+#undef FGG_LAST
+}
+
+// The same with one base.
+template <int N>
+__device__ inline void dma16_run(const void* sbase, const uint32_t* voff, uint32_t lds) {
+  const void* all[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) all[i] = sbase;
+  dma16_run<N>((const void* const*)all, voff, lds);
+}
+
 // 4 bytes per lane from sbase + voff into LDS at m0 + 4 * lane.
 __device__ inline void dma4(const void* sbase, uint32_t voff, uint32_t lds) {
   uint32_t save;

@@ -327,12 +327,8 @@ gemm_fp8_contig_kernel(int G, int64_t M, int64_t N, int64_t K, const uint8_t* __
   auto issue = [&](int kb, int stage) {
     const uint8_t* a_src = Atile + (int64_t)kb * BK;
     const uint8_t* b_src = Btile + (int64_t)kb * BK;
-#pragma unroll
-    for (int i = 0; i < kADma; ++i)
-      dma16(a_src, offA[i], lds_base + kAOff + stage * kABytes + (wave * kADma + i) * 1024);
-#pragma unroll
-    for (int i = 0; i < kBDma; ++i)
-      dma16(b_src, offB[i], lds_base + kBOff + stage * kBBytes + (wave * kBDma + i) * 1024);
+    dma16_run<kADma>(a_src, offA, lds_base + kAOff + stage * kABytes + wave * kADma * 1024);
+    dma16_run<kBDma>(b_src, offB, lds_base + kBOff + stage * kBBytes + wave * kBDma * 1024);
     // kSRows scales per wave: the first kSRows lanes only (still one DMA instruction per wave)
     const float* s_src = SAt + (int64_t)kb * M;
     if (lane < kSRows) dma4(s_src, offS, lds_base + kSOff + stage * kSBytes + wave * kSRows * 4);
@@ -754,10 +750,8 @@ gemm_fp8_dense_kernel(int64_t M, int64_t N, int64_t K, const uint8_t* __restrict
       const uint8_t* a_src = Atile + (int64_t)kb * BK;
       const uint8_t* b_src = Btile + (int64_t)kb * BK;
       const uint32_t base = lds_base + stage * kStageBytes;
-#pragma unroll
-      for (int i = 0; i < kADma; ++i) dma16(a_src, offA[i], base + (wave * kADma + i) * 1024);
-#pragma unroll
-      for (int i = 0; i < kBDma; ++i) dma16(b_src, offB[i], base + kABytes + (wave * kBDma + i) * 1024);
+      dma16_run<kADma>(a_src, offA, base + wave * kADma * 1024);
+      dma16_run<kBDma>(b_src, offB, base + kABytes + wave * kBDma * 1024);
       const float* s_src = SA + (int64_t)kb * M + m0;
       if (lane < 32) dma4(s_src, offS, base + kABytes + kBBytes + wave * 128);
     };

@@ -128,11 +128,10 @@ gemm_mxfp4_kernel(int64_t M, int64_t N, int64_t K, const uint8_t* __restrict__ A
     const uint32_t sbase = lds_base + stage * kStageBytes;
     const uint8_t* asrc = Abase + (int64_t)kb * kRowBytes;
     const uint8_t* bsrc = Bbase + (int64_t)kb * kRowBytes;
-    dma16(asrc, oa0, sbase + a_seg0 * 1024);
-    dma16(asrc, oa1, sbase + (a_seg0 + 1) * 1024);
+    const uint32_t oa[2] = {oa0, oa1}, ob[2] = {ob0, ob1};
+    dma16_run<2>(asrc, oa, sbase + a_seg0 * 1024);
     if (wave < 4) {
-      dma16(bsrc, ob0, sbase + kABytes + b_seg0 * 1024);
-      dma16(bsrc, ob1, sbase + kABytes + (b_seg0 + 1) * 1024);
+      dma16_run<2>(bsrc, ob, sbase + kABytes + b_seg0 * 1024);
       if (lane < 48) dma4(SBbase + (int64_t)kb * 4, os0, sbase + kSBOff + 48 * wave * 4);
     } else {
       dma16(bsrc, ob0, sbase + kABytes + b_seg0 * 1024);

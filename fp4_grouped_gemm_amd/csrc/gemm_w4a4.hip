@@ -284,12 +284,11 @@ w4a4_gemm_kernel(int64_t M, int64_t N, int64_t K, const uint16_t* __restrict__ A
   }
   auto issue = [&](int ks, int stage) {
     if (wave >= kDmaWaves) return;
+    const void* src[kDma];
 #pragma unroll
-    for (int i = 0; i < kDma; ++i) {
-      const int seg = wave * kDma + i;               // wave-uniform
-      const uint8_t* src = (seg < kAGroups ? Abase : Bbase) + (int64_t)ks * (BK * 2);
-      dma16(src, voff[i], lds_base + stage * kStageBytes + seg * 1024);
-    }
+    for (int i = 0; i < kDma; ++i)                   // (a wave's segments: wave-uniform)
+      src[i] = (wave * kDma + i < kAGroups ? Abase : Bbase) + (int64_t)ks * (BK * 2);
+    dma16_run<kDma>((const void* const*)src, voff, lds_base + stage * kStageBytes + wave * kDma * 1024);
   };
 
   v4f acc[4][kNJ];
