@@ -9,9 +9,11 @@ namespace fgg {
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
-// 1 / (1 + e^-g) by the hardware's base-2 exponential and reciprocal: within |g| 2^-23 of the
-// value for g < 0 (the product's rounding), far inside the bf16 rounding that follows; an
-// overflowing e^-g gives 0, NaN stays NaN.
+// 1 / (1 + e^-g) by the hardware's base-2 exponential and reciprocal.  Relative error at most about (1.3 |g| + 5)
+// 2^-24 down to g = -87: g log2(e) is off by 1.3 2^-24 of itself (the constant's and the product's roundings), which
+// the exponential turns into 1.3 |g| 2^-24 of its value; exponential and reciprocal add an ulp (two 2^-24) each and
+// the sum its rounding.  That is 2^-18.4 at |g| = 32, far inside the bf16 rounding that follows.  Below -87, where the
+// value is under 2^-126, the result is 0; NaN stays NaN.
 __device__ inline float sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896341f));
 }

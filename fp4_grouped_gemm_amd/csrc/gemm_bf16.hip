@@ -17,8 +17,8 @@
 //    one row; fp32 accumulators, rounded once.
 //  * three workgroup shapes, chosen by an estimate (plan_rows, plan_dw).  Large: 256 x 256 outputs, 64 deep,
 //    8 waves (two per SIMD) of 128 x 64, two LDS stages of 64 KB; per 64 deep a wave reads 24 KB of LDS for
-//    64 MFMAs, which is what the LDS delivers in the MFMAs' time.  8192^3: 790 us, 1.39 PFLOP/s (row x row;
-//    row x col and col x col within 3 %).  Medium: 128 x 128 by 4 waves, two workgroups per compute unit, for
+//    64 MFMAs, which is what the LDS delivers in the MFMAs' time.  8192^3: 802 us, 1.37 PFLOP/s (row x row;
+//    row x col and col x col within 4 %; the library's product 681 us).  Medium: 128 x 128 by 4 waves, two workgroups per compute unit, for
 //    tiles that would not fill the chip.  Small: 64 x 64, four stages, where time is the sum's latency or
 //    the weights' bytes (16 rows onto 16384 columns, sum 4096: 21 us, 6.4 TB/s).
 //  * stages are filled by buffer loads straight into LDS, the next one's issued before the current one is
@@ -34,7 +34,9 @@
 //    go to one XCD, whose L2 then holds what they share.
 //  * what bounds the Large shape: the matrix cores at the clock that the card holds under them, and writing:
 //    without its stores the weights' gradient of 8 x 14336 x 4096 in fp32 (1.9 GB) takes 775 us instead of
-//    1170, in every shape alike, so that the stores' 4.7 TB/s do not hide behind the products.
+//    1170 (bf16 results: 961), in every shape alike: a tile's first stages wait for the last one's stores, which share
+//    their counter.  Where segments are a few tiles high, a tile at most half full of rows is a whole turn of its
+//    compute unit though it does half the products.
 #include "fgg_device.hpp"
 #include "fgg_internal.hpp"
 #include "fgg_segments.hpp"
@@ -482,7 +484,7 @@ __device__ __forceinline__ void run_tiles(const BfArgs& A, uint8_t* smem, Source
         }
       };
       if (nk > 0) {
-        // (after the first tile the last one's stores are under way too, in no order with the loads)
+        // (after the first tile the last one's stores are in the count too: all of it is awaited)
         if (nk >= S::kStages && round == 1) wait_vmcnt<kAhead * (S::kPDma + S::kQDma)>();
         else wait_vmcnt<0>();
         block_barrier();
@@ -711,7 +713,7 @@ __global__ void __launch_bounds__(S::kThreads, 2) gemm_bf16_kernel(const BfArgs 
 // The first product of the adapters of many tokens (see lora.hip): x A^T of a tile of 64 tokens over each adapter among
 // them, of which a token takes its own: part[chunk][t][j] in fp32.  Up to four adapters lie side by side in a tile of
 // 64 columns, 2^shift of them each (8192 tokens of 64 adapters in any order, rank 16, 1024 -> 1024: 98 us, one adapter
-// a tile 148); of more than 64 ranks two workgroups take half each where the chip is not full (651 tokens of 8 runs,
+// a tile 148, with the second product 5 us faster than it is now); of more than 64 ranks two workgroups take half each where the chip is not full (651 tokens of 8 runs,
 // rank 128, 456 -> 664: 17 us, both halves in one 28).
 __global__ void __launch_bounds__(Small::kThreads, 2)
 lora_tiles_kernel(const uint16_t* __restrict__ x, int64_t ldx, const int32_t* __restrict__ ids,
@@ -817,7 +819,8 @@ hipError_t launch_shape(BfArgs a, int index, hipStream_t st) {
 // (Medium loads one stage ahead and waits for cold operands), 1.5 / 0.95 / 0.37 to 0.42 for a round of what it
 // holds (1 / 2 / 2 workgroups) when the chip is full; plus 10 / 4 / 2 to begin and end each.  E.g. linear, one
 // segment: 2048^3 50 / 25 / 32 us, 4096 x 2048 x 2048 53 / 36 / 55, 8192^3 791 / 943 / 1520, 256 x 4096 x 4096
-// 87 / 41 / 20.
+// 87 / 41 / 20.  The estimates are for 256 compute units also where the caller leaves fewer to the Large grid: the
+// parts of a sum, and with them the workspace and the result's bits, stay the same.
 struct Plan {
   int shape, splits;   // 0 Large, 1 Medium, 2 Small; parts of the sum
 };

@@ -4,9 +4,11 @@
 //
 // Few tokens: one kernel for both products (lora_few_kernel).  Else two: x A^T into fp32 sums per token (the sum over
 // K cut into chunks, a workgroup per chunk and tile of tokens; lora_shrink_kernel, for many tokens lora_tiles_kernel),
-// and the product with B on top of base (lora_expand_kernel).  What bounds them is memory: every adapter's factors
-// once, x, base and out (8192 tokens of 8 prompts, rank 64, 4096 -> 4096: 50 us for 210 MB; 16 tokens of 16 requests,
-// rank 16, 7168 -> 4096: 6 us for 5 MB).
+// and the product with B on top of base (lora_expand_kernel).  What bounds them: many tokens are near memory (every
+// adapter's factors once, x, base and out: 8192 tokens of 8 prompts, rank 64, 4096 -> 4096: 52 us for 203 MB, 3.9
+// TB/s), less the start of two launches; few are a chain of latencies, ids, A with x, then B (16 tokens of 16
+// requests, rank 16, 7168 -> 4096: 5.8 us for 4.2 MB); many in any order are the first product's passes, one for each
+// of a tile's adapters (the same 8192 tokens 206 us).
 //
 //  * tokens come in any order, in tiles of 16 to 64.  A wave finds the tile's distinct adapters by
 //    ballots over the tokens' ids; the work is cut into items of one adapter and one piece of the
@@ -546,7 +548,7 @@ struct LoraPlan {
 // Whether the one-launch kernel takes the call.  One of its workgroups fills a compute unit for about 1.5 us, the
 // time that A takes at 65 bytes a nanosecond, and 0.053 us a rank for the rows of B, of which a lane has one; the two
 // kernels take 10 to 20 us for the token counts in question (captured; the second launch and the workspace cost the
-// host 4 us more).  Measured, one / two launches: 16 tokens of 16 requests, N 4096, K 7168, r 16 6.1 / 10.1 us, K 4096,
+// host 4 us more).  Measured, one / two launches: 16 tokens of 16 requests, N 4096, K 7168, r 16 5.8 / 10.1 us, K 4096,
 // r 64 12.8 / 12.7; 256 of 32, K 4096, r 16 16.7 / 21; 256 of 2, r 64 43 / 12; 512 of 8, r 16 29 / 13; 168 of 6,
 // N 6104, K 104, r 64 25 / 17.
 bool few_tokens(int64_t T, int32_t r, int64_t N, int64_t K) {
